@@ -420,6 +420,104 @@ const char *moe_kernel_name(int kernel_id);
 int moe_timing_query(int kernel_id, long long *launches, double *total_ms);
 
 /* ---------------------------------------------------------------------------
+ * Expert products: the layer's matrix products as calls of their own, for
+ * experts whose matrices are bf16 (inference and training) or FP8 with a
+ * scale per 128 x 128 block (the FP8 weights the pages list, aimodeling.com/en
+ * page, "Reported Numbers and Ecosystem Position", in the form checkpoints
+ * with block scales have). moe_permute gives the order they work on.
+ *
+ * Sorted order: the R rows of all experts, grouped by expert; expert e owns
+ * rows offsets[e] .. offsets[e+1]-1 (device [E+1], as moe_permute writes it).
+ * offsets == NULL: one group of R rows (E must be 1). Rows at and past
+ * offsets[E] are left as they are in every output. Offsets are kept inside
+ * [0, R] whatever they hold.
+ * Row indices: an input matrix with rows != NULL gives row i of sorted order
+ * its row rows[i] / div (rows = sorted_pair, div = k reads a pair's token);
+ * without, row i. An output with rows != NULL takes row i at its row rows[i]
+ * (rows = sorted_pair writes pair order), which must be distinct. *_n is the
+ * number of rows the matrix has; a row whose index is outside it is skipped:
+ * its output row is left as it is, and it adds nothing to dw.
+ * Matrices [N][K] row-major, one per expert: either w_* = [E][N][K]
+ * contiguous (and w_scale [E][ceil(N/128)][ceil(K/128)]), or experts = device
+ * array [E] of moe_expert_w with mat = MOE_MAT_W13 (w13, s13) or MOE_MAT_W2
+ * (w2, s2), for matrices that live in an expert cache or in blobs; exactly one
+ * of the two is given. Matrices and rows start 16-byte aligned.
+ * Sums are fp32. Results do not depend on timing: the same call gives the same
+ * bits. All sizes 1 <= E <= 512; R = 0 does nothing (dw writes its zeros).
+ * Neither these calls nor the ones after them need a workspace. */
+enum { MOE_MAT_W13 = 0, MOE_MAT_W2 = 1 };
+
+/* moe_grouped_gemm -- y[i] = W_e x[i] for every row i of sorted order and its
+ * expert e: x [x_n][K] bf16, y [y_n][N] bf16 (y_is_fp32 = 0, rounded once) or
+ * fp32. N and K multiples of 8. */
+int moe_grouped_gemm(const uint16_t *x_bf16, const int32_t *x_rows, int x_div, int x_n,
+                     const int32_t *offsets, const uint16_t *w_bf16, const moe_expert_w *experts,
+                     int mat, int R, int N, int K, int E, void *y, const int32_t *y_rows, int y_n,
+                     int y_is_fp32, void *stream);
+
+/* moe_grouped_gemm_dx -- the product's gradient by its rows: dx[i] = W_e^T
+ * dy[i]; dy [dy_n][N] bf16, dx [dx_n][K] bf16 or fp32. (Tokens read by several
+ * pairs: write dx in pair order and add the pairs of a token with moe_combine
+ * and weights 1.) N and K multiples of 8. */
+int moe_grouped_gemm_dx(const uint16_t *dy_bf16, const int32_t *dy_rows, int dy_div, int dy_n,
+                        const int32_t *offsets, const uint16_t *w_bf16,
+                        const moe_expert_w *experts, int mat, int R, int N, int K, int E, void *dx,
+                        const int32_t *dx_rows, int dx_n, int dx_is_fp32, void *stream);
+
+/* moe_grouped_gemm_dw -- the product's gradient by its matrices: dw_e = sum
+ * over the expert's rows i of dy[i] x[i]^T; dy [dy_n][N], x [x_n][K] bf16, dw
+ * [E][N][K] fp32 or bf16, zero for an expert without rows. accumulate != 0
+ * (fp32 only) adds to what dw holds. N and K multiples of 8. */
+int moe_grouped_gemm_dw(const uint16_t *dy_bf16, const int32_t *dy_rows, int dy_div, int dy_n,
+                        const uint16_t *x_bf16, const int32_t *x_rows, int x_div, int x_n,
+                        const int32_t *offsets, int R, int N, int K, int E, void *dw,
+                        int dw_is_fp32, int accumulate, void *stream);
+
+/* moe_grouped_gemm_fp8 -- moe_grouped_gemm from block-scaled FP8:
+ *   y[i][n] = sum_b x_scale[i][b] w_scale[e][n/128][b]
+ *             sum_{k in 128 b .. 128 b + 127} x[i][k] w_e[n][k]
+ * over E4M3 codes x [x_n][K] with fp32 scales [x_n][ceil(K/128)] (moe_quant_fp8
+ * makes them) and matrices with fp32 scales as above (moe_expert_w's s13 / s2
+ * point at them). Both indices of x (codes and scales) go through x_rows. N a
+ * multiple of 8, K of 16. */
+int moe_grouped_gemm_fp8(const uint8_t *x_e4m3, const float *x_scale, const int32_t *x_rows,
+                         int x_div, int x_n, const int32_t *offsets, const uint8_t *w_e4m3,
+                         const float *w_scale, const moe_expert_w *experts, int mat, int R, int N,
+                         int K, int E, void *y, const int32_t *y_rows, int y_n, int y_is_fp32,
+                         void *stream);
+
+/* moe_swiglu -- a[r] = w_r silu(g) u of rows h[r] = [g (I) | u (I)], bf16 in
+ * and out, fp32 between. w (optional, fp32 [w_n]): the row's weight, w[r] or
+ * w[w_rows[r]] (w = topk_w, w_rows = sorted_pair puts the router's weights
+ * here, so that the combine adds rows with weight 1); a row whose index is
+ * outside w is skipped. n_rows (optional, device): only rows below *n_rows
+ * (e.g. offsets + E); the others are left as they are. I a multiple of 8. */
+int moe_swiglu(const uint16_t *h_bf16, const float *w, const int32_t *w_rows, int w_n,
+               const int32_t *n_rows, int R, int I, uint16_t *a_bf16, void *stream);
+
+/* moe_swiglu_grad -- gradients of moe_swiglu for da = dL/da [R][I] bf16:
+ * dh [R][2I] bf16, and with w: dw (optional, fp32 [w_n], at the row's index;
+ * indices must be distinct) = sum_i da_i silu(g_i) u_i. a_bf16 (optional)
+ * receives moe_swiglu's result again. */
+int moe_swiglu_grad(const uint16_t *h_bf16, const uint16_t *da_bf16, const float *w,
+                    const int32_t *w_rows, int w_n, const int32_t *n_rows, int R, int I,
+                    uint16_t *dh_bf16, float *dw, uint16_t *a_bf16, void *stream);
+
+/* moe_quant_fp8 -- rows x [R][K] bf16 as E4M3 codes [R][K] and fp32 scales
+ * [R][ceil(K/128)]: scale = max(amax, 2^-100) / 448 with amax the largest
+ * magnitude of the row's 128 columns, code = x / scale to the nearest E4M3
+ * (ties to even). An infinity or NaN makes its block's scale and codes NaN.
+ * n_rows as in moe_swiglu. K a multiple of 8. */
+int moe_quant_fp8(const uint16_t *x_bf16, const int32_t *n_rows, int R, int K, uint8_t *q_e4m3,
+                  float *scale, void *stream);
+
+/* moe_swiglu_quant_fp8 -- moe_quant_fp8 of the fp32 values silu(g) u of rows
+ * h [R][2I] (not rounded to bf16 in between): codes [R][I], scales
+ * [R][ceil(I/128)]. */
+int moe_swiglu_quant_fp8(const uint16_t *h_bf16, const int32_t *n_rows, int R, int I,
+                         uint8_t *q_e4m3, float *scale, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Measurement helpers (not part of the layer): the references the layer's
  * kernels are compared with in a benchmark.
  *

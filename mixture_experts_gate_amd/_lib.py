@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(_PKG, "libmoe.so")
 
 MOE_OK, MOE_EINVAL, MOE_ENOMEM, MOE_EHIP, MOE_EUNSUPPORTED, MOE_EBUSY = 0, -1, -2, -3, -4, -5
 MOE_W_BF16, MOE_W_MXFP4, MOE_W_NVFP4, MOE_W_FP8 = 0, 1, 2, 3
+MOE_MAT_W13, MOE_MAT_W2 = 0, 1
 MOE_OPT_FFN_PATH = 1
 MOE_OPT_TIMING = 2
 MOE_OPT_DEC_SPLIT = 3
@@ -33,7 +34,9 @@ EXPORTS = [
     "expert_cache_slots", "expert_cache_slot_of", "expert_cache_destroy", "expert_cache_resize",
     "moe_micro_read", "moe_micro_mfma", "expert_cache_bandwidth", "expert_cache_prefetch_qstar",
     "moe_permute_split", "moe_cpu_expert_ffn", "moe_scatter_rows", "moe_permute_ffn_combine",
-    "moe_layer_fused",
+    "moe_layer_fused", "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw",
+    "moe_grouped_gemm_fp8", "moe_swiglu", "moe_swiglu_grad", "moe_quant_fp8",
+    "moe_swiglu_quant_fp8",
 ]
 
 
@@ -102,6 +105,14 @@ def load(path: str | None = None):
         "moe_permute_split": (I, [P, P, I, P, P, P, P, C.POINTER(I)]),
         "moe_cpu_expert_ffn": (I, [I, P, P, P, P, I, I, P, I, P, I]),
         "moe_scatter_rows": (I, [P, P, I, Z, P, P]),
+        "moe_grouped_gemm": (I, [P, P, I, I, P, P, P, I, I, I, I, I, P, P, I, I, P]),
+        "moe_grouped_gemm_dx": (I, [P, P, I, I, P, P, P, I, I, I, I, I, P, P, I, I, P]),
+        "moe_grouped_gemm_dw": (I, [P, P, I, I, P, P, I, I, P, I, I, I, I, P, I, I, P]),
+        "moe_grouped_gemm_fp8": (I, [P, P, P, I, I, P, P, P, P, I, I, I, I, I, P, P, I, I, P]),
+        "moe_swiglu": (I, [P, P, P, I, P, I, I, P, P]),
+        "moe_swiglu_grad": (I, [P, P, P, P, I, P, I, I, P, P, P, P]),
+        "moe_quant_fp8": (I, [P, P, I, I, P, P, P]),
+        "moe_swiglu_quant_fp8": (I, [P, P, I, I, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)

@@ -209,3 +209,66 @@ def test_cache_reserve_argument_errors(lib):
     assert L.expert_cache_destroy(None) == lib.MOE_EINVAL
     assert L.expert_cache_slots(None) == lib.MOE_EINVAL
     assert L.expert_cache_resize(None, 0x1000, 1 << 20, None, None) == lib.MOE_EINVAL
+
+
+def test_products_reject_bad_arguments(lib):
+    """The expert products and their companions: sizes, null pointers,
+    alignment, contradictory matrices (before any device work)."""
+    L, d, bad = lib.load(), 0x1000, lib.MOE_EINVAL
+
+    def gemm(fn, x=d, rows=None, div=1, n=8, off=d, w=d, tab=None, mat=0, R=8, N=16, K=16, E=2,
+             y=d, y_rows=None, y_n=8):
+        return fn(x, rows, div, n, off, w, tab, mat, R, N, K, E, y, y_rows, y_n, 0, None)
+
+    for fn in (L.moe_grouped_gemm, L.moe_grouped_gemm_dx):
+        for kw in (dict(R=-1), dict(E=0), dict(E=513), dict(N=12), dict(K=12), dict(N=0),
+                   dict(off=None), dict(w=None), dict(tab=d), dict(mat=2), dict(y=None),
+                   dict(y=d + 8), dict(x=None), dict(x=d + 2), dict(n=7), dict(rows=d, n=0),
+                   dict(rows=d, div=0), dict(y_n=7), dict(y_rows=d, y_n=0)):
+            assert gemm(fn, **kw) == bad, kw
+        assert gemm(fn, R=0, x=None, y=None) == lib.MOE_OK
+
+    def fp8(x=d, xs=d, n=8, w=d, ws=d, tab=None, K=16, N=16, y=d):
+        return L.moe_grouped_gemm_fp8(x, xs, None, 1, n, d, w, ws, tab, 0, 8, N, K, 2, y, None, 8,
+                                      0, None)
+
+    for kw in (dict(x=None), dict(xs=None), dict(ws=None), dict(w=None), dict(tab=d), dict(K=24),
+               dict(K=8), dict(N=12), dict(y=None), dict(n=3), dict(x=d + 8)):
+        assert fp8(**kw) == bad, kw
+
+    def dw(dy=d, n=8, x=d, m=8, off=d, R=8, N=16, K=16, E=2, out=d, f32=1, acc=0):
+        return L.moe_grouped_gemm_dw(dy, None, 1, n, x, None, 1, m, off, R, N, K, E, out, f32, acc,
+                                     None)
+
+    for kw in (dict(dy=None), dict(x=None), dict(n=7), dict(m=7), dict(off=None), dict(out=None),
+               dict(f32=0, acc=1), dict(N=4), dict(K=20), dict(out=d + 4), dict(E=600)):
+        assert dw(**kw) == bad, kw
+
+    def act(h=d, w=None, rows=None, wn=0, R=4, I=16, a=d):
+        return L.moe_swiglu(h, w, rows, wn, None, R, I, a, None)
+
+    for kw in (dict(h=None), dict(a=None), dict(I=12), dict(R=-1), dict(rows=d), dict(w=d, wn=3),
+               dict(w=d, rows=d, wn=0), dict(h=d + 4)):
+        assert act(**kw) == bad, kw
+    assert L.moe_swiglu_grad(d, d, None, None, 0, None, 4, 16, d, d, None, None) == bad  # dw, no w
+    assert L.moe_swiglu_grad(d, None, None, None, 0, None, 4, 16, d, None, None, None) == bad
+    assert L.moe_swiglu_grad(d, d, None, None, 0, None, 4, 16, d, None, d + 2, None) == bad
+    for fn in (L.moe_quant_fp8, L.moe_swiglu_quant_fp8):
+        assert fn(d, None, 4, 12, d, d, None) == bad
+        assert fn(None, None, 4, 16, d, d, None) == bad
+        assert fn(d, None, 4, 16, d, None, None) == bad
+        assert fn(d, None, 4, 16, d + 4, d, None) == bad
+        assert fn(d, None, 0, 16, None, None, None) == lib.MOE_OK
+
+
+def test_products_module_needs_device_tensors():
+    import torch
+    from mixture_experts_gate_amd import products as P
+    x = torch.zeros(4, 32, dtype=torch.bfloat16)
+    w = torch.zeros(2, 16, 32, dtype=torch.bfloat16)
+    for call in (lambda: P.grouped_matmul(x, w), lambda: P.grouped_matmul_dx(x, w),
+                 lambda: P.grouped_matmul_dw(x, x), lambda: P.swiglu(x), lambda: P.quant_fp8(x),
+                 lambda: P.swiglu_grad(x, x), lambda: P.swiglu_quant_fp8(x),
+                 lambda: P.grouped_matmul_fp8(x, x, w)):
+        with pytest.raises(ValueError):
+            call()
