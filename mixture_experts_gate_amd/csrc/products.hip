@@ -25,8 +25,8 @@
 // adding them to the fp32 sums is four multiply-adds.
 //
 // Rows past an expert's last one read a row that exists and are not stored;
-// columns past the end of c read zeros from a zero page (both operands, so
-// that no garbage meets a zero).
+// columns past the end of c are zeros in LDS (both operands, so that no
+// garbage meets a zero).
 #include <atomic>
 
 #include "products.hpp"
@@ -36,11 +36,13 @@ namespace moe {
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(8))) int i32x8;
 
-constexpr int kPThreads = 512;   // 8 wavefronts: 2 along p x 4 along q
-constexpr int kBQ = 256;         // q per tile
-constexpr int kMaxE = 512;
+__device__ __forceinline__ i32x8 as_i32x8(u32x4 a, u32x4 b) {
+    return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
 
-__device__ const uint32_t g_zero_page[64] = {0};
+constexpr int kPThreads = 512;   // 8 wavefronts: 2 along p x 4 along q
+constexpr int kBP = 256, kBQ = 256;   // p and q per tile
+constexpr int kMaxE = 512;
 
 // XOR key of the 16-byte chunks of an LDS row of c-major data: rows c..c+3 of
 // one transposing read (4 pieces of 8 bytes, 32 bytes apart) land in 16
@@ -50,55 +52,91 @@ __device__ __forceinline__ int t_key(int c) { return (c & 1) | ((c & 2) << 2); }
 // Index inside a 64-row block of the p or q that tile j, row r stands for.
 __device__ __forceinline__ int perm64(int j, int r) { return 16 * (r >> 2) + 4 * j + (r & 3); }
 
-template <int BP>
+// Barrier without a memory fence (a fenced one would wait for the copies in
+// flight); the compiler keeps memory accesses and matrix instructions on
+// their side of it.
+__device__ __forceinline__ void phase_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+// Tile li of mp x tq: groups of at most 8 p tiles, in a group q outer and p
+// inner, so that the 32 tiles an XCD works on at a time are about 8 x 4 of them
+// and share their rows of P and Q in its L2 (8192 x 8192 x 8192, bf16: 992 us
+// against 1045 us with p inner over all 32 p tiles, whose misses fill the
+// bandwidth behind the L2).
+__device__ __forceinline__ void place_of(int li, int mp, int tq, int &p, int &q) {
+    const int ng = (mp + 7) / 8, gp = (mp + ng - 1) / ng;
+    const int gi = li / (gp * tq), rest = li - gi * gp * tq;
+    const int gl = mp - gi * gp < gp ? mp - gi * gp : gp;
+    q = rest / gl;
+    p = gi * gp + rest - q * gl;
+}
+
+// A wavefront-uniform address kept in scalar registers: the lanes' offsets are
+// added by the load, not kept added to it in vector registers.
+__device__ __forceinline__ const char *scalar_base(const char *p) {
+    asm volatile("" : "+s"(p));
+    return p;
+}
+
+// The offset, widened where it is used and not before.
+__device__ __forceinline__ uint32_t here(uint32_t o) {
+    asm volatile("" : "+v"(o));
+    return o;
+}
+
+// This lane's index, which the compiler takes for a new value.
+__device__ __forceinline__ int fresh_lane() {
+    int l = lane_id();
+    asm volatile("" : "+v"(l));
+    return l;
+}
+
+// Waits for this wavefront's LDS accesses (lgkmcnt 0, the vector counter as it is).
+__device__ __forceinline__ void wait_lds() {
+    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));
+}
+
 struct TileLds {
-    char p[2][BP * 128];
+    char p[2][kBP * 128];
     char q[2][kBQ * 128];
-    int src[BP];          // source row of each p (forward, dx)
-    int dst[BP];          // row of out, or -1
-    float xs[2][BP];      // FP8: scales of the p rows, this step and the next
-    int rows[2][2][64];   // dw: source rows of dy and x, this step and the next
+    int src[kBP];         // source row of each LDS row of p (forward, dx)
+    int dst[kBP];         // row of out, or -1
+    float xs[4][kBP];     // FP8: scales of the p rows, by step
+    int rows[4][2][64];   // dw: source rows of dy and x, by step
     int base[kMaxE + 1];  // p tiles before each expert
     int wsum[8];
 };
 
-// One tile's place: expert, first p and q.
-struct Place {
-    int e, p0, q0;
-};
-
-template <int MODE, int BP>
+template <int MODE>
 __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
-    constexpr bool kPT = MODE == kDw, kQT = MODE == kDx || MODE == kDw;
+    constexpr bool kDwMode = MODE == kDw, kQT = MODE == kDx || MODE == kDw;
     constexpr int ES = MODE == kFwdFp8 ? 1 : 2;       // bytes of an element
     constexpr int CK = 128 / ES;                       // c per step
-    constexpr int WP = BP / 2, NP = WP / 16;           // p of a wavefront, its tiles
-    constexpr int DP = BP / 64, DQ = kBQ / 64;         // copies per thread and step
-    __shared__ TileLds<BP> L;
-    const int t = threadIdx.x, l = lane_id(), w = __builtin_amdgcn_readfirstlane(t / kWave);
-    const int wq = w & 3, wp = w >> 2, g = l >> 4, r = l & 15;
+    __shared__ TileLds L;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wq = w & 3, wp = w >> 2;
 
-    const int Pn = MODE == kDw ? A.N : 0;                        // p count (dw)
     const int Qn = MODE == kFwd || MODE == kFwdFp8 ? A.N : A.K;  // q count
     const int tq = (Qn + kBQ - 1) / kBQ;
-    const int tpw = (A.N + BP - 1) / BP;
+    const int tpw = (A.N + kBP - 1) / kBP;                        // p tiles (dw)
     const int KB = (A.K + 127) / 128;
 
     // tiles in expert order
     int total;
-    if (MODE == kDw) {
+    if (kDwMode) {
         total = A.E * tpw * tq;
     } else {
+        const int t = threadIdx.x, l = lane_id();
         int n = 0;
         if (t < A.E) {
-            int lo = 0, cnt = A.R;
-            if (A.offsets) {
-                const int b = A.offsets[t], f = A.offsets[t + 1];
-                lo = b < 0 ? 0 : b > A.R ? A.R : b;
-                const int hi = f < 0 ? 0 : f > A.R ? A.R : f;
-                cnt = hi > lo ? hi - lo : 0;
-            }
-            n = (cnt + BP - 1) / BP;
+            int lo, cnt;
+            group_of_lane(A, t, lo, cnt);
+            n = (cnt + kBP - 1) / kBP;
         }
         int incl = n;
 #pragma unroll
@@ -122,39 +160,48 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
     const int xcd = blockIdx.x % nx, per = ((int)gridDim.x - xcd + nx - 1) / nx;
     const int t0 = (int)((long)total * xcd / nx), t1 = (int)((long)total * (xcd + 1) / nx);
     for (int ti = t0 + (int)blockIdx.x / nx; ti < t1; ti += per) {
-        Place at;
-        int lo, cnt;
-        if (MODE == kDw) {
-            at.e = ti / (tpw * tq);
-            const int li = ti - at.e * tpw * tq;
-            at.p0 = (li % tpw) * BP;
-            at.q0 = (li / tpw) * kBQ;
-            group_of(A, at.e, lo, cnt);
+        // the lane is read anew for every tile, so that what is made of it is
+        // not kept in registers from tile to tile
+        const int l = fresh_lane(), t = kWave * w + l, g = l >> 4, r = l & 15;
+        // expert, first p, p rows of a wavefront row (half the tile's), first q
+        int e, p0, q0, lo, cnt, half = 128;
+        if (kDwMode) {
+            e = ti / (tpw * tq);
+            const int li = ti - e * tpw * tq;
+            place_of(li, tpw, tq, p0, q0);
+            p0 *= kBP;
+            group_of(A, e, lo, cnt);
         } else {
-            // expert e with base[e] <= m < base[e+1]; q outer, p inner
+            // expert e with base[e] <= m < base[e+1]; q outer, p inner. The
+            // expert's rows are spread evenly over its tiles, in units of 64.
             int a = 0, b = A.E;
             while (b - a > 1) {
                 const int mid = (a + b) >> 1;
                 if ((long)L.base[mid] * tq <= ti) a = mid;
                 else b = mid;
             }
-            at.e = __builtin_amdgcn_readfirstlane(a);
+            e = __builtin_amdgcn_readfirstlane(a);
             const int mp = __builtin_amdgcn_readfirstlane(L.base[a + 1] - L.base[a]);
             const int li = ti - __builtin_amdgcn_readfirstlane(L.base[a]) * tq;
-            at.p0 = (li % mp) * BP;
-            at.q0 = (li / mp) * kBQ;
-            group_of(A, at.e, lo, cnt);
+            group_of(A, e, lo, cnt);
+            half = 32 * ((cnt + 64 * mp - 1) / (64 * mp));
+            place_of(li, mp, tq, p0, q0);
+            p0 *= 2 * half;
         }
-        const int C = MODE == kDw ? cnt : MODE == kDx ? A.N : A.K;
+        q0 *= kBQ;
+        const int nc = half / 32;    // clusters of 32 rows with work
+        const int C = kDwMode ? cnt : MODE == kDx ? A.N : A.K;
         const int steps = (C + CK - 1) / CK;
 
         __syncthreads();   // the last tile's readers of L are done
-        if (MODE != kDw) {
-            if (t < BP) {
-                const int p = at.p0 + t, i = lo + (p < cnt ? p : at.p0);
+        if (!kDwMode) {
+            if (t < kBP) {
+                const int o = t & 127, p = p0 + (t >> 7) * half + o;
+                const bool in = o < half && p < cnt;
+                const int i = lo + (in ? p : 0);
                 const int s = source_row(A.a, i);
                 int d = -1;
-                if (p < cnt && s >= 0) {
+                if (in && s >= 0) {
                     d = A.out_rows ? A.out_rows[i] : i;
                     if (d < 0 || d >= A.out_n) d = -1;
                 }
@@ -162,101 +209,107 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
                 L.dst[t] = d;
             }
         } else if (t < 128) {
-            const int c = t & 63;
-            L.rows[0][t >> 6][c] = c < cnt ? source_row(t < 64 ? A.a : A.b, lo + c) : -1;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const int c = 64 * k + l;
+                L.rows[k][w][l] = c < cnt ? source_row(w == 0 ? A.a : A.b, lo + c) : -1;
+            }
         }
         __syncthreads();
 
-        // this thread's copies: 8 rows of 128 bytes (or 2 rows of 512) a
-        // wavefront and instruction
-        const char *pp[DP];
-        const char *qp[DQ];
-        const char *const mat = MODE == kDw ? nullptr : mat_of(A, at.e, ES);
-        const char *const zero = (const char *)g_zero_page;
-        const int chunk = (l & 7) ^ (l >> 3);                 // 16-byte chunk of a 128-byte row
-        const int tc = 2 * w + (l >> 5);                      // c of a c-major copy (+ 16 i)
-        const int tchunk = (l & 31) ^ t_key(tc);              // its chunk (8 columns)
+        // A copy instruction of a wavefront takes 8 rows of 128 bytes, or 2 rows
+        // of 512 (c-major). Where nothing has to be cut off, its address is a
+        // uniform base and a lane's 32-bit offset, made once per tile (fast);
+        // where c or q ends inside the copy or a is beyond 32 bits, it is
+        // made anew each time (slow), columns of c past the end becoming zeros.
+        const int prow = 128 * wp + 8 * wq;                   // LDS row of a p copy (+ 32 i)
         const size_t lda = (size_t)(MODE == kFwd || MODE == kFwdFp8 ? A.K : A.N) * ES;
         const size_t ldq = (size_t)A.K * ES;                  // rows of W, x
-        if (!kPT) {
+        const char *qb = kDwMode ? A.b.base : mat_of(A, e, ES);
+        if (!kQT) qb += (size_t)q0 * ldq;
+        const bool easy = kDwMode || (q0 + kBQ <= Qn && (size_t)A.a.n * lda <= 0xFFFFFFFFull);
+        uint32_t po[4] = {0, 0, 0, 0}, qo;
+        {
+            const int chunk = (l & 7) ^ (l >> 3);                 // 16-byte chunk of a 128-byte row
+            const int tc = 2 * w + (l >> 5);                      // c of a c-major copy (+ 16 i)
+            const int tchunk = (l & 31) ^ t_key(tc);              // its chunk (8 columns)
+            if (!kDwMode) {
 #pragma unroll
-            for (int i = 0; i < DP; ++i)
-                pp[i] = A.a.base + (size_t)L.src[64 * i + 8 * w + (l >> 3)] * lda + 16 * chunk;
-        }
-        if (!kQT) {
-#pragma unroll
-            for (int i = 0; i < DQ; ++i) {
-                const int rr = 8 * w + (l >> 3);
-                int n = at.q0 + 64 * i + perm64(rr >> 4, rr & 15);
-                n = n < Qn ? n : Qn - 1;
-                qp[i] = mat + (size_t)n * ldq + 16 * chunk;
-            }
-        } else if (MODE == kDx) {
-            int col = at.q0 + 8 * tchunk;
-            col = col < Qn ? col : 0;
-#pragma unroll
-            for (int i = 0; i < DQ; ++i)
-                qp[i] = mat + (size_t)(16 * i + tc) * ldq + (size_t)col * 2;
-        }
-        const float *ws = nullptr;
-        const float *xs = nullptr;
-        if (MODE == kFwdFp8) {
-            const int nb = (at.q0 + 64 * wq) / 128;
-            ws = scales_of(A, at.e) + (size_t)(nb < (A.N + 127) / 128 ? nb : 0) * KB;
-            if (t < BP) xs = A.a_s + (size_t)L.src[t] * KB;
-        }
-
-        // copies of step k into buffer b
-        auto fetch = [&](int k, int b) {
-            const bool tail = (k + 1) * CK > C;
-            if (!kPT) {
-                const bool in = !tail || k * CK + chunk * (16 / ES) < C;
-#pragma unroll
-                for (int i = 0; i < DP; ++i)
-                    lds_dma16(in ? pp[i] + (size_t)k * 128 : zero, L.p[b] + (64 * i + 8 * w) * 128);
+                for (int i = 0; i < 4; ++i)
+                    po[i] = (uint32_t)(L.src[prow + 32 * i + (l >> 3)] * lda) + 16 * chunk;
             } else {
-                int col = at.p0 + 8 * tchunk;
-                col = col < Pn ? col : 0;
-#pragma unroll
-                for (int i = 0; i < DQ; ++i) {
-                    const int s = L.rows[k & 1][0][16 * i + tc];
-                    lds_dma16(s >= 0 ? A.a.base + (size_t)s * lda + (size_t)col * 2 : zero,
-                              L.p[b] + (16 * i + 2 * w) * 512);
-                }
+                po[0] = 2 * (p0 + 8 * tchunk < A.N ? p0 + 8 * tchunk : 0);
             }
             if (!kQT) {
-                const bool in = !tail || k * CK + chunk * (16 / ES) < C;
-#pragma unroll
-                for (int i = 0; i < DQ; ++i)
-                    lds_dma16(in ? qp[i] + (size_t)k * 128 : zero, L.q[b] + (64 * i + 8 * w) * 128);
-            } else if (MODE == kDx) {
-#pragma unroll
-                for (int i = 0; i < DQ; ++i)
-                    lds_dma16(k * CK + 16 * i + tc < C ? qp[i] + (size_t)k * CK * ldq : zero,
-                              L.q[b] + (16 * i + 2 * w) * 512);
+                const int rr = 8 * w + (l >> 3);
+                qo = (uint32_t)(perm64(rr >> 4, rr & 15) * ldq) + 16 * chunk;
             } else {
-                int col = at.q0 + 8 * tchunk;
-                col = col < Qn ? col : 0;
-#pragma unroll
-                for (int i = 0; i < DQ; ++i) {
-                    const int s = L.rows[k & 1][1][16 * i + tc];
-                    lds_dma16(s >= 0 ? A.b.base + (size_t)s * ldq + (size_t)col * 2 : zero,
-                              L.q[b] + (16 * i + 2 * w) * 512);
-                }
+                const int col = q0 + 8 * tchunk < Qn ? q0 + 8 * tchunk : 0;
+                qo = (MODE == kDx ? (uint32_t)(tc * ldq) : 0) + 2 * col;
             }
-            if (MODE == kFwdFp8 && w < BP / kWave) lds_dma4(xs + k, &L.xs[b][64 * w]);
+        }
+        const float *ws = nullptr;
+        uint32_t xo = 0;         // this thread's row of the scales of a
+        if (MODE == kFwdFp8) {
+            const int nb = (q0 + 64 * wq) / 128;
+            ws = scales_of(A, e) + (size_t)(nb < (A.N + 127) / 128 ? nb : 0) * KB;
+            if (t < kBP) xo = (uint32_t)L.src[t];
+        }
+
+        auto copy_or_zero = [&](bool in, const char *from, char *to, int lane) {
+            if (in) lds_dma16(from, to);
+            else *(MOE_LDS u32x4 *)(to + 16 * lane) = u32x4{0, 0, 0, 0};
+        };
+        // copy i of 4 of step k, operands P and Q
+        auto copy_p = [&](int i, int k, bool fast) {
+            char *const to = L.p[k & 1] + (kDwMode ? (16 * i + 2 * w) * 512 : (prow + 32 * i) * 128);
+            if (kDwMode) {
+                const int fl = fresh_lane(), s = L.rows[k & 3][0][16 * i + 2 * w + (fl >> 5)];
+                copy_or_zero(s >= 0, A.a.base + (size_t)s * lda + po[0], to, fl);
+            } else if (fast) {
+                lds_dma16(scalar_base(A.a.base + (size_t)k * 128) + here(po[i]), to);
+            } else {
+                const int fl = fresh_lane(), chunk = (fl & 7) ^ (fl >> 3);
+                copy_or_zero(k * CK + chunk * (16 / ES) < C,
+                             A.a.base + (size_t)L.src[prow + 32 * i + (fl >> 3)] * lda +
+                                 (size_t)k * 128 + 16 * chunk, to, fl);
+            }
+        };
+        auto copy_q = [&](int i, int k, bool fast) {
+            char *const to = L.q[k & 1] + (kQT ? (16 * i + 2 * w) * 512 : (64 * i + 8 * w) * 128);
+            if (kDwMode) {
+                const int fl = fresh_lane(), s = L.rows[k & 3][1][16 * i + 2 * w + (fl >> 5)];
+                copy_or_zero(s >= 0, qb + (size_t)s * ldq + qo, to, fl);
+            } else if (MODE == kDx) {
+                const char *const from = scalar_base(qb + (size_t)(k * CK + 16 * i) * ldq) + here(qo);
+                if (fast) lds_dma16(from, to);
+                else copy_or_zero(k * CK + 16 * i + 2 * w + (fresh_lane() >> 5) < C, from, to, fresh_lane());
+            } else if (fast) {
+                lds_dma16(scalar_base(qb + (size_t)i * 64 * ldq + (size_t)k * 128) + here(qo), to);
+            } else {
+                const int fl = fresh_lane(), chunk = (fl & 7) ^ (fl >> 3), rr = 8 * w + (fl >> 3);
+                int n = 64 * i + perm64(rr >> 4, rr & 15);
+                n = q0 + n < Qn ? n : Qn - 1 - q0;
+                copy_or_zero(k * CK + chunk * (16 / ES) < C, qb + n * ldq + (size_t)k * 128 + 16 * chunk,
+                             to, fl);
+            }
+        };
+        auto copy_xs = [&](int k) {
+            if (MODE == kFwdFp8 && w < kBP / kWave)
+                lds_dma4(A.a_s + (size_t)here(xo) * KB + k, &L.xs[k & 3][64 * w]);
         };
 
-        f32x4 acc[NP][4];
+        f32x4 acc[8][4];
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-        // 8 consecutive c (16 bytes) of the wavefront's tile j of p or q, half s
+        // 8 consecutive c (16 bytes) a lane of the 16 rows at `row`, half s
         auto frag_n = [&](const char *buf, int row, int s) {
             return *(const MOE_LDS u32x4 *)(buf + (row + r) * 128 + (((4 * s + g) ^ (r & 7)) << 4));
         };
+        // the same of tile j of the 64-column block blk of c-major data
         auto frag_t = [&](const char *buf, int blk, int j, int s) {
             const int ci = r >> 2, tt = r & 3;
             const int ch = (8 * blk + 2 * tt + (j >> 1)) ^ t_key(ci);
@@ -267,76 +320,182 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
             const s16x8 v = {lo4[0], lo4[1], lo4[2], lo4[3], hi4[0], hi4[1], hi4[2], hi4[3]};
             return __builtin_bit_cast(u32x4, v);
         };
+        auto frag_q = [&](const char *buf, int j, int s) {
+            return kQT ? frag_t(buf, wq, j, s) : frag_n(buf, 64 * wq + 16 * j, s);
+        };
+        auto frag_p = [&](const char *buf, int i, int s) {
+            return kDwMode ? frag_t(buf, 2 * wp + (i >> 2), i & 3, s)
+                           : frag_n(buf, 128 * wp + 16 * i, s);
+        };
 
-        if (steps > 0) fetch(0, 0);
-        for (int k = 0; k < steps; ++k) {
-            const int b = k & 1;
-            int next_row = 0;
-            if (MODE == kDw && t < 128) {
-                const int c = (k + 1) * 64 + (t & 63);
-                next_row = c < cnt ? source_row(t < 64 ? A.a : A.b, lo + c) : -1;
-                L.rows[(k + 1) & 1][t >> 6][t & 63] = next_row;
-            }
-            wait_vm<0>();
-            __syncthreads();
-            if (k + 1 < steps) fetch(k + 1, b ^ 1);
-            if (MODE == kFwdFp8) {
-                const float wsk = as_scalar(ws)[k];
-                i32x8 qf[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const u32x4 a0 = frag_n(L.q[b], 64 * wq + 16 * j, 0);
-                    const u32x4 a1 = frag_n(L.q[b], 64 * wq + 16 * j, 1);
-                    qf[j] = i32x8{(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3],
-                                  (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
-                }
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const u32x4 b0 = frag_n(L.p[b], WP * wp + 16 * i, 0);
-                    const u32x4 b1 = frag_n(L.p[b], WP * wp + 16 * i, 1);
-                    const i32x8 pf = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3],
-                                      (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
-                    const float sc = L.xs[b][WP * wp + 16 * i + r] * wsk;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            qf[j], pf, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(d[c], sc, acc[i][j][c]);
-                    }
-                }
+        // A step is two clusters of 32 matrix instructions; cluster 0 / 1 takes
+        // the first / second 64 p rows of the wavefront with all of q (dw: all
+        // rows with the first / second 32 of c). A cluster is two phases, in
+        // each of which the wavefronts of one half of p load (fragments of
+        // the next cluster from LDS, copies of later steps) while those of
+        // the other half, on the same SIMDs, multiply: the halves run one
+        // phase apart, a barrier after every phase.
+        //   A buffer is written again two phases after its last reader's load
+        // phase began, by copies issued after a barrier that the reads'
+        // completion (the wait at the end of every load phase) precedes: the
+        // first half of step k + 2 in cluster 1 of step k, its second half in
+        // cluster 0 of step k + 1. Each copy is waited for a whole step after its
+        // issue, in the load phase before the first one that reads it; the 8
+        // copies issued since may stay in flight.
+        auto first = [&](int k, bool fast) {      // 6 copies (dw: 4)
+            if (kDwMode) {
+                copy_p(0, k, fast), copy_q(0, k, fast), copy_p(1, k, fast), copy_q(1, k, fast);
             } else {
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    bf16x8 qf[4];
+                for (int i = 0; i < 4; ++i) copy_q(i, k, fast);
+                copy_p(0, k, fast), copy_p(1, k, fast);
+            }
+        };
+        auto second = [&](int k, bool fast) {     // 2 copies (dw: 4)
+            if (kDwMode) copy_p(2, k, fast), copy_q(2, k, fast), copy_p(3, k, fast), copy_q(3, k, fast);
+            else copy_p(2, k, fast), copy_p(3, k, fast);
+        };
+        auto copy_first = [&](int k) {
+            copy_xs(k);
+            if (easy && (k + 1) * CK <= C) first(k, true);
+            else first(k, false);
+        };
+        auto copy_second = [&](int k) {
+            if (easy && (k + 1) * CK <= C) second(k, true);
+            else second(k, false);
+        };
+        if (steps > 0) {
+            copy_first(0);
+            copy_second(0);
+            if (steps > 1) {
+                copy_first(1);
+                wait_vm<8>();
+            } else {
+                wait_vm<0>();
+            }
+            wait_lds();
+        }
+        phase_barrier();
+        if (wp == 1) phase_barrier();
+
+        for (int k = 0; k < steps; ++k) {
+            const char *const bp = L.p[k & 1], *const bq = L.q[k & 1];
+            constexpr int NF = kDwMode ? 8 : 4;      // p fragments of a cluster
+            u32x4 qf[4][2], pf[NF][2];
+            float sc[4] = {0, 0, 0, 0};
+            const float wsk = MODE == kFwdFp8 ? as_scalar(ws)[k] : 0.0f;
+            int next = -1;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        qf[j] = as_bf16x8(kQT ? frag_t(L.q[b], wq, j, s)
-                                              : frag_n(L.q[b], 64 * wq + 16 * j, s));
+            for (int c = 0; c < 2; ++c) {
+                const bool work0 = nc > 2 * c, work1 = nc > 2 * c + 1;   // 32 rows each
+                if (kDwMode) {
 #pragma unroll
-                    for (int i = 0; i < NP; ++i) {
-                        const bf16x8 pf =
-                            as_bf16x8(kPT ? frag_t(L.p[b], (WP / 64) * wp + (i >> 2), i & 3, s)
-                                          : frag_n(L.p[b], WP * wp + 16 * i, s));
+                    for (int j = 0; j < 4; ++j) qf[j][0] = frag_q(bq, j, c);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) pf[i % NF][0] = frag_p(bp, i, c);
+                    // rows of step k + 3
+                    if (w < 2 && c == 0) {
+                        const int cc = 64 * (k + 3) + l;
+                        if (cc < cnt) next = source_row(w == 0 ? A.a : A.b, lo + cc);
+                    }
+                    if (w < 2 && c == 1) L.rows[(k + 3) & 3][w][l] = next;
+                } else {
+                    if (c == 0) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) qf[j][0] = frag_q(bq, j, 0), qf[j][1] = frag_q(bq, j, 1);
+                    }
+                    if (work0) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            pf[i][0] = frag_p(bp, 4 * c + i, 0), pf[i][1] = frag_p(bp, 4 * c + i, 1);
+                            if (MODE == kFwdFp8) sc[i] = L.xs[k & 3][128 * wp + 64 * c + 16 * i + r] * wsk;
+                        }
+                    }
+                }
+                if (c == 0) {
+                    if (k + 1 < steps) {
+                        copy_second(k + 1);
+                        wait_vm<8>();
+                    } else {
+                        wait_vm<0>();
+                    }
+                } else {
+                    if (k + 2 < steps) {
+                        copy_first(k + 2);
+                        wait_vm<8>();
+                    } else if (k + 1 < steps) {
+                        wait_vm<kDwMode ? 4 : 2>();
+                    } else {
+                        wait_vm<0>();
+                    }
+                }
+                wait_lds();
+                phase_barrier();
+                __builtin_amdgcn_s_setprio(1);
+                if (kDwMode) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[j], pf,
-                                                                                acc[i][j], 0, 0, 0);
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                as_bf16x8(qf[j][0]), as_bf16x8(pf[i % NF][0]), acc[i][j], 0, 0, 0);
+                } else {
+                    auto multiply = [&](int i0) {     // p tiles i0, i0 + 1 of the cluster
+                        if (MODE == kFwdFp8) {
+                            f32x4 part[2][4];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    part[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                        as_i32x8(qf[j][0], qf[j][1]),
+                                        as_i32x8(pf[(i0 + i) % NF][0], pf[(i0 + i) % NF][1]),
+                                        f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                    for (int v = 0; v < 4; ++v)
+                                        acc[4 * c + i0 + i][j][v] = fmaf(
+                                            part[i][j][v], sc[i0 + i], acc[4 * c + i0 + i][j][v]);
+                        } else {
+#pragma unroll
+                            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                                for (int i = i0; i < i0 + 2; ++i)
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j)
+                                        acc[4 * c + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                            as_bf16x8(qf[j][s]), as_bf16x8(pf[i % NF][s]),
+                                            acc[4 * c + i][j], 0, 0, 0);
+                        }
+                    };
+                    if (work1) {
+                        multiply(0);
+                        multiply(2);
+                    } else if (work0) {
+                        multiply(0);
                     }
                 }
+                __builtin_amdgcn_s_setprio(0);
+                phase_barrier();
             }
         }
+        if (wp == 0) phase_barrier();
 
         // lane (g, r): p of tile i, q = 64 wq + 16 g + 4 j + 0..3
-        const int q = at.q0 + 64 * wq + 16 * g;
+        const int le = fresh_lane(), re = le & 15;
+        const int q = q0 + 64 * wq + 16 * (le >> 4);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
+        for (int i = 0; i < 8; ++i) {
+            if (i >= 2 * nc) continue;
             long row;
-            if (MODE == kDw) {
-                const int p = at.p0 + WP * wp + (i >> 2) * 64 + perm64(i & 3, r);
-                row = p < Pn ? (long)at.e * A.N + p : -1;
+            if (kDwMode) {
+                const int p = p0 + 128 * wp + (i >> 2) * 64 + perm64(i & 3, re);
+                row = p < A.N ? (long)e * A.N + p : -1;
             } else {
-                row = L.dst[WP * wp + 16 * i + r];
+                row = L.dst[128 * wp + 16 * i + re];
             }
             if (row < 0) continue;
             if (A.out_f32) {
@@ -345,7 +504,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
                 for (int j = 0; j < 4; ++j) {
                     if (q + 4 * j < Qn) {
                         f32x4 v = acc[i][j];
-                        if (MODE == kDw && A.accumulate) v += *(const MOE_GLOBAL f32x4 *)(o + 4 * j);
+                        if (kDwMode && A.accumulate) v += *(const MOE_GLOBAL f32x4 *)(o + 4 * j);
                         *(MOE_GLOBAL f32x4 *)(o + 4 * j) = v;
                     }
                 }
@@ -383,27 +542,18 @@ static void launch_product(const ProductArgs &a, hipStream_t s) {
     const int cu = compute_units();
     constexpr int kid = MODE == kFwd ? K_PROD : MODE == kFwdFp8 ? K_PROD_FP8 : MODE == kDx ? K_PROD_DX : K_PROD_DW;
     // one workgroup a compute unit (its LDS); fewer where there are fewer tiles
-    if (MODE == kDw) {
-        constexpr int BP = 256;
-        const long tiles = (long)a.E * ((a.N + BP - 1) / BP) * ((a.K + kBQ - 1) / kBQ);
-        MOE_LAUNCH(kid, (product_kernel<MODE, 256>), dim3((unsigned)(tiles < cu ? tiles : cu)),
-                   dim3(kPThreads), 0, s, a);
-        return;
-    }
-    const int Qn = MODE == kDx ? a.K : a.N;
-    const long avg = a.R / a.E;
-    const int BP = avg > 128 ? 256 : avg > 64 ? 128 : 64;
-    const long most = ((a.R + BP - 1) / BP + (a.R < a.E ? a.R : a.E)) * (long)((Qn + kBQ - 1) / kBQ);
-    const dim3 grid((unsigned)(most < cu ? most : cu));
-    if (BP == 256) MOE_LAUNCH(kid, (product_kernel<MODE, 256>), grid, dim3(kPThreads), 0, s, a);
-    else if (BP == 128) MOE_LAUNCH(kid, (product_kernel<MODE, 128>), grid, dim3(kPThreads), 0, s, a);
-    else MOE_LAUNCH(kid, (product_kernel<MODE, 64>), grid, dim3(kPThreads), 0, s, a);
+    const int Qn = MODE == kFwd || MODE == kFwdFp8 ? a.N : a.K;
+    const long tq = (Qn + kBQ - 1) / kBQ;
+    const long tiles = MODE == kDw ? (long)a.E * ((a.N + kBP - 1) / kBP) * tq
+                                   : (a.R / kBP + (a.R < a.E ? a.R : a.E)) * tq;
+    MOE_LAUNCH(kid, product_kernel<MODE>, dim3((unsigned)(tiles < cu ? tiles : cu)),
+               dim3(kPThreads), 0, s, a);
 }
 
 // Sizes that every product shares; unit: the elements of 16 bytes.
 static int check_sizes(int R, int N, int K, int E, const int32_t *offsets, int unit) {
     if (R < 0 || E < 1 || E > kMaxE || N < 8 || K < unit || N % 8 || K % unit) return MOE_EINVAL;
-    if (N > (1 << 24) || K > (1 << 24)) return MOE_EINVAL;
+    if (N > (1 << 20) || K > (1 << 20)) return MOE_EINVAL;
     if (!offsets && E != 1) return MOE_EINVAL;
     return MOE_OK;
 }

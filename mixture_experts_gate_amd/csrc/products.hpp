@@ -53,6 +53,16 @@ __device__ __forceinline__ void group_of(const ProductArgs &a, int e, int &lo, i
     cnt = hi > lo ? hi - lo : 0;
 }
 
+// The same for an expert of this lane's own.
+__device__ __forceinline__ void group_of_lane(const ProductArgs &a, int e, int &lo, int &cnt) {
+    lo = 0, cnt = a.R;
+    if (!a.offsets) return;
+    const int b = a.offsets[e], f = a.offsets[e + 1];
+    lo = b < 0 ? 0 : b > a.R ? a.R : b;
+    const int hi = f < 0 ? 0 : f > a.R ? a.R : f;
+    cnt = hi > lo ? hi - lo : 0;
+}
+
 // Source row of sorted row i, or -1 where the index is not a row of r.
 __device__ __forceinline__ int source_row(const RowsIn &r, int i) {
     if (!r.idx) return i;
