@@ -27,30 +27,16 @@
 // Rows past an expert's last one read a row that exists and are not stored;
 // columns past the end of c are zeros in LDS (both operands, so that no
 // garbage meets a zero).
+#include <stdlib.h>
+
 #include <atomic>
 
 #include "products.hpp"
 
 namespace moe {
 
-typedef __attribute__((ext_vector_type(4))) short s16x4;
-typedef __attribute__((ext_vector_type(8))) int i32x8;
-
-__device__ __forceinline__ i32x8 as_i32x8(u32x4 a, u32x4 b) {
-    return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
-}
-
 constexpr int kPThreads = 512;   // 8 wavefronts: 2 along p x 4 along q
 constexpr int kBP = 256, kBQ = 256;   // p and q per tile
-constexpr int kMaxE = 512;
-
-// XOR key of the 16-byte chunks of an LDS row of c-major data: rows c..c+3 of
-// one transposing read (4 pieces of 8 bytes, 32 bytes apart) land in 16
-// different chunks of the 256 bytes that the banks span.
-__device__ __forceinline__ int t_key(int c) { return (c & 1) | ((c & 2) << 2); }
-
-// Index inside a 64-row block of the p or q that tile j, row r stands for.
-__device__ __forceinline__ int perm64(int j, int r) { return 16 * (r >> 2) + 4 * j + (r & 3); }
 
 // Barrier without a memory fence (a fenced one would wait for the copies in
 // flight); the compiler keeps memory accesses and matrix instructions on
@@ -61,44 +47,6 @@ __device__ __forceinline__ void phase_barrier() {
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
-}
-
-// Tile li of mp x tq: groups of at most 8 p tiles, in a group q outer and p
-// inner, so that the 32 tiles an XCD works on at a time are about 8 x 4 of them
-// and share their rows of P and Q in its L2 (8192 x 8192 x 8192, bf16: 992 us
-// against 1045 us with p inner over all 32 p tiles, whose misses fill the
-// bandwidth behind the L2).
-__device__ __forceinline__ void place_of(int li, int mp, int tq, int &p, int &q) {
-    const int ng = (mp + 7) / 8, gp = (mp + ng - 1) / ng;
-    const int gi = li / (gp * tq), rest = li - gi * gp * tq;
-    const int gl = mp - gi * gp < gp ? mp - gi * gp : gp;
-    q = rest / gl;
-    p = gi * gp + rest - q * gl;
-}
-
-// A wavefront-uniform address kept in scalar registers: the lanes' offsets are
-// added by the load, not kept added to it in vector registers.
-__device__ __forceinline__ const char *scalar_base(const char *p) {
-    asm volatile("" : "+s"(p));
-    return p;
-}
-
-// The offset, widened where it is used and not before.
-__device__ __forceinline__ uint32_t here(uint32_t o) {
-    asm volatile("" : "+v"(o));
-    return o;
-}
-
-// This lane's index, which the compiler takes for a new value.
-__device__ __forceinline__ int fresh_lane() {
-    int l = lane_id();
-    asm volatile("" : "+v"(l));
-    return l;
-}
-
-// Waits for this wavefront's LDS accesses (lgkmcnt 0, the vector counter as it is).
-__device__ __forceinline__ void wait_lds() {
-    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));
 }
 
 struct TileLds {
@@ -131,26 +79,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
     if (kDwMode) {
         total = A.E * tpw * tq;
     } else {
-        const int t = threadIdx.x, l = lane_id();
-        int n = 0;
-        if (t < A.E) {
-            int lo, cnt;
-            group_of_lane(A, t, lo, cnt);
-            n = (cnt + kBP - 1) / kBP;
-        }
-        int incl = n;
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) {
-            const int o = __shfl_up(incl, d);
-            if (l >= d) incl += o;
-        }
-        if (l == kWave - 1) L.wsum[w] = incl;
-        __syncthreads();
-        int before = 0;
-        for (int i = 0; i < w; ++i) before += L.wsum[i];
-        if (t < A.E) L.base[t + 1] = before + incl;
-        if (t == 0) L.base[0] = 0;
-        __syncthreads();
+        total_tiles<kPThreads>(A, kBP, L.base, L.wsum);
         total = L.base[A.E] * tq;
     }
 
@@ -174,15 +103,9 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
         } else {
             // expert e with base[e] <= m < base[e+1]; q outer, p inner. The
             // expert's rows are spread evenly over its tiles, in units of 64.
-            int a = 0, b = A.E;
-            while (b - a > 1) {
-                const int mid = (a + b) >> 1;
-                if ((long)L.base[mid] * tq <= ti) a = mid;
-                else b = mid;
-            }
-            e = __builtin_amdgcn_readfirstlane(a);
-            const int mp = __builtin_amdgcn_readfirstlane(L.base[a + 1] - L.base[a]);
-            const int li = ti - __builtin_amdgcn_readfirstlane(L.base[a]) * tq;
+            e = expert_of(L.base, A.E, tq, ti);
+            const int mp = __builtin_amdgcn_readfirstlane(L.base[e + 1] - L.base[e]);
+            const int li = ti - __builtin_amdgcn_readfirstlane(L.base[e]) * tq;
             group_of(A, e, lo, cnt);
             half = 32 * ((cnt + 64 * mp - 1) / (64 * mp));
             place_of(li, mp, tq, p0, q0);
@@ -305,27 +228,12 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-        // 8 consecutive c (16 bytes) a lane of the 16 rows at `row`, half s
-        auto frag_n = [&](const char *buf, int row, int s) {
-            return *(const MOE_LDS u32x4 *)(buf + (row + r) * 128 + (((4 * s + g) ^ (r & 7)) << 4));
-        };
-        // the same of tile j of the 64-column block blk of c-major data
-        auto frag_t = [&](const char *buf, int blk, int j, int s) {
-            const int ci = r >> 2, tt = r & 3;
-            const int ch = (8 * blk + 2 * tt + (j >> 1)) ^ t_key(ci);
-            const char *a = buf + (32 * s + 8 * g + ci) * 512 + ch * 16 + (j & 1) * 8;
-            const s16x4 lo4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4 *)(a));
-            const s16x4 hi4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4 *)(a + 4 * 512));
-            typedef __attribute__((ext_vector_type(8))) short s16x8;
-            const s16x8 v = {lo4[0], lo4[1], lo4[2], lo4[3], hi4[0], hi4[1], hi4[2], hi4[3]};
-            return __builtin_bit_cast(u32x4, v);
-        };
         auto frag_q = [&](const char *buf, int j, int s) {
-            return kQT ? frag_t(buf, wq, j, s) : frag_n(buf, 64 * wq + 16 * j, s);
+            return kQT ? frag_t(buf, 512, wq, j, s, g, r) : frag_n(buf, 64 * wq + 16 * j, s, g, r);
         };
         auto frag_p = [&](const char *buf, int i, int s) {
-            return kDwMode ? frag_t(buf, 2 * wp + (i >> 2), i & 3, s)
-                           : frag_n(buf, 128 * wp + 16 * i, s);
+            return kDwMode ? frag_t(buf, 512, 2 * wp + (i >> 2), i & 3, s, g, r)
+                           : frag_n(buf, 128 * wp + 16 * i, s, g, r);
         };
 
         // A step is two clusters of 32 matrix instructions; cluster 0 / 1 takes
@@ -369,9 +277,9 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
             copy_second(0);
             if (steps > 1) {
                 copy_first(1);
-                wait_vm<8>();
+                wait_copies<8>();
             } else {
-                wait_vm<0>();
+                wait_copies<0>();
             }
             wait_lds();
         }
@@ -415,18 +323,18 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
                 if (c == 0) {
                     if (k + 1 < steps) {
                         copy_second(k + 1);
-                        wait_vm<8>();
+                        wait_copies<8>();
                     } else {
-                        wait_vm<0>();
+                        wait_copies<0>();
                     }
                 } else {
                     if (k + 2 < steps) {
                         copy_first(k + 2);
-                        wait_vm<8>();
+                        wait_copies<8>();
                     } else if (k + 1 < steps) {
-                        wait_vm<kDwMode ? 4 : 2>();
+                        wait_copies<kDwMode ? 4 : 2>();
                     } else {
-                        wait_vm<0>();
+                        wait_copies<0>();
                     }
                 }
                 wait_lds();
@@ -497,29 +405,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
             } else {
                 row = L.dst[128 * wp + 16 * i + re];
             }
-            if (row < 0) continue;
-            if (A.out_f32) {
-                float *o = (float *)A.out + (size_t)row * Qn + q;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (q + 4 * j < Qn) {
-                        f32x4 v = acc[i][j];
-                        if (kDwMode && A.accumulate) v += *(const MOE_GLOBAL f32x4 *)(o + 4 * j);
-                        *(MOE_GLOBAL f32x4 *)(o + 4 * j) = v;
-                    }
-                }
-            } else {
-                uint16_t *o = (uint16_t *)A.out + (size_t)row * Qn + q;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (q + 8 * h < Qn) {
-                        const f32x4 a0 = acc[i][2 * h], a1 = acc[i][2 * h + 1];
-                        *(MOE_GLOBAL u32x4 *)(o + 8 * h) =
-                            u32x4{pack_bf16x2(a0[0], a0[1]), pack_bf16x2(a0[2], a0[3]),
-                                  pack_bf16x2(a1[0], a1[1]), pack_bf16x2(a1[2], a1[3])};
-                    }
-                }
-            }
+            store_row(A, kDwMode, row, q, Qn, acc[i]);
         }
     }
 }
@@ -537,16 +423,33 @@ int compute_units() {
     return n;
 }
 
+int kernel_of(int mode) {
+    return mode == kFwd ? K_PROD : mode == kFwdFp8 ? K_PROD_FP8 : mode == kDx ? K_PROD_DX : K_PROD_DW;
+}
+
+// Whether a product runs in 128 x 128 tiles rather than 256 x 256.
+static bool product_small(const ProductArgs &a, int mode) {
+    const char *f = getenv("MOE_SMALL");
+    return f && f[0] == '1';
+}
+
 template <int MODE>
 static void launch_product(const ProductArgs &a, hipStream_t s) {
     const int cu = compute_units();
-    constexpr int kid = MODE == kFwd ? K_PROD : MODE == kFwdFp8 ? K_PROD_FP8 : MODE == kDx ? K_PROD_DX : K_PROD_DW;
+    if ((MODE == kFwd || MODE == kFwdFp8) && product_streams(a)) {
+        launch_product_stream(a, MODE == kFwdFp8, s);
+        return;
+    }
+    if (product_small(a, MODE)) {
+        launch_product_small(a, MODE, s);
+        return;
+    }
     // one workgroup a compute unit (its LDS); fewer where there are fewer tiles
     const int Qn = MODE == kFwd || MODE == kFwdFp8 ? a.N : a.K;
     const long tq = (Qn + kBQ - 1) / kBQ;
     const long tiles = MODE == kDw ? (long)a.E * ((a.N + kBP - 1) / kBP) * tq
                                    : (a.R / kBP + (a.R < a.E ? a.R : a.E)) * tq;
-    MOE_LAUNCH(kid, product_kernel<MODE>, dim3((unsigned)(tiles < cu ? tiles : cu)),
+    MOE_LAUNCH(kernel_of(MODE), product_kernel<MODE>, dim3((unsigned)(tiles < cu ? tiles : cu)),
                dim3(kPThreads), 0, s, a);
 }
 

@@ -6,6 +6,8 @@
 
 namespace moe {
 
+constexpr int kMaxE = 512;       // experts of a product
+
 // A matrix whose rows a product reads: row i of the sorted order is row
 // idx[i] / div of the matrix (row i where idx is NULL); n rows exist.
 struct RowsIn {
@@ -83,6 +85,176 @@ __device__ __forceinline__ const float *scales_of(const ProductArgs &a, int e) {
     return a.m.s + (size_t)e * ((a.N + 127) / 128) * ((a.K + 127) / 128);
 }
 
+typedef __attribute__((ext_vector_type(8))) int i32x8;
+
+__device__ __forceinline__ i32x8 as_i32x8(u32x4 a, u32x4 b) {
+    return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+
+// A wavefront-uniform address kept in scalar registers: the lanes' offsets are
+// added by the load, not kept added to it in vector registers.
+__device__ __forceinline__ const char *scalar_base(const char *p) {
+    asm volatile("" : "+s"(p));
+    return p;
+}
+
+// The offset, widened where it is used and not before.
+__device__ __forceinline__ uint32_t here(uint32_t o) {
+    asm volatile("" : "+v"(o));
+    return o;
+}
+
+// This lane's index, which the compiler takes for a new value.
+__device__ __forceinline__ int fresh_lane() {
+    int l = lane_id();
+    asm volatile("" : "+v"(l));
+    return l;
+}
+
+// Waits for this wavefront's LDS accesses (lgkmcnt 0, the vector counter as
+// it is), or until at most n of its copies and loads are in flight; the
+// compiler keeps memory accesses on their side.
+__device__ __forceinline__ void wait_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));
+    asm volatile("" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("" ::: "memory");
+    wait_vm<N>();
+    asm volatile("" ::: "memory");
+}
+
+// Barrier without a memory fence (a fenced one would also wait for the loads
+// in flight).
+__device__ __forceinline__ void bare_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// XOR key of the 16-byte chunks of an LDS row of c-major data: rows c..c+3 of
+// one transposing read (4 pieces of 8 bytes, 32 bytes apart) land in 16
+// different chunks of the 256 bytes that the banks span.
+__device__ __forceinline__ int t_key(int c) { return (c & 1) | ((c & 2) << 2); }
+
+// Index inside a 64-row block of the p or q that tile j, row r stands for.
+__device__ __forceinline__ int perm64(int j, int r) { return 16 * (r >> 2) + 4 * j + (r & 3); }
+
+// Tile li of mp x tq: groups of at most 8 p tiles, in a group q outer and p
+// inner, so that the 32 tiles an XCD works on at a time are about 8 x 4 of them
+// and share their rows of P and Q in its L2 (8192 x 8192 x 8192, bf16: 992 us
+// against 1045 us with p inner over all 32 p tiles, whose misses fill the
+// bandwidth behind the L2).
+__device__ __forceinline__ void place_of(int li, int mp, int tq, int &p, int &q) {
+    const int ng = (mp + 7) / 8, gp = (mp + ng - 1) / ng;
+    const int gi = li / (gp * tq), rest = li - gi * gp * tq;
+    const int gl = mp - gi * gp < gp ? mp - gi * gp : gp;
+    q = rest / gl;
+    p = gi * gp + rest - q * gl;
+}
+
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(8))) short s16x8;
+
+// Fragments of a matrix instruction from LDS, lane (g, r) = (l / 16, l % 16): 8
+// consecutive c (16 bytes), half s of a step, of
+//   row `row` + r of c-contiguous data (rows of 128 bytes, chunks XORed with the row), or
+//   tile j of 64-column block blk of c-major data with rows of `stride` bytes.
+__device__ __forceinline__ u32x4 frag_n(const char *buf, int row, int s, int g, int r) {
+    return *(const MOE_LDS u32x4 *)(buf + (row + r) * 128 + (((4 * s + g) ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ u32x4 frag_t(const char *buf, int stride, int blk, int j, int s, int g, int r) {
+    const int ci = r >> 2, tt = r & 3;
+    const int ch = (8 * blk + 2 * tt + (j >> 1)) ^ t_key(ci);
+    const char *a = buf + (32 * s + 8 * g + ci) * stride + ch * 16 + (j & 1) * 8;
+    const s16x4 lo4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4 *)(a));
+    const s16x4 hi4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4 *)(a + 4 * stride));
+    const s16x8 v = {lo4[0], lo4[1], lo4[2], lo4[3], hi4[0], hi4[1], hi4[2], hi4[3]};
+    return __builtin_bit_cast(u32x4, v);
+}
+
+// p tiles before each expert (base[0 .. E]), for tiles of bp rows; by all THREADS
+// threads of a workgroup.
+template <int THREADS>
+__device__ __forceinline__ void total_tiles(const ProductArgs &A, int bp, int *base, int *wsum) {
+    const int l = lane_id(), w = threadIdx.x / kWave;
+    int run = 0;
+    if (threadIdx.x == 0) base[0] = 0;
+    for (int e0 = 0; e0 < A.E; e0 += THREADS) {
+        const int e = e0 + threadIdx.x;
+        int n = 0;
+        if (e < A.E) {
+            int lo, cnt;
+            group_of_lane(A, e, lo, cnt);
+            n = (cnt + bp - 1) / bp;
+        }
+        int incl = n;
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int o = __shfl_up(incl, d);
+            if (l >= d) incl += o;
+        }
+        if (l == kWave - 1) wsum[w] = incl;
+        __syncthreads();
+        int before = run, all = run;
+        for (int i = 0; i < THREADS / kWave; ++i) {
+            before += i < w ? wsum[i] : 0;
+            all += wsum[i];
+        }
+        if (e < A.E) base[e + 1] = before + incl;
+        run = all;
+        __syncthreads();
+    }
+}
+
+// Expert e with base[e] tq <= ti < base[e+1] tq.
+__device__ __forceinline__ int expert_of(const int *base, int E, int tq, int ti) {
+    int a = 0, b = E;
+    while (b - a > 1) {
+        const int mid = (a + b) >> 1;
+        if ((long)base[mid] * tq <= ti) a = mid;
+        else b = mid;
+    }
+    return __builtin_amdgcn_readfirstlane(a);
+}
+
+// 16 consecutive q of one row of out, of which those below Qn exist.
+__device__ __forceinline__ void store_row(const ProductArgs &A, bool dw, long row, int q, int Qn,
+                                          const f32x4 (&v)[4]) {
+    if (row < 0) return;
+    if (A.out_f32) {
+        float *const o = (float *)A.out + (size_t)row * Qn + q;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (q + 4 * j >= Qn) continue;
+            f32x4 x = v[j];
+            if (dw && A.accumulate) x += *(const MOE_GLOBAL f32x4 *)(o + 4 * j);
+            *(MOE_GLOBAL f32x4 *)(o + 4 * j) = x;
+        }
+    } else {
+        uint16_t *const o = (uint16_t *)A.out + (size_t)row * Qn + q;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (q + 8 * h < Qn)
+                *(MOE_GLOBAL u32x4 *)(o + 8 * h) =
+                    u32x4{pack_bf16x2(v[2 * h][0], v[2 * h][1]), pack_bf16x2(v[2 * h][2], v[2 * h][3]),
+                          pack_bf16x2(v[2 * h + 1][0], v[2 * h + 1][1]),
+                          pack_bf16x2(v[2 * h + 1][2], v[2 * h + 1][3])};
+    }
+}
+
+// products_stream.hip: the forward products at a handful of rows per expert
+bool product_streams(const ProductArgs &a);
+void launch_product_stream(const ProductArgs &a, bool fp8, hipStream_t s);
+
+// products_small.hip: any product in tiles of 128 x 128, two workgroups a
+// compute unit
+void launch_product_small(const ProductArgs &a, int mode, hipStream_t s);
+
+int kernel_of(int mode);   // timing id of a product
 int compute_units();   // of the current device (256 on MI355X)
 
 }  // namespace moe

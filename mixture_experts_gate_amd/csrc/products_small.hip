@@ -1,0 +1,245 @@
+// The products of products.hip in tiles of 128 x 128, for calls in which tiles of
+// 256 x 256 are too few to fill the device, or in which a tile has so few
+// steps that reading its first rows and writing its results is most of it: a
+// workgroup of four wavefronts (64 x 64 each) takes 70 KB of LDS, so two share a
+// compute unit, and one loads or stores while the other multiplies. Operand
+// layouts as there; one step is copied while the one before is multiplied.
+#include "products.hpp"
+
+namespace moe {
+
+constexpr int kTThreads = 256;
+constexpr int kT = 128;          // p and q per tile
+
+struct SmallLds {
+    char p[2][kT * 128];
+    char q[2][kT * 128];
+    int src[kT];          // source row of each LDS row of p (forward, dx)
+    int dst[kT];          // row of out, or -1
+    float xs[2][kT];      // FP8: scales of the p rows, by step
+    int rows[2][2][64];   // dw: source rows of dy and x, by step
+    int base[kMaxE + 1];  // p tiles before each expert
+    int wsum[4];
+};
+
+template <int MODE>
+__global__ __launch_bounds__(kTThreads, 2) void product_small_kernel(ProductArgs A) {
+    constexpr bool kDwMode = MODE == kDw, kQT = MODE == kDx || MODE == kDw;
+    constexpr int ES = MODE == kFwdFp8 ? 1 : 2;       // bytes of an element
+    constexpr int CK = 128 / ES;                       // c per step
+    __shared__ SmallLds L;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int l = lane_id(), t = threadIdx.x, g = l >> 4, r = l & 15;
+    const int wq = w & 1, wp = w >> 1;
+
+    const int Qn = MODE == kFwd || MODE == kFwdFp8 ? A.N : A.K;  // q count
+    const int tq = (Qn + kT - 1) / kT;
+    const int tpw = (A.N + kT - 1) / kT;                          // p tiles (dw)
+    const int KB = (A.K + 127) / 128;
+    const size_t lda = (size_t)(MODE == kFwd || MODE == kFwdFp8 ? A.K : A.N) * ES;
+    const size_t ldq = (size_t)A.K * ES;                          // rows of W, x
+
+    int total;
+    if (kDwMode) {
+        total = A.E * tpw * tq;
+    } else {
+        total_tiles<kTThreads>(A, kT, L.base, L.wsum);
+        total = L.base[A.E] * tq;
+    }
+    const int nx = gridDim.x >= 8 ? 8 : 1;
+    const int xcd = blockIdx.x % nx, per = ((int)gridDim.x - xcd + nx - 1) / nx;
+    const int t0 = (int)((long)total * xcd / nx), t1 = (int)((long)total * (xcd + 1) / nx);
+    for (int ti = t0 + (int)blockIdx.x / nx; ti < t1; ti += per) {
+        int e, p0, q0, lo, cnt, half = 64;
+        if (kDwMode) {
+            e = ti / (tpw * tq);
+            place_of(ti - e * tpw * tq, tpw, tq, p0, q0);
+            group_of(A, e, lo, cnt);
+            p0 *= kT;
+        } else {
+            // the expert's rows are spread evenly over its tiles, in units of 32
+            e = expert_of(L.base, A.E, tq, ti);
+            const int mp = __builtin_amdgcn_readfirstlane(L.base[e + 1] - L.base[e]);
+            const int li = ti - __builtin_amdgcn_readfirstlane(L.base[e]) * tq;
+            group_of(A, e, lo, cnt);
+            half = 16 * ((cnt + 32 * mp - 1) / (32 * mp));
+            place_of(li, mp, tq, p0, q0);
+            p0 *= 2 * half;
+        }
+        q0 *= kT;
+        const int np = half / 16;    // p tiles of a wavefront with work
+        const int C = kDwMode ? cnt : MODE == kDx ? A.N : A.K;
+        const int steps = (C + CK - 1) / CK;
+
+        __syncthreads();   // the last tile's readers of L are done
+        if (!kDwMode) {
+            if (t < kT) {
+                const int o = t & 63, p = p0 + (t >> 6) * half + o;
+                const bool in = o < half && p < cnt;
+                const int i = lo + (in ? p : 0);
+                const int s = source_row(A.a, i);
+                int d = -1;
+                if (in && s >= 0) {
+                    d = A.out_rows ? A.out_rows[i] : i;
+                    if (d < 0 || d >= A.out_n) d = -1;
+                }
+                L.src[t] = s < 0 ? 0 : s;
+                L.dst[t] = d;
+            }
+        } else if (t < 128) {
+            L.rows[0][w][l] = l < cnt ? source_row(w == 0 ? A.a : A.b, lo + l) : -1;
+        }
+        __syncthreads();
+
+        // Copies: 8 rows of 128 bytes an instruction, or 4 rows of 256 (c-major);
+        // rows past the end of p or q read one that exists, c past its end
+        // becomes zeros.
+        const char *pp[4], *qp[4];
+        const int chunk = (l & 7) ^ (l >> 3), tchunk = (l & 15) ^ t_key(l >> 4);
+        const int tc = 4 * w + (l >> 4);                      // c of a c-major copy (+ 16 i)
+        const char *const mat = kDwMode ? A.b.base : mat_of(A, e, ES);
+        const size_t pcol = kDwMode ? 2 * (size_t)(p0 + 8 * tchunk < A.N ? p0 + 8 * tchunk : 0) : 0;
+        const size_t qcol = kQT ? 2 * (size_t)(q0 + 8 * tchunk < Qn ? q0 + 8 * tchunk : 0) : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!kDwMode) pp[i] = A.a.base + (size_t)L.src[32 * i + 8 * w + (l >> 3)] * lda + 16 * chunk;
+            if (!kQT) {
+                const int rr = (32 * i + 8 * w + (l >> 3)) & 63;
+                int n = q0 + 64 * (i >> 1) + perm64(rr >> 4, rr & 15);
+                n = n < Qn ? n : Qn - 1;
+                qp[i] = mat + (size_t)n * ldq + 16 * chunk;
+            } else if (MODE == kDx) {
+                qp[i] = mat + (size_t)(16 * i + tc) * ldq + qcol;
+            }
+        }
+        const float *ws = nullptr;
+        if (MODE == kFwdFp8) ws = scales_of(A, e) + (size_t)(q0 / 128) * KB;
+
+        auto copy = [&](bool in, const char *from, char *to) {
+            if (in) lds_dma16(from, to);
+            else *(MOE_LDS u32x4 *)(to + 16 * l) = u32x4{0, 0, 0, 0};
+        };
+        auto fetch = [&](int k) {
+            char *const P = L.p[k & 1], *const Q = L.q[k & 1];
+            const bool full = (k + 1) * CK <= C;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                char *const tn = P + (32 * i + 8 * w) * 128, *const tt = P + (16 * i + 4 * w) * 256;
+                if (kDwMode) {
+                    const int s = L.rows[k & 1][0][16 * i + tc];
+                    copy(s >= 0, A.a.base + (size_t)s * lda + pcol, tt);
+                } else {
+                    copy(full || k * CK + chunk * (16 / ES) < C, pp[i] + (size_t)k * 128, tn);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                char *const tn = Q + (32 * i + 8 * w) * 128, *const tt = Q + (16 * i + 4 * w) * 256;
+                if (kDwMode) {
+                    const int s = L.rows[k & 1][1][16 * i + tc];
+                    copy(s >= 0, mat + (size_t)s * ldq + qcol, tt);
+                } else if (MODE == kDx) {
+                    copy(full || k * CK + 16 * i + tc < C, qp[i] + (size_t)k * CK * ldq, tt);
+                } else {
+                    copy(full || k * CK + chunk * (16 / ES) < C, qp[i] + (size_t)k * 128, tn);
+                }
+            }
+            if (MODE == kFwdFp8 && w < 2)
+                lds_dma4(A.a_s + (size_t)L.src[64 * w + l] * KB + k, &L.xs[k & 1][64 * w]);
+        };
+
+        f32x4 acc[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+        int next = -1;      // dw: source row of the step after the next
+        auto look = [&](int k) {
+            if (kDwMode && t < 128) {
+                next = -1;
+                if (64 * k + l < cnt) next = source_row(w == 0 ? A.a : A.b, lo + 64 * k + l);
+            }
+        };
+        look(1);
+        if (steps > 0) fetch(0);
+        for (int k = 0; k < steps; ++k) {
+            const char *const bp = L.p[k & 1], *const bq = L.q[k & 1];
+            if (kDwMode && t < 128) L.rows[(k + 1) & 1][w][l] = next;
+            wait_copies<0>();
+            wait_lds();
+            bare_barrier();     // step k is in LDS, step k - 1 is read
+            look(k + 2);
+            if (k + 1 < steps) fetch(k + 1);
+            const float wsk = MODE == kFwdFp8 ? as_scalar(ws)[k] : 0.0f;
+            if (MODE == kFwdFp8) {
+                u32x4 qf[4][2];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) qf[j][s] = frag_n(bq, 64 * wq + 16 * j, s, g, r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (i >= np) continue;
+                    const u32x4 a = frag_n(bp, 64 * wp + 16 * i, 0, g, r), b = frag_n(bp, 64 * wp + 16 * i, 1, g, r);
+                    const float sc = L.xs[k & 1][64 * wp + 16 * i + r] * wsk;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            as_i32x8(qf[j][0], qf[j][1]), as_i32x8(a, b), f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(d[c], sc, acc[i][j][c]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    bf16x8 qf[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        qf[j] = as_bf16x8(kQT ? frag_t(bq, 256, wq, j, s, g, r)
+                                              : frag_n(bq, 64 * wq + 16 * j, s, g, r));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (i >= np) continue;
+                        const bf16x8 pf = as_bf16x8(kDwMode ? frag_t(bp, 256, wp, i, s, g, r)
+                                                            : frag_n(bp, 64 * wp + 16 * i, s, g, r));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[j], pf, acc[i][j], 0, 0, 0);
+                    }
+                }
+            }
+        }
+
+        // lane (g, r): p of tile i, q = 64 wq + 16 g + 4 j + 0..3
+        const int q = q0 + 64 * wq + 16 * g;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= np) continue;
+            long row;
+            if (kDwMode) {
+                const int p = p0 + 64 * wp + perm64(i, r);
+                row = p < A.N ? (long)e * A.N + p : -1;
+            } else {
+                row = L.dst[64 * wp + 16 * i + r];
+            }
+            store_row(A, kDwMode, row, q, Qn, acc[i]);
+        }
+    }
+}
+
+void launch_product_small(const ProductArgs &a, int mode, hipStream_t s) {
+    const int Qn = mode == kFwd || mode == kFwdFp8 ? a.N : a.K;
+    const long tq = (Qn + kT - 1) / kT;
+    const long tiles = mode == kDw ? (long)a.E * ((a.N + kT - 1) / kT) * tq
+                                   : (a.R / kT + (a.R < a.E ? a.R : a.E)) * tq;
+    const long most = 2L * compute_units();
+    const dim3 grid((unsigned)(tiles < most ? tiles : most)), block(kTThreads);
+    const int kid = kernel_of(mode);
+    if (mode == kFwd) MOE_LAUNCH(kid, product_small_kernel<kFwd>, grid, block, 0, s, a);
+    else if (mode == kFwdFp8) MOE_LAUNCH(kid, product_small_kernel<kFwdFp8>, grid, block, 0, s, a);
+    else if (mode == kDx) MOE_LAUNCH(kid, product_small_kernel<kDx>, grid, block, 0, s, a);
+    else MOE_LAUNCH(kid, product_small_kernel<kDw>, grid, block, 0, s, a);
+}
+
+}  // namespace moe
