@@ -14,15 +14,14 @@
 // c; the matrix core wants 8 consecutive c per lane, which the first kind
 // gives with one 16-byte read and the second with two transposing reads
 // (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 columns and each gets one
-// column). Q is the A operand and P the B operand of the 16x16 instruction, so
-// a lane ends with 4 consecutive q of one p; the 16 rows of an A tile are
-// chosen as q = 16 (r/4) + 4 j + r%4 over four tiles j, which makes them 16
-// consecutive q and the stores full lines.
+// column). Which operand is A and which q make a tile goes by the stores (perm64).
 //
 // FP8: out[p][q] = sum_b xs[p][b] ws[q/128][b] (sum over 128 columns of block
-// b). The inner sum is one 16x16x128 instruction started at zero; a lane's
-// four results share one p, so their scale is one number per lane, and
-// adding them to the fp32 sums is four multiply-adds.
+// b). The inner sum is one 16x16x128 instruction started at zero, whose results
+// are scaled and added to the fp32 sums. (The instruction adds 8 columns'
+// products aligned to the largest, dropping what lies 13 bits below its
+// leading bit; across the eights it keeps fp32. That is 2^-4 of what rounding
+// the codes to E4M3 took away already, at twice the rate of bf16.)
 //
 // Rows past an expert's last one read a row that exists and are not stored;
 // columns past the end of c are zeros in LDS (both operands, so that no
@@ -155,7 +154,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
         {
             const int chunk = (l & 7) ^ (l >> 3);                 // 16-byte chunk of a 128-byte row
             const int tc = 2 * w + (l >> 5);                      // c of a c-major copy (+ 16 i)
-            const int tchunk = (l & 31) ^ t_key(tc);              // its chunk (8 columns)
+            const int tchunk = (l & 31) ^ t_key<kDwMode>(tc);              // its chunk (8 columns)
             if (!kDwMode) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -165,7 +164,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
             }
             if (!kQT) {
                 const int rr = 8 * w + (l >> 3);
-                qo = (uint32_t)(perm64(rr >> 4, rr & 15) * ldq) + 16 * chunk;
+                qo = (uint32_t)(perm64<MODE>(rr >> 4, rr & 15) * ldq) + 16 * chunk;
             } else {
                 const int col = q0 + 8 * tchunk < Qn ? q0 + 8 * tchunk : 0;
                 qo = (MODE == kDx ? (uint32_t)(tc * ldq) : 0) + 2 * col;
@@ -179,42 +178,38 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
             if (t < kBP) xo = (uint32_t)L.src[t];
         }
 
-        auto copy_or_zero = [&](bool in, const char *from, char *to, int lane) {
-            if (in) lds_dma16(from, to);
-            else *(MOE_LDS u32x4 *)(to + 16 * lane) = u32x4{0, 0, 0, 0};
-        };
         // copy i of 4 of step k, operands P and Q
         auto copy_p = [&](int i, int k, bool fast) {
             char *const to = L.p[k & 1] + (kDwMode ? (16 * i + 2 * w) * 512 : (prow + 32 * i) * 128);
             if (kDwMode) {
                 const int fl = fresh_lane(), s = L.rows[k & 3][0][16 * i + 2 * w + (fl >> 5)];
-                copy_or_zero(s >= 0, A.a.base + (size_t)s * lda + po[0], to, fl);
+                copy_or_zeros(s >= 0, A.a.base + (size_t)s * lda + po[0], to);
             } else if (fast) {
                 lds_dma16(scalar_base(A.a.base + (size_t)k * 128) + here(po[i]), to);
             } else {
                 const int fl = fresh_lane(), chunk = (fl & 7) ^ (fl >> 3);
-                copy_or_zero(k * CK + chunk * (16 / ES) < C,
+                copy_or_zeros(k * CK + chunk * (16 / ES) < C,
                              A.a.base + (size_t)L.src[prow + 32 * i + (fl >> 3)] * lda +
-                                 (size_t)k * 128 + 16 * chunk, to, fl);
+                                 (size_t)k * 128 + 16 * chunk, to);
             }
         };
         auto copy_q = [&](int i, int k, bool fast) {
             char *const to = L.q[k & 1] + (kQT ? (16 * i + 2 * w) * 512 : (64 * i + 8 * w) * 128);
             if (kDwMode) {
                 const int fl = fresh_lane(), s = L.rows[k & 3][1][16 * i + 2 * w + (fl >> 5)];
-                copy_or_zero(s >= 0, qb + (size_t)s * ldq + qo, to, fl);
+                copy_or_zeros(s >= 0, qb + (size_t)s * ldq + qo, to);
             } else if (MODE == kDx) {
                 const char *const from = scalar_base(qb + (size_t)(k * CK + 16 * i) * ldq) + here(qo);
                 if (fast) lds_dma16(from, to);
-                else copy_or_zero(k * CK + 16 * i + 2 * w + (fresh_lane() >> 5) < C, from, to, fresh_lane());
+                else copy_or_zeros(k * CK + 16 * i + 2 * w + (fresh_lane() >> 5) < C, from, to);
             } else if (fast) {
                 lds_dma16(scalar_base(qb + (size_t)i * 64 * ldq + (size_t)k * 128) + here(qo), to);
             } else {
                 const int fl = fresh_lane(), chunk = (fl & 7) ^ (fl >> 3), rr = 8 * w + (fl >> 3);
-                int n = 64 * i + perm64(rr >> 4, rr & 15);
+                int n = 64 * i + perm64<MODE>(rr >> 4, rr & 15);
                 n = q0 + n < Qn ? n : Qn - 1 - q0;
-                copy_or_zero(k * CK + chunk * (16 / ES) < C, qb + n * ldq + (size_t)k * 128 + 16 * chunk,
-                             to, fl);
+                copy_or_zeros(k * CK + chunk * (16 / ES) < C, qb + n * ldq + (size_t)k * 128 + 16 * chunk,
+                              to);
             }
         };
         auto copy_xs = [&](int k) {
@@ -229,10 +224,10 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
             for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
         auto frag_q = [&](const char *buf, int j, int s) {
-            return kQT ? frag_t(buf, 512, wq, j, s, g, r) : frag_n(buf, 64 * wq + 16 * j, s, g, r);
+            return kQT ? frag_t<kDwMode>(buf, 512, wq, j, s, g, r) : frag_n(buf, 64 * wq + 16 * j, s, g, r);
         };
         auto frag_p = [&](const char *buf, int i, int s) {
-            return kDwMode ? frag_t(buf, 512, 2 * wp + (i >> 2), i & 3, s, g, r)
+            return kDwMode ? frag_t<kDwMode>(buf, 512, 2 * wp + (i >> 2), i & 3, s, g, r)
                            : frag_n(buf, 128 * wp + 16 * i, s, g, r);
         };
 
@@ -281,7 +276,6 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
             } else {
                 wait_copies<0>();
             }
-            wait_lds();
         }
         phase_barrier();
         if (wp == 1) phase_barrier();
@@ -346,7 +340,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                as_bf16x8(qf[j][0]), as_bf16x8(pf[i % NF][0]), acc[i][j], 0, 0, 0);
+                                as_bf16x8(pf[i % NF][0]), as_bf16x8(qf[j][0]), acc[i][j], 0, 0, 0);
                 } else {
                     auto multiply = [&](int i0) {     // p tiles i0, i0 + 1 of the cluster
                         if (MODE == kFwdFp8) {
@@ -375,7 +369,8 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
 #pragma unroll
                                     for (int j = 0; j < 4; ++j)
                                         acc[4 * c + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                            as_bf16x8(qf[j][s]), as_bf16x8(pf[i % NF][s]),
+                                            as_bf16x8(q_is_row(MODE) ? qf[j][s] : pf[i % NF][s]),
+                                            as_bf16x8(q_is_row(MODE) ? pf[i % NF][s] : qf[j][s]),
                                             acc[4 * c + i][j], 0, 0, 0);
                         }
                     };
@@ -392,20 +387,15 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
         }
         if (wp == 0) phase_barrier();
 
-        // lane (g, r): p of tile i, q = 64 wq + 16 g + 4 j + 0..3
-        const int le = fresh_lane(), re = le & 15;
-        const int q = q0 + 64 * wq + 16 * (le >> 4);
+        const int le = fresh_lane();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (i >= 2 * nc) continue;
-            long row;
-            if (kDwMode) {
-                const int p = p0 + 128 * wp + (i >> 2) * 64 + perm64(i & 3, re);
-                row = p < A.N ? (long)e * A.N + p : -1;
-            } else {
-                row = L.dst[128 * wp + 16 * i + re];
-            }
-            store_row(A, kDwMode, row, q, Qn, acc[i]);
+            store_tile<MODE>(A, q0 + 64 * wq, Qn, le >> 4, le & 15, acc[i], [&](int p) -> long {
+                if (!kDwMode) return L.dst[128 * wp + 16 * i + p];
+                const int n = p0 + 128 * wp + 16 * i + p;
+                return n < A.N ? (long)e * A.N + n : -1;
+            });
         }
     }
 }

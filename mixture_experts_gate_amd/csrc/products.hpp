@@ -91,6 +91,13 @@ __device__ __forceinline__ i32x8 as_i32x8(u32x4 a, u32x4 b) {
     return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
+// 16 bytes a lane from `from`, or zeros. Always one copy instruction, whichever
+// lanes are in: the waits count them.
+__device__ const uint32_t g_zeros[4] = {0, 0, 0, 0};
+__device__ __forceinline__ void copy_or_zeros(bool in, const char *from, char *to) {
+    lds_dma16(in ? from : (const char *)g_zeros, to);
+}
+
 // A wavefront-uniform address kept in scalar registers: the lanes' offsets are
 // added by the load, not kept added to it in vector registers.
 __device__ __forceinline__ const char *scalar_base(const char *p) {
@@ -135,13 +142,30 @@ __device__ __forceinline__ void bare_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// XOR key of the 16-byte chunks of an LDS row of c-major data: rows c..c+3 of
-// one transposing read (4 pieces of 8 bytes, 32 bytes apart) land in 16
-// different chunks of the 256 bytes that the banks span.
-__device__ __forceinline__ int t_key(int c) { return (c & 1) | ((c & 2) << 2); }
+// Whether q is the row of the matrix instruction's result (Q its A operand) or
+// its column. dx: row, see below; FP8: row, so that a lane's four results share
+// one p and one scale (as column, with four scales a lane: 632 against 530 us
+// for the FP8 down projection of 4096 tokens).
+constexpr bool q_is_row(int mode) { return mode == kDx || mode == kFwdFp8; }
 
-// Index inside a 64-row block of the p or q that tile j, row r stands for.
-__device__ __forceinline__ int perm64(int j, int r) { return 16 * (r >> 2) + 4 * j + (r & 3); }
+// The 16 q of a matrix instruction's tile j of a 64-column block. Where q is the
+// column, four tiles give a lane q = 4 r + 0..3: 16 lanes store 64 consecutive q
+// of a row. Where it is the row (and for dx, whose W comes through the
+// transposing read, which takes groups of four consecutive columns), q = 16
+// (r/4) + 4 j + r%4: a lane has 16 consecutive q.
+template <int MODE>
+__device__ __forceinline__ int perm64(int j, int r) {
+    return q_is_row(MODE) ? 16 * (r >> 2) + 4 * j + (r & 3) : 4 * r + j;
+}
+
+// XOR key of the 16-byte chunks of an LDS row of c-major data: what one
+// transposing read takes of rows c..c+3 lands in different banks. dw reads 16
+// consecutive columns (32 bytes) of each row, dx four times 4 columns 32 bytes
+// apart (8 bytes of each of 4 chunks; 16 different chunks of the 256 bytes that the banks span).
+template <bool DW>
+__device__ __forceinline__ int t_key(int c) {
+    return DW ? 2 * (c & 3) : (c & 1) | ((c & 2) << 2);
+}
 
 // Tile li of mp x tq: groups of at most 8 p tiles, in a group q outer and p
 // inner, so that the 32 tiles an XCD works on at a time are about 8 x 4 of them
@@ -162,14 +186,16 @@ typedef __attribute__((ext_vector_type(8))) short s16x8;
 // Fragments of a matrix instruction from LDS, lane (g, r) = (l / 16, l % 16): 8
 // consecutive c (16 bytes), half s of a step, of
 //   row `row` + r of c-contiguous data (rows of 128 bytes, chunks XORed with the row), or
-//   tile j of 64-column block blk of c-major data with rows of `stride` bytes.
+//   tile j of 64-column block blk of c-major data with rows of `stride` bytes
+//   (dw: columns 16 j + 0..15).
 __device__ __forceinline__ u32x4 frag_n(const char *buf, int row, int s, int g, int r) {
     return *(const MOE_LDS u32x4 *)(buf + (row + r) * 128 + (((4 * s + g) ^ (r & 7)) << 4));
 }
+template <bool DW>
 __device__ __forceinline__ u32x4 frag_t(const char *buf, int stride, int blk, int j, int s, int g, int r) {
     const int ci = r >> 2, tt = r & 3;
-    const int ch = (8 * blk + 2 * tt + (j >> 1)) ^ t_key(ci);
-    const char *a = buf + (32 * s + 8 * g + ci) * stride + ch * 16 + (j & 1) * 8;
+    const int ch = (DW ? 8 * blk + 2 * j + (tt >> 1) : 8 * blk + 2 * tt + (j >> 1)) ^ t_key<DW>(ci);
+    const char *a = buf + (32 * s + 8 * g + ci) * stride + ch * 16 + (DW ? tt & 1 : j & 1) * 8;
     const s16x4 lo4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4 *)(a));
     const s16x4 hi4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4 *)(a + 4 * stride));
     const s16x8 v = {lo4[0], lo4[1], lo4[2], lo4[3], hi4[0], hi4[1], hi4[2], hi4[3]};
@@ -221,28 +247,61 @@ __device__ __forceinline__ int expert_of(const int *base, int E, int tq, int ti)
     return __builtin_amdgcn_readfirstlane(a);
 }
 
-// 16 consecutive q of one row of out, of which those below Qn exist.
-__device__ __forceinline__ void store_row(const ProductArgs &A, bool dw, long row, int q, int Qn,
-                                          const f32x4 (&v)[4]) {
-    if (row < 0) return;
-    if (A.out_f32) {
-        float *const o = (float *)A.out + (size_t)row * Qn + q;
+// A wavefront's results of p tile i, acc[j][c] for the four q tiles j of its
+// 64-column block from q0, to the rows of out that `row` gives for p of the tile (-1: none).
+//   dx, FP8: lane (g, r) has q = 16 g + 4 j + c of p = r;
+//   forward bf16: q = 4 r + j of p = 4 g + c;  dw: q = 16 j + r of p = 4 g + c.
+template <int MODE, class Row>
+__device__ __forceinline__ void store_tile(const ProductArgs &A, int q0, int Qn, int g, int r,
+                                           const f32x4 (&v)[4], Row row) {
+    typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+    if (q_is_row(MODE)) {
+        const long to = row(r);
+        const int q = q0 + 16 * g;
+        if (to < 0) return;
+        if (A.out_f32) {
+            float *const o = (float *)A.out + (size_t)to * Qn + q;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (q + 4 * j >= Qn) continue;
-            f32x4 x = v[j];
-            if (dw && A.accumulate) x += *(const MOE_GLOBAL f32x4 *)(o + 4 * j);
-            *(MOE_GLOBAL f32x4 *)(o + 4 * j) = x;
+            for (int j = 0; j < 4; ++j)
+                if (q + 4 * j < Qn) *(MOE_GLOBAL f32x4 *)(o + 4 * j) = v[j];
+        } else {
+            uint16_t *const o = (uint16_t *)A.out + (size_t)to * Qn + q;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (q + 8 * h < Qn)
+                    *(MOE_GLOBAL u32x4 *)(o + 8 * h) =
+                        u32x4{pack_bf16x2(v[2 * h][0], v[2 * h][1]), pack_bf16x2(v[2 * h][2], v[2 * h][3]),
+                              pack_bf16x2(v[2 * h + 1][0], v[2 * h + 1][1]),
+                              pack_bf16x2(v[2 * h + 1][2], v[2 * h + 1][3])};
         }
-    } else {
-        uint16_t *const o = (uint16_t *)A.out + (size_t)row * Qn + q;
+        return;
+    }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (q + 8 * h < Qn)
-                *(MOE_GLOBAL u32x4 *)(o + 8 * h) =
-                    u32x4{pack_bf16x2(v[2 * h][0], v[2 * h][1]), pack_bf16x2(v[2 * h][2], v[2 * h][3]),
-                          pack_bf16x2(v[2 * h + 1][0], v[2 * h + 1][1]),
-                          pack_bf16x2(v[2 * h + 1][2], v[2 * h + 1][3])};
+    for (int c = 0; c < 4; ++c) {
+        const long to = row(4 * g + c);
+        if (to < 0) continue;
+        if (MODE == kDw) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int q = q0 + 16 * j + r;
+                if (q >= Qn) continue;
+                if (A.out_f32) {
+                    MOE_GLOBAL float *const o = (MOE_GLOBAL float *)A.out + (size_t)to * Qn + q;
+                    *o = A.accumulate ? *o + v[j][c] : v[j][c];
+                } else {
+                    ((MOE_GLOBAL uint16_t *)A.out)[(size_t)to * Qn + q] = (uint16_t)f32_to_bf16_bits(v[j][c]);
+                }
+            }
+        } else {
+            const int q = q0 + 4 * r;
+            if (q >= Qn) continue;
+            if (A.out_f32)
+                *(MOE_GLOBAL f32x4 *)((float *)A.out + (size_t)to * Qn + q) =
+                    f32x4{v[0][c], v[1][c], v[2][c], v[3][c]};
+            else
+                *(MOE_GLOBAL u32x2 *)((uint16_t *)A.out + (size_t)to * Qn + q) =
+                    u32x2{pack_bf16x2(v[0][c], v[1][c]), pack_bf16x2(v[2][c], v[3][c])};
+        }
     }
 }
 

@@ -11,23 +11,26 @@ namespace moe {
 constexpr int kTThreads = 256;
 constexpr int kT = 128;          // p and q per tile
 
+template <int S>
 struct SmallLds {
-    char p[2][kT * 128];
-    char q[2][kT * 128];
-    int src[kT];          // source row of each LDS row of p (forward, dx)
-    int dst[kT];          // row of out, or -1
-    float xs[2][kT];      // FP8: scales of the p rows, by step
-    int rows[2][2][64];   // dw: source rows of dy and x, by step
+    char p[S][kT * 128];
+    char q[S][kT * 128];
+    int src[kT];              // source row of each LDS row of p (forward, dx)
+    int dst[kT];              // row of out, or -1
+    float xs[S][kT];          // FP8: scales of the p rows, by step
+    int rows[S + 1][2][64];   // dw: source rows of dy and x, by step
     int base[kMaxE + 1];  // p tiles before each expert
     int wsum[4];
 };
 
-template <int MODE>
-__global__ __launch_bounds__(kTThreads, 2) void product_small_kernel(ProductArgs A) {
+// S: steps that LDS holds, of which S - 1 are copied ahead (S = 1: none; four workgroups share a
+// compute unit then).
+template <int MODE, int S>
+__global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) void product_small_kernel(ProductArgs A) {
     constexpr bool kDwMode = MODE == kDw, kQT = MODE == kDx || MODE == kDw;
     constexpr int ES = MODE == kFwdFp8 ? 1 : 2;       // bytes of an element
     constexpr int CK = 128 / ES;                       // c per step
-    __shared__ SmallLds L;
+    __shared__ SmallLds<S> L;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l = lane_id(), t = threadIdx.x, g = l >> 4, r = l & 15;
     const int wq = w & 1, wp = w >> 1;
@@ -87,7 +90,11 @@ __global__ __launch_bounds__(kTThreads, 2) void product_small_kernel(ProductArgs
                 L.dst[t] = d;
             }
         } else if (t < 128) {
-            L.rows[0][w][l] = l < cnt ? source_row(w == 0 ? A.a : A.b, lo + l) : -1;
+#pragma unroll
+            for (int k = 0; k < S; ++k) {
+                const int c = 64 * k + l;
+                L.rows[k][w][l] = c < cnt ? source_row(w == 0 ? A.a : A.b, lo + c) : -1;
+            }
         }
         __syncthreads();
 
@@ -95,7 +102,7 @@ __global__ __launch_bounds__(kTThreads, 2) void product_small_kernel(ProductArgs
         // rows past the end of p or q read one that exists, c past its end
         // becomes zeros.
         const char *pp[4], *qp[4];
-        const int chunk = (l & 7) ^ (l >> 3), tchunk = (l & 15) ^ t_key(l >> 4);
+        const int chunk = (l & 7) ^ (l >> 3), tchunk = (l & 15) ^ t_key<kDwMode>(l >> 4);
         const int tc = 4 * w + (l >> 4);                      // c of a c-major copy (+ 16 i)
         const char *const mat = kDwMode ? A.b.base : mat_of(A, e, ES);
         const size_t pcol = kDwMode ? 2 * (size_t)(p0 + 8 * tchunk < A.N ? p0 + 8 * tchunk : 0) : 0;
@@ -105,7 +112,7 @@ __global__ __launch_bounds__(kTThreads, 2) void product_small_kernel(ProductArgs
             if (!kDwMode) pp[i] = A.a.base + (size_t)L.src[32 * i + 8 * w + (l >> 3)] * lda + 16 * chunk;
             if (!kQT) {
                 const int rr = (32 * i + 8 * w + (l >> 3)) & 63;
-                int n = q0 + 64 * (i >> 1) + perm64(rr >> 4, rr & 15);
+                int n = q0 + 64 * (i >> 1) + perm64<MODE>(rr >> 4, rr & 15);
                 n = n < Qn ? n : Qn - 1;
                 qp[i] = mat + (size_t)n * ldq + 16 * chunk;
             } else if (MODE == kDx) {
@@ -115,37 +122,33 @@ __global__ __launch_bounds__(kTThreads, 2) void product_small_kernel(ProductArgs
         const float *ws = nullptr;
         if (MODE == kFwdFp8) ws = scales_of(A, e) + (size_t)(q0 / 128) * KB;
 
-        auto copy = [&](bool in, const char *from, char *to) {
-            if (in) lds_dma16(from, to);
-            else *(MOE_LDS u32x4 *)(to + 16 * l) = u32x4{0, 0, 0, 0};
-        };
         auto fetch = [&](int k) {
-            char *const P = L.p[k & 1], *const Q = L.q[k & 1];
+            char *const P = L.p[k % S], *const Q = L.q[k % S];
             const bool full = (k + 1) * CK <= C;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 char *const tn = P + (32 * i + 8 * w) * 128, *const tt = P + (16 * i + 4 * w) * 256;
                 if (kDwMode) {
-                    const int s = L.rows[k & 1][0][16 * i + tc];
-                    copy(s >= 0, A.a.base + (size_t)s * lda + pcol, tt);
+                    const int s = L.rows[k % (S + 1)][0][16 * i + tc];
+                    copy_or_zeros(s >= 0, A.a.base + (size_t)s * lda + pcol, tt);
                 } else {
-                    copy(full || k * CK + chunk * (16 / ES) < C, pp[i] + (size_t)k * 128, tn);
+                    copy_or_zeros(full || k * CK + chunk * (16 / ES) < C, pp[i] + (size_t)k * 128, tn);
                 }
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 char *const tn = Q + (32 * i + 8 * w) * 128, *const tt = Q + (16 * i + 4 * w) * 256;
                 if (kDwMode) {
-                    const int s = L.rows[k & 1][1][16 * i + tc];
-                    copy(s >= 0, mat + (size_t)s * ldq + qcol, tt);
+                    const int s = L.rows[k % (S + 1)][1][16 * i + tc];
+                    copy_or_zeros(s >= 0, mat + (size_t)s * ldq + qcol, tt);
                 } else if (MODE == kDx) {
-                    copy(full || k * CK + 16 * i + tc < C, qp[i] + (size_t)k * CK * ldq, tt);
+                    copy_or_zeros(full || k * CK + 16 * i + tc < C, qp[i] + (size_t)k * CK * ldq, tt);
                 } else {
-                    copy(full || k * CK + chunk * (16 / ES) < C, qp[i] + (size_t)k * 128, tn);
+                    copy_or_zeros(full || k * CK + chunk * (16 / ES) < C, qp[i] + (size_t)k * 128, tn);
                 }
             }
             if (MODE == kFwdFp8 && w < 2)
-                lds_dma4(A.a_s + (size_t)L.src[64 * w + l] * KB + k, &L.xs[k & 1][64 * w]);
+                lds_dma4(A.a_s + (size_t)L.src[64 * w + l] * KB + k, &L.xs[k % S][64 * w]);
         };
 
         f32x4 acc[4][4];
@@ -153,23 +156,30 @@ __global__ __launch_bounds__(kTThreads, 2) void product_small_kernel(ProductArgs
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-        int next = -1;      // dw: source row of the step after the next
+        int next = -1;      // dw: a source row of step k + S
         auto look = [&](int k) {
             if (kDwMode && t < 128) {
                 next = -1;
                 if (64 * k + l < cnt) next = source_row(w == 0 ? A.a : A.b, lo + 64 * k + l);
             }
         };
-        look(1);
-        if (steps > 0) fetch(0);
+#pragma unroll
+        for (int k = 0; k < S - 1; ++k)
+            if (k < steps) fetch(k);
         for (int k = 0; k < steps; ++k) {
-            const char *const bp = L.p[k & 1], *const bq = L.q[k & 1];
-            if (kDwMode && t < 128) L.rows[(k + 1) & 1][w][l] = next;
-            wait_copies<0>();
+            if (S == 1) fetch(k);
+            const char *const bp = L.p[k % S], *const bq = L.q[k % S];
+            look(k + S);
+            // step k is in LDS (of the S - 2 steps after it, those copied may be in
+            // flight), and step k - 1 is read
+            const int later = steps - 1 - k < S - 2 ? steps - 1 - k : S - 2;
+            if (later >= 2) wait_copies<16>();
+            else if (later == 1) wait_copies<8>();
+            else wait_copies<0>();
             wait_lds();
-            bare_barrier();     // step k is in LDS, step k - 1 is read
-            look(k + 2);
-            if (k + 1 < steps) fetch(k + 1);
+            bare_barrier();
+            if (kDwMode && t < 128) L.rows[(k + S) % (S + 1)][w][l] = next;
+            if (S > 1 && k + S - 1 < steps) fetch(k + S - 1);
             const float wsk = MODE == kFwdFp8 ? as_scalar(ws)[k] : 0.0f;
             if (MODE == kFwdFp8) {
                 u32x4 qf[4][2];
@@ -181,7 +191,7 @@ __global__ __launch_bounds__(kTThreads, 2) void product_small_kernel(ProductArgs
                 for (int i = 0; i < 4; ++i) {
                     if (i >= np) continue;
                     const u32x4 a = frag_n(bp, 64 * wp + 16 * i, 0, g, r), b = frag_n(bp, 64 * wp + 16 * i, 1, g, r);
-                    const float sc = L.xs[k & 1][64 * wp + 16 * i + r] * wsk;
+                    const float sc = L.xs[k % S][64 * wp + 16 * i + r] * wsk;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
@@ -196,34 +206,35 @@ __global__ __launch_bounds__(kTThreads, 2) void product_small_kernel(ProductArgs
                     bf16x8 qf[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        qf[j] = as_bf16x8(kQT ? frag_t(bq, 256, wq, j, s, g, r)
+                        qf[j] = as_bf16x8(kQT ? frag_t<kDwMode>(bq, 256, wq, j, s, g, r)
                                               : frag_n(bq, 64 * wq + 16 * j, s, g, r));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (i >= np) continue;
-                        const bf16x8 pf = as_bf16x8(kDwMode ? frag_t(bp, 256, wp, i, s, g, r)
+                        const bf16x8 pf = as_bf16x8(kDwMode ? frag_t<kDwMode>(bp, 256, wp, i, s, g, r)
                                                             : frag_n(bp, 64 * wp + 16 * i, s, g, r));
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[j], pf, acc[i][j], 0, 0, 0);
+                            acc[i][j] = q_is_row(MODE)
+                                            ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[j], pf, acc[i][j], 0, 0, 0)
+                                            : __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf, qf[j], acc[i][j], 0, 0, 0);
                     }
                 }
             }
+            if (S == 1) {
+                wait_lds();
+                bare_barrier();     // the step is read
+            }
         }
 
-        // lane (g, r): p of tile i, q = 64 wq + 16 g + 4 j + 0..3
-        const int q = q0 + 64 * wq + 16 * g;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i >= np) continue;
-            long row;
-            if (kDwMode) {
-                const int p = p0 + 64 * wp + perm64(i, r);
-                row = p < A.N ? (long)e * A.N + p : -1;
-            } else {
-                row = L.dst[64 * wp + 16 * i + r];
-            }
-            store_row(A, kDwMode, row, q, Qn, acc[i]);
+            store_tile<MODE>(A, q0 + 64 * wq, Qn, g, r, acc[i], [&](int p) -> long {
+                if (!kDwMode) return L.dst[64 * wp + 16 * i + p];
+                const int n = p0 + 64 * wp + 16 * i + p;
+                return n < A.N ? (long)e * A.N + n : -1;
+            });
         }
     }
 }
@@ -233,13 +244,20 @@ void launch_product_small(const ProductArgs &a, int mode, hipStream_t s) {
     const long tq = (Qn + kT - 1) / kT;
     const long tiles = mode == kDw ? (long)a.E * ((a.N + kT - 1) / kT) * tq
                                    : (a.R / kT + (a.R < a.E ? a.R : a.E)) * tq;
-    const long most = 2L * compute_units();
-    const dim3 grid((unsigned)(tiles < most ? tiles : most)), block(kTThreads);
+    const int cu = compute_units();
+    const bool deep = tiles <= 2L * cu;
+    const dim3 grid((unsigned)(tiles < 4L * cu ? tiles : 4L * cu)), block(kTThreads);
     const int kid = kernel_of(mode);
-    if (mode == kFwd) MOE_LAUNCH(kid, product_small_kernel<kFwd>, grid, block, 0, s, a);
-    else if (mode == kFwdFp8) MOE_LAUNCH(kid, product_small_kernel<kFwdFp8>, grid, block, 0, s, a);
-    else if (mode == kDx) MOE_LAUNCH(kid, product_small_kernel<kDx>, grid, block, 0, s, a);
-    else MOE_LAUNCH(kid, product_small_kernel<kDw>, grid, block, 0, s, a);
+#define MOE_SMALL_LAUNCH(MODE)                                                                     \
+    do {                                                                                           \
+        if (deep) MOE_LAUNCH(kid, (product_small_kernel<MODE, 4>), grid, block, 0, s, a);          \
+        else MOE_LAUNCH(kid, (product_small_kernel<MODE, 1>), grid, block, 0, s, a);               \
+    } while (0)
+    if (mode == kFwd) MOE_SMALL_LAUNCH(kFwd);
+    else if (mode == kFwdFp8) MOE_SMALL_LAUNCH(kFwdFp8);
+    else if (mode == kDx) MOE_SMALL_LAUNCH(kDx);
+    else MOE_SMALL_LAUNCH(kDw);
+#undef MOE_SMALL_LAUNCH
 }
 
 }  // namespace moe

@@ -91,6 +91,7 @@ SHAPES = [
     ([16] * 40, 512, 1024),
     ([2] * 100 + [0] * 50, 128, 384),
     ([1000, 3], 1536, 512),
+    ([150, 61, 0, 97] * 14, 768, 768),
 ]
 # the FP8 product's and the forward's calls through a gather and a scatter
 INDEXING = ["plain", "gather", "scatter"]
