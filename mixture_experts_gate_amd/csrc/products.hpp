@@ -13,9 +13,25 @@ constexpr int kMaxE = 512;       // experts of a product
 struct RowsIn {
     const char *base;
     const int32_t *idx;
-    int div;
     int n;
+    // v / div for 0 <= v < 2^31 as (v mul) >> (32 + shift), mul = floor(2^(31 +
+    // l) / div) + 1 and shift = l - 1 for 2^(l-1) < div <= 2^l: mul exceeds the
+    // quotient by at most one, which moves v mul by less than 2^31 <= 2^(31 +
+    // l) / div, one unit of the result over div. mul = 0: div is 1.
+    uint32_t mul;
+    int shift;
 };
+
+inline RowsIn rows_in(const void *base, const int32_t *idx, int div, int n) {
+    RowsIn r{(const char *)base, idx, n, 0, 0};
+    if (div > 1) {
+        int l = 1;
+        while ((1LL << l) < div) ++l;
+        r.mul = (uint32_t)((1ULL << (31 + l)) / (uint64_t)div + 1);
+        r.shift = l - 1;
+    }
+    return r;
+}
 
 // The experts' matrices [N][K]: either one array [E][N][K] (tab NULL) or the
 // w13 / w2 pointers of a moe_expert_w table.
@@ -70,7 +86,7 @@ __device__ __forceinline__ int source_row(const RowsIn &r, int i) {
     if (!r.idx) return i;
     int v = r.idx[i];
     if (v < 0) return -1;
-    v = r.div == 1 ? v : v / r.div;
+    if (r.mul) v = (int)(__umulhi((uint32_t)v, r.mul) >> r.shift);
     return v < r.n ? v : -1;
 }
 

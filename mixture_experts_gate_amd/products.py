@@ -29,8 +29,9 @@ import torch
 
 from . import _lib
 
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
+_OUT = (torch.bfloat16, torch.float32)
 
 
 class TableMatrices(NamedTuple):
@@ -48,17 +49,19 @@ def _fail(what):
     raise ValueError(what)
 
 
-def _need(t, name, dtype, dev=None):
-    """t is a contiguous device tensor of `dtype` (on `dev`)."""
+def _need(t, name, dtypes, dev=None):
+    """t is a contiguous tensor of one of `dtypes` on a GPU (number `dev`).
+    (One line where it is: a call's checks cost as much as a small kernel.)"""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous()
+            and (dev is None or t.get_device() == dev)):
+        return t
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _fail(f"{name}: a tensor on the GPU is needed")
-    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
-        _fail(f"{name}: {t.dtype}, {dtype} is needed")
+    if t.dtype not in dtypes:
+        _fail(f"{name}: {t.dtype}, {' or '.join(map(str, dtypes))} is needed")
     if not t.is_contiguous():
         _fail(f"{name}: must be contiguous")
-    if dev is not None and t.device != dev:
-        _fail(f"{name}: on {t.device}, the others are on {dev}")
-    return t
+    _fail(f"{name}: on GPU {t.get_device()}, the others are on {dev}")
 
 
 def _matrix(t, name, dtype, dev=None):
@@ -75,7 +78,7 @@ def _weights(w, ws, dtype, dev):
         if ws is not None:
             _fail("w_scale: the table of w has the scales")
         if isinstance(w.table, torch.Tensor):
-            _need(w.table, "w.table", torch.int64, dev)
+            _need(w.table, "w.table", (torch.int64,), dev)
             if w.table.numel() < 4 * w.E:
                 _fail("w.table: fewer than E entries")
         return None, None, _lib._ptr(w.table), w.mat, w.E, w.N, w.K
@@ -125,11 +128,11 @@ def _output(out, name, shape, dtypes, dev, stream):
     """`out`, checked, or a new tensor (made on the stream that writes it)."""
     if out is None:
         if stream is None:
-            return torch.empty(shape, dtype=dtypes[0], device=dev)
+            return torch.empty(shape, dtype=dtypes[0], device=torch.device("cuda", dev))
         if isinstance(stream, int):
             _fail(f"{name}: a stream handle needs the output given")
         with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtypes[0], device=dev)
+            return torch.empty(shape, dtype=dtypes[0], device=torch.device("cuda", dev))
     _need(out, name, dtypes, dev)
     return out
 
@@ -141,24 +144,32 @@ def _rows_output(out, name, R, n, out_rows, dtypes, dev, stream):
     return out
 
 
+_calls = {}      # the library's functions, once looked up
+
+
 def _run(fn, dev, stream, *args):
-    if torch.cuda.current_device() != dev.index:
+    """Enqueue on the current stream of GPU `dev`, or on `stream`."""
+    call = _calls.get(fn)
+    if call is None:
+        call = _calls[fn] = getattr(_lib.load(), fn)
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _run(fn, dev, stream, *args)
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    rc = getattr(_lib.load(), fn)(*args, stream if isinstance(stream, int) else stream.cuda_stream)
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        if stream.device_index != dev:
+            _fail(f"stream: of GPU {stream.device_index}, the tensors are on {dev}")
+        stream = stream.cuda_stream
+    rc = call(*args, stream)
     if rc < 0:
         _lib._check(fn, rc)
-
-
-_OUT = (_BF16, _F32)
 
 
 def grouped_matmul(x, w, offsets=None, *, rows=None, div=1, out_rows=None, out=None, stream=None):
     """y[i] = W_e x[i] over sorted rows: x bf16 [n, K], w bf16 -> [R, N] (``out``
     may be bf16, the default, or fp32). N and K are multiples of 8."""
-    dev = _matrix(x, "x", _BF16).device
+    dev = _matrix(x, "x", _BF16).get_device()
     pw, _, tab, mat, E, N, K = _weights(w, None, _BF16, dev)
     if x.shape[1] != K:
         _fail(f"x: {x.shape[1]} columns, w has {K}")
@@ -166,7 +177,7 @@ def grouped_matmul(x, w, offsets=None, *, rows=None, div=1, out_rows=None, out=N
     out = _rows_output(out, "out", R, N, out_rows, _OUT, dev, stream)
     _run("moe_grouped_gemm", dev, stream, x.data_ptr(), _index(rows, "rows", R, dev), div,
          x.shape[0], _offsets(offsets, E, dev), pw, tab, mat, R, N, K, E, out.data_ptr(),
-         _index(out_rows, "out_rows", R, dev), out.shape[0], int(out.dtype is _F32))
+         _index(out_rows, "out_rows", R, dev), out.shape[0], int(out.dtype is torch.float32))
     return out
 
 
@@ -176,7 +187,7 @@ def grouped_matmul_fp8(x, x_scale, w, w_scale=None, offsets=None, *, rows=None, 
     (float8_e4m3fn or uint8 codes) with fp32 scales [n, ceil(K/128)] (from
     ``quant_fp8``), w E4M3 with fp32 scales [E, ceil(N/128), ceil(K/128)] ->
     [R, N] bf16 or fp32. N is a multiple of 8, K of 16."""
-    dev = _matrix(x, "x", _FP8).device
+    dev = _matrix(x, "x", _FP8).get_device()
     pw, ps, tab, mat, E, N, K = _weights(w, w_scale, _FP8, dev)
     if x.shape[1] != K:
         _fail(f"x: {x.shape[1]} columns, w has {K}")
@@ -187,7 +198,7 @@ def grouped_matmul_fp8(x, x_scale, w, w_scale=None, offsets=None, *, rows=None, 
     _run("moe_grouped_gemm_fp8", dev, stream, x.data_ptr(), x_scale.data_ptr(),
          _index(rows, "rows", R, dev), div, x.shape[0], _offsets(offsets, E, dev), pw, ps, tab,
          mat, R, N, K, E, out.data_ptr(), _index(out_rows, "out_rows", R, dev), out.shape[0],
-         int(out.dtype is _F32))
+         int(out.dtype is torch.float32))
     return out
 
 
@@ -195,7 +206,7 @@ def grouped_matmul_dx(dy, w, offsets=None, *, rows=None, div=1, out_rows=None, o
                       stream=None):
     """dx[i] = W_e^T dy[i] over sorted rows: dy bf16 [n, N], w bf16 -> [R, K]
     bf16 or fp32; ``rows``/``div`` index dy, ``out_rows`` dx."""
-    dev = _matrix(dy, "dy", _BF16).device
+    dev = _matrix(dy, "dy", _BF16).get_device()
     pw, _, tab, mat, E, N, K = _weights(w, None, _BF16, dev)
     if dy.shape[1] != N:
         _fail(f"dy: {dy.shape[1]} columns, w has {N} rows")
@@ -203,7 +214,7 @@ def grouped_matmul_dx(dy, w, offsets=None, *, rows=None, div=1, out_rows=None, o
     out = _rows_output(out, "out", R, K, out_rows, _OUT, dev, stream)
     _run("moe_grouped_gemm_dx", dev, stream, dy.data_ptr(), _index(rows, "rows", R, dev), div,
          dy.shape[0], _offsets(offsets, E, dev), pw, tab, mat, R, N, K, E, out.data_ptr(),
-         _index(out_rows, "out_rows", R, dev), out.shape[0], int(out.dtype is _F32))
+         _index(out_rows, "out_rows", R, dev), out.shape[0], int(out.dtype is torch.float32))
     return out
 
 
@@ -212,7 +223,7 @@ def grouped_matmul_dw(dy, x, offsets=None, *, dy_rows=None, dy_div=1, x_rows=Non
     """dW_e = sum over the expert's sorted rows i of dy[i] x[i]^T: dy bf16
     [n, N], x bf16 [m, K] -> [E, N, K] fp32 (or bf16, given as ``out``); zeros
     for an expert without rows. ``accumulate`` adds to fp32 ``out``."""
-    dev = _matrix(dy, "dy", _BF16).device
+    dev = _matrix(dy, "dy", _BF16).get_device()
     _matrix(x, "x", _BF16, dev)
     N, K = dy.shape[1], x.shape[1]
     R = _count(dy, dy_rows, "dy_rows")
@@ -221,12 +232,12 @@ def grouped_matmul_dw(dy, x, offsets=None, *, dy_rows=None, dy_div=1, x_rows=Non
     E = 1 if offsets is None else _need(offsets, "offsets", _I32, dev).numel() - 1
     if accumulate and out is None:
         _fail("out: needed to accumulate into")
-    out = _output(out, "out", (E, N, K), (_F32, _BF16), dev, stream)
+    out = _output(out, "out", (E, N, K), (torch.float32, torch.bfloat16), dev, stream)
     if out.shape[-2:] != (N, K) or out.numel() != E * N * K:
         _fail(f"out: {tuple(out.shape)}, [{E}, {N}, {K}] is needed")
     _run("moe_grouped_gemm_dw", dev, stream, dy.data_ptr(), _index(dy_rows, "dy_rows", R, dev),
          dy_div, dy.shape[0], x.data_ptr(), _index(x_rows, "x_rows", R, dev), x_div, x.shape[0],
-         _offsets(offsets, E, dev), R, N, K, E, out.data_ptr(), int(out.dtype is _F32),
+         _offsets(offsets, E, dev), R, N, K, E, out.data_ptr(), int(out.dtype is torch.float32),
          int(bool(accumulate)))
     return out
 
@@ -253,7 +264,7 @@ def _limit(n_rows, dev):
 def _halves(h):
     if _matrix(h, "h", _BF16).shape[1] % 2:
         _fail(f"h: an even number of columns is needed, got {h.shape[1]}")
-    return h.shape[0], h.shape[1] // 2, h.device
+    return h.shape[0], h.shape[1] // 2, h.get_device()
 
 
 def swiglu(h, w=None, w_rows=None, n_rows=None, out=None, stream=None):
@@ -263,7 +274,7 @@ def swiglu(h, w=None, w_rows=None, n_rows=None, out=None, stream=None):
     rows below it. I is a multiple of 8."""
     R, I, dev = _halves(h)
     pw, pr, wn = _row_weights(w, w_rows, R, dev)
-    out = _rows_output(out, "out", R, I, None, (_BF16,), dev, stream)
+    out = _rows_output(out, "out", R, I, None, _BF16, dev, stream)
     _run("moe_swiglu", dev, stream, h.data_ptr(), pw, pr, wn, _limit(n_rows, dev), R, I,
          out.data_ptr())
     return out
@@ -277,9 +288,9 @@ def swiglu_grad(h, da, w=None, w_rows=None, n_rows=None, dh=None, dw=None, a=Non
     if _matrix(da, "da", _BF16, dev).shape != (R, I):
         _fail(f"da: {tuple(da.shape)}, [{R}, {I}] is needed")
     pw, pr, wn = _row_weights(w, w_rows, R, dev)
-    dh = _rows_output(dh, "dh", R, 2 * I, None, (_BF16,), dev, stream)
+    dh = _rows_output(dh, "dh", R, 2 * I, None, _BF16, dev, stream)
     if w is not None:
-        dw = _output(dw, "dw", w.shape, (_F32,), dev, stream)
+        dw = _output(dw, "dw", w.shape, _F32, dev, stream)
         if dw.numel() != wn:
             _fail(f"dw: {tuple(dw.shape)}, {tuple(w.shape)} is needed")
     elif dw is not None:
@@ -294,7 +305,7 @@ def swiglu_grad(h, da, w=None, w_rows=None, n_rows=None, dh=None, dw=None, a=Non
 
 def _to_fp8(fn, x, R, K, n_rows, q, s, dev, stream):
     q = _output(q, "q", (R, K), _FP8, dev, stream)
-    s = _output(s, "s", (R, -(-K // 128)), (_F32,), dev, stream)
+    s = _output(s, "s", (R, -(-K // 128)), _F32, dev, stream)
     if q.shape != (R, K) or s.shape != (R, -(-K // 128)):
         _fail(f"q, s: {tuple(q.shape)}, {tuple(s.shape)} for {R} rows of {K}")
     _run(fn, dev, stream, x.data_ptr(), _limit(n_rows, dev), R, K, q.data_ptr(), s.data_ptr())
@@ -305,7 +316,7 @@ def quant_fp8(x, n_rows=None, q=None, s=None, stream=None):
     """Rows x bf16 [R, K] as (E4M3 codes [R, K], fp32 scales [R, ceil(K/128)]):
     scale = max(amax, 2^-100) / 448 over 128 columns of a row, code = x / scale
     to the nearest E4M3. K is a multiple of 8."""
-    dev = _matrix(x, "x", _BF16).device
+    dev = _matrix(x, "x", _BF16).get_device()
     return _to_fp8("moe_quant_fp8", x, x.shape[0], x.shape[1], n_rows, q, s, dev, stream)
 
 

@@ -92,6 +92,8 @@ SHAPES = [
     ([2] * 100 + [0] * 50, 128, 384),
     ([1000, 3], 1536, 512),
     ([150, 61, 0, 97] * 14, 768, 768),
+    ([1300, 513, 1, 900, 1255], 2056, 1168),
+    ([1300, 513, 1, 900, 1255], 1160, 2064),
 ]
 # the FP8 product's and the forward's calls through a gather and a scatter
 INDEXING = ["plain", "gather", "scatter"]
