@@ -11,7 +11,7 @@ import time
 import numpy as np
 import torch
 
-from . import _lib
+from . import _lib, products
 from .synth import blob_layout
 
 # moe_permute_ffn_combine derives the permutation in its gate/up launch from
@@ -46,12 +46,13 @@ def expert_table(base_ptr: int, n: int, layout, stride: int | None = None, devic
 def pack_to_device(pool: np.ndarray, layout, device="cuda"):
     """Upload expert blobs [n][nbytes] in the interchange layout and return a
     device tensor of the same shape in the kernel layout (MXFP4, NVFP4 and FP8
-    blocks packed by the library; bf16 blobs are used as they are)."""
+    blocks packed by the library; bf16 and block-scaled FP8 blobs are used as
+    they are)."""
     host = torch.from_numpy(np.ascontiguousarray(pool, dtype=np.uint8))
     if host.dim() == 1:
         host = host[None, :]
     src = host.to(device)
-    if layout.fmt == "bf16":
+    if layout.fmt in ("bf16", "fp8_block"):
         return src
     dst = torch.empty_like(src)
     n, nb = src.shape
@@ -359,6 +360,86 @@ class MoeLayer:
         _lib.moe_expert_ffn(x, self.sh_pair, self.sh_off, shared_table, self.fmt, T, 1, self.H,
                             self.I, 1, self.y_sh, self.y_fp32, self.ws_sh, self.ws_sh_bytes,
                             stream)
+
+
+class Fp8BlockLayer:
+    """One layer whose experts are FP8 matrices with a scale per 128 x 128 block
+    (blobs of ``blob_layout(H, I, "fp8_block")``), with at most T_max tokens:
+    route and permute, the tokens to FP8 with a scale per 128 columns, the
+    gate/up product, silu(g) u to FP8, the down product and the combine. H and I
+    are multiples of 32.
+
+    ``table`` is a device table of moe_expert_w, as ``expert_table`` makes it
+    for resident experts or ``ExpertCache.prefetch`` returns it."""
+
+    def __init__(self, H, E, k, I, T_max, shared=False, device="cuda"):
+        if H % 32 or I % 32:
+            raise ValueError("H and I must be multiples of 32")
+        self.H, self.E, self.k, self.I, self.T_max, self.shared = H, E, k, I, T_max, shared
+        n = max(T_max * k, 1)
+        bf16, i32 = torch.bfloat16, torch.int32
+
+        def buf(*shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+        self.topk_ids, self.topk_w = buf(T_max, k, dtype=i32), buf(T_max, k, dtype=torch.float32)
+        self.logits = buf(T_max, E, dtype=torch.float32)
+        self.offsets = buf(E + 1, dtype=i32)
+        self.sorted_pair, self.pair_row = buf(n, dtype=i32), buf(n, dtype=i32)
+        self.ws_perm_bytes = max(_lib.moe_workspace_size(T_max, k, H, I, E)[0], 256)
+        self.ws_perm = buf(self.ws_perm_bytes, dtype=torch.uint8)
+        self.xq, self.xs = buf(T_max, H, dtype=torch.uint8), buf(T_max, -(-H // 128), dtype=torch.float32)
+        self.h = buf(n, 2 * I, dtype=bf16)
+        self.aq, self.a_s = buf(n, I, dtype=torch.uint8), buf(n, -(-I // 128), dtype=torch.float32)
+        self.y, self.out = buf(n, H, dtype=bf16), buf(T_max, H, dtype=bf16)
+        if shared:
+            self.h_sh, self.y_sh = buf(T_max, 2 * I, dtype=bf16), buf(T_max, H, dtype=bf16)
+            self.aq_sh = buf(T_max, I, dtype=torch.uint8)
+            self.as_sh = buf(T_max, -(-I // 128), dtype=torch.float32)
+
+    def matrices(self, table, E=None):
+        """(W13, W2) of the experts of `table`."""
+        E = self.E if E is None else E
+        return (products.TableMatrices(table, _lib.MOE_MAT_W13, E, 2 * self.I, self.H),
+                products.TableMatrices(table, _lib.MOE_MAT_W2, E, self.H, self.I))
+
+    def ffn(self, T, x, table, shared_table=None, stream=None):
+        """The experts of the current permutation: y in pair order, and the
+        shared expert's rows (or None)."""
+        n = T * self.k
+        pair = self.sorted_pair[:n]
+        w13, w2 = self.matrices(table)
+        xq, xs = products.quant_fp8(x[:T], q=self.xq[:T], s=self.xs[:T], stream=stream)
+        h = products.grouped_matmul_fp8(xq, xs, w13, None, self.offsets, rows=pair, div=self.k,
+                                        out=self.h[:n], stream=stream)
+        aq, a_s = products.swiglu_quant_fp8(h, n_rows=self.offsets[self.E:], q=self.aq[:n],
+                                            s=self.a_s[:n], stream=stream)
+        products.grouped_matmul_fp8(aq, a_s, w2, None, self.offsets, out_rows=pair,
+                                    out=self.y[:n], stream=stream)
+        if shared_table is None:
+            return self.y[:n], None
+        if not self.shared:
+            raise ValueError("layer was built without shared-expert buffers")
+        s13, s2 = self.matrices(shared_table, 1)
+        h = products.grouped_matmul_fp8(xq, xs, s13, out=self.h_sh[:T], stream=stream)
+        aq, a_s = products.swiglu_quant_fp8(h, q=self.aq_sh[:T], s=self.as_sh[:T], stream=stream)
+        products.grouped_matmul_fp8(aq, a_s, s2, out=self.y_sh[:T], stream=stream)
+        return self.y[:n], self.y_sh[:T]
+
+    def forward(self, T, x, table, logits=None, wg=None, shared_table=None, renormalize=True,
+                stream=None):
+        """route -> permute -> experts -> combine; returns out[:T] (bf16)."""
+        if T > self.T_max:
+            raise ValueError("T exceeds the buffers' T_max")
+        if T == 0:
+            return self.out[:0]
+        _lib.moe_route_permute(x, wg, logits, None if logits is not None else self.logits, T, self.H,
+                               self.E, self.k, renormalize, self.topk_ids, self.topk_w,
+                               self.offsets, self.sorted_pair, self.pair_row, self.ws_perm,
+                               self.ws_perm_bytes, stream)
+        y, y_sh = self.ffn(T, x, table, shared_table, stream)
+        _lib.moe_combine(y, False, self.topk_w, y_sh, T, self.k, self.H, self.out, stream)
+        return self.out[:T]
 
 
 def layout_for(cfg):

@@ -87,6 +87,9 @@ class BlobLayout:
     MXFP4: [W13 codes (2I rows x H/2 bytes)][W13 scales (2I x H/32)]
            [W2 codes (H rows x I/2 bytes)][W2 scales (H x I/32)]
     BF16:  [W13 (2I x H bf16)][W2 (H x I bf16)]; scale sections are empty.
+    FP8 with block scales ("fp8_block"): [W13 E4M3 codes (2I x H)][fp32 scales
+           (ceil(2I/128) x ceil(H/128))][W2 codes (H x I)][scales], row-major,
+           every section padded to 16 bytes; read as it is (no kernel layout).
     Rows 0..I-1 of W13 are the gate projection, rows I..2I-1 the up projection.
     In a code byte the low nibble is the even element along K.
     """
@@ -124,6 +127,15 @@ def blob_layout(H: int, I: int, fmt: str) -> BlobLayout:
         w2 = s13 + 16
         s2 = w2 + H * I
         end = s2 + 16
+    elif fmt == "fp8_block":
+        # one-byte E4M3 codes, one fp32 scale per 128 x 128 block of a matrix
+        def pad16(n):
+            return (n + 15) // 16 * 16
+        w13 = 0
+        s13 = w13 + 2 * I * H
+        w2 = s13 + pad16(-(-2 * I // 128) * -(-H // 128) * 4)
+        s2 = w2 + H * I
+        end = s2 + pad16(-(-H // 128) * -(-I // 128) * 4)
     elif fmt == "bf16":
         w13 = 0
         w2 = 2 * I * H * 2
@@ -232,6 +244,20 @@ def encode_fp8(w: np.ndarray) -> tuple[np.ndarray, np.float32]:
     return _to_e4m3(np.clip(w / g, -448.0, 448.0)), g
 
 
+def encode_fp8_block(w: np.ndarray) -> tuple[np.ndarray, np.ndarray]:
+    """Quantise an fp32 matrix [R][K] to E4M3 codes [R][K] with one fp32 scale
+    per 128 x 128 block (the block's largest magnitude over 448; blocks at the
+    edges are what is left of the matrix)."""
+    R, K = w.shape
+    nr, nk = -(-R // 128), -(-K // 128)
+    full = np.zeros((nr * 128, nk * 128), dtype=np.float32)
+    full[:R, :K] = w
+    b = full.reshape(nr, 128, nk, 128)
+    s = (np.abs(b).max(axis=(1, 3)) / np.float32(448.0)).astype(np.float32)
+    q = b / np.where(s == 0, np.float32(1.0), s)[:, None, :, None]
+    return _to_e4m3(q.reshape(nr * 128, nk * 128)[:R, :K]), s
+
+
 def f32_to_bf16_bits(a: np.ndarray) -> np.ndarray:
     """Round fp32 to bf16 bit patterns (torch's RNE conversion)."""
     import torch
@@ -287,6 +313,17 @@ def _gauss_fp8_blob(rng: np.random.Generator, H: int, I: int, sigma: float) -> n
         c, g = encode_fp8(w)
         out[o_c:o_s] = c.reshape(-1)
         out[o_s:o_end] = _scale_field(g)
+    return out
+
+
+def _gauss_fp8_block_blob(rng: np.random.Generator, H: int, I: int, sigma: float) -> np.ndarray:
+    lay = blob_layout(H, I, "fp8_block")
+    out = np.zeros(lay.nbytes, dtype=np.uint8)
+    for rows, cols, oc, osc in ((2 * I, H, lay.w13, lay.s13), (H, I, lay.w2, lay.s2)):
+        q, s = encode_fp8_block(rng.standard_normal((rows, cols), dtype=np.float32)
+                                * np.float32(sigma))
+        out[oc:oc + rows * cols] = q.reshape(-1)
+        out[osc:osc + s.nbytes] = s.reshape(-1).view(np.uint8)
     return out
 
 
@@ -414,6 +451,8 @@ def expert_blob(cfg: LayerConfig, layer: int, expert: int, shared: bool = False,
         return _gauss_nvfp4_blob(rng, H, I, WEIGHT_SIGMA)
     if cfg.weights == "gauss_fp8":
         return _gauss_fp8_blob(rng, H, I, WEIGHT_SIGMA)
+    if cfg.weights == "gauss_fp8_block":
+        return _gauss_fp8_block_blob(rng, H, I, WEIGHT_SIGMA)
     if cfg.weights == "marginal_nvfp4":
         return _marginal_nvfp4_blob(rng, H, I, WEIGHT_SIGMA)
     if cfg.weights == "marginal_fp8":

@@ -1,0 +1,93 @@
+"""The routed experts of a layer in training: forward and backward in bf16 with
+fp32 sums, from the library's products.
+
+With pairs p = (token t, choice j), expert e, router weight w_p:
+  h_p = W13_e x_t = [g | u],  a_p = w_p silu(g) u,  out_t = sum_j W2_e a_p.
+The weight sits in the activation, so that the tokens' sum and its gradient need
+no weights: dy_p = dout_t, and dw_p = <da_p, silu(g) u> comes with the
+activation's gradient.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib, products as P
+
+
+class TrainExperts:
+    """Buffers and call sequence for at most T_max tokens. ``forward`` keeps what
+    ``backward`` needs: its inputs must be unchanged until then, and one
+    backward belongs to the last forward. Both run on the current stream and
+    allocate nothing, so a training step can be captured into a graph."""
+
+    def __init__(self, H, E, k, I, T_max, device="cuda"):
+        self.H, self.E, self.k, self.I, self.T_max = H, E, k, I, T_max
+        n = max(T_max * k, 1)
+
+        def buf(*shape, dtype=torch.bfloat16):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+        self.offsets = buf(E + 1, dtype=torch.int32)
+        self.sorted_pair, self.pair_row = buf(n, dtype=torch.int32), buf(n, dtype=torch.int32)
+        self.ws_bytes = max(_lib.moe_workspace_size(T_max, k, H, I, E)[0], 256)
+        self.ws = buf(self.ws_bytes, dtype=torch.uint8)
+        self.ones = torch.ones(T_max, k, dtype=torch.float32, device=device)
+        self.h, self.a = buf(n, 2 * I), buf(n, I)
+        self.y, self.out = buf(n, H), buf(T_max, H)
+        self.da, self.dh, self.dx = buf(n, I), buf(n, 2 * I), buf(T_max, H)
+        self.dtopk_w = buf(T_max, k, dtype=torch.float32)
+        self.dw13 = buf(E, 2 * I, H, dtype=torch.float32)
+        self.dw2 = buf(E, H, I, dtype=torch.float32)
+        self._saved = None
+
+    def forward(self, x, topk_ids, topk_w, w13, w2):
+        """out [T, H] bf16 of x [T, H] bf16, the router's topk_ids [T, k] int32
+        (distinct experts of a token) and topk_w [T, k] fp32, w13 [E, 2I, H] and
+        w2 [E, H, I] bf16."""
+        T, k = x.shape[0], self.k
+        if T > self.T_max or x.shape[1] != self.H:
+            raise ValueError(f"x: {tuple(x.shape)}, at most [{self.T_max}, {self.H}]")
+        for t, name, dtype in ((topk_ids, "topk_ids", torch.int32), (topk_w, "topk_w", torch.float32)):
+            if t.shape != (T, k) or t.dtype != dtype or not t.is_contiguous() or t.device != x.device:
+                raise ValueError(f"{name}: contiguous {dtype} [{T}, {k}] on {x.device} is needed")
+        if w13.shape != (self.E, 2 * self.I, self.H) or w2.shape != (self.E, self.H, self.I):
+            raise ValueError(f"w13, w2: {tuple(w13.shape)}, {tuple(w2.shape)}")
+        n = T * k
+        self._saved = (x, topk_w, w13, w2)
+        if T == 0:
+            return self.out[:0]
+        pair, off = self.sorted_pair[:n], self.offsets
+        _lib.moe_permute(topk_ids, T, k, self.E, off, self.sorted_pair, self.pair_row, self.ws,
+                         self.ws_bytes)
+        P.grouped_matmul(x, w13, off, rows=pair, div=k, out=self.h[:n])
+        P.swiglu(self.h[:n], topk_w, pair, off[self.E:], out=self.a[:n])
+        P.grouped_matmul(self.a[:n], w2, off, out_rows=pair, out=self.y[:n])
+        _lib.moe_combine(self.y, False, self.ones, None, T, k, self.H, self.out)
+        return self.out[:T]
+
+    def backward(self, dout, accumulate=False):
+        """(dx [T, H] bf16, dtopk_w [T, k] fp32, dw13, dw2 fp32) of the last
+        forward for dout [T, H] bf16; with ``accumulate`` the matrices' gradients
+        are added to what dw13 and dw2 hold."""
+        if self._saved is None:
+            raise RuntimeError("backward without a forward")
+        x, topk_w, w13, w2 = self._saved
+        T, k = x.shape[0], self.k
+        if dout.shape != x.shape:
+            raise ValueError(f"dout: {tuple(dout.shape)}, {tuple(x.shape)} is needed")
+        n = T * k
+        if T == 0:
+            if not accumulate:
+                self.dw13.zero_(), self.dw2.zero_()
+            return self.dx[:0], self.dtopk_w[:0], self.dw13, self.dw2
+        pair, off = self.sorted_pair[:n], self.offsets
+        da, dh, dxp = self.da[:n], self.dh[:n], self.y[:n]
+        P.grouped_matmul_dx(dout, w2, off, rows=pair, div=k, out=da)
+        P.grouped_matmul_dw(dout, self.a[:n], off, dy_rows=pair, dy_div=k, out=self.dw2,
+                            accumulate=accumulate)
+        P.swiglu_grad(self.h[:n], da, topk_w.view(-1), pair, off[self.E:], dh=dh,
+                      dw=self.dtopk_w[:T].view(-1))
+        P.grouped_matmul_dx(dh, w13, off, out_rows=pair, out=dxp)
+        _lib.moe_combine(dxp, False, self.ones, None, T, k, self.H, self.dx)
+        P.grouped_matmul_dw(dh, x, off, x_rows=pair, x_div=k, out=self.dw13, accumulate=accumulate)
+        return self.dx[:T], self.dtopk_w[:T], self.dw13, self.dw2

@@ -69,3 +69,22 @@ def test_permute_split(lib, orc, T, E, k, seed):
         assert np.array_equal(h_p, np.concatenate(
             [sp[off[e]:off[e + 1]] for e in range(E) if mask[e]] + [np.zeros(0, np.int32)]))
         assert sorted(np.concatenate([d_sp, h_p]).tolist()) == list(range(T * k))
+
+
+def test_fp8_block_blob_layout_and_codes():
+    """Sections on 16 bytes without overlap; codes times scales within half an
+    E4M3 step (2^-4 of a value, or 2^-10 of the scale) of the matrix."""
+    for H, I in ((32, 32), (256, 128), (160, 96), (2048, 768)):
+        lay = synth.blob_layout(H, I, "fp8_block")
+        blocks = [-(-2 * I // 128) * -(-H // 128), -(-H // 128) * -(-I // 128)]
+        assert lay.s13 == 2 * I * H and lay.w2 >= lay.s13 + 4 * blocks[0]
+        assert lay.s2 == lay.w2 + H * I and lay.nbytes >= lay.s2 + 4 * blocks[1]
+        assert all(v % 16 == 0 for v in (lay.s13, lay.w2, lay.s2, lay.nbytes))
+    rng = np.random.default_rng(0)
+    w = rng.standard_normal((200, 300)).astype(np.float32)
+    w[128:, 256:] = 0
+    q, s = synth.encode_fp8_block(w)
+    assert q.shape == w.shape and s.shape == (2, 3) and s[1, 2] == 0
+    wide = np.repeat(np.repeat(s, 128, 0)[:200], 128, 1)[:, :300]
+    err = np.abs(synth._from_e4m3(q) * wide - w)
+    assert (err <= np.abs(w) * 2.0 ** -4 + wide * 2.0 ** -10).all()
