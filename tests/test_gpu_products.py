@@ -92,6 +92,8 @@ SHAPES = [
     ([2] * 100 + [0] * 50, 128, 384),
     ([1000, 3], 1536, 512),
     ([150, 61, 0, 97] * 14, 768, 768),
+    ([0, 40, 1, 16, 17, 0, 3] + [0] * 9, 136, 4672),
+    ([60, 0, 2, 16] + [1] * 20, 208, 2240),
     ([1300, 513, 1, 900, 1255], 2056, 1168),
     ([1300, 513, 1, 900, 1255], 1160, 2064),
 ]
