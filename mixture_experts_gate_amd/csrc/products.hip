@@ -52,7 +52,8 @@ struct TileLds {
     int src[kBP];         // source row of each LDS row of p (forward, dx)
     int dst[kBP];         // row of out, or -1
     float xs[4][kBP];     // FP8: scales of the p rows, by step
-    int rows[4][2][64];   // dw: source rows of dy and x, by step
+    int raw[4][2][64];    // dw: indices of the rows of dy and x, by step,
+    int rows[4][2][64];   // and the rows
     int base[kMaxE + 1];  // p tiles before each expert
     int wsum[8];
 };
@@ -128,12 +129,13 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
                 L.src[t] = s < 0 ? 0 : s;
                 L.dst[t] = d;
             }
-        } else if (t < 128) {
+        } else if (w < 2 && cnt > 0) {
+            const RowsIn &in = w == 0 ? A.a : A.b;
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                const int c = 64 * k + l;
-                L.rows[k][w][l] = c < cnt ? source_row(w == 0 ? A.a : A.b, lo + c) : -1;
-            }
+            for (int k = 0; k < 4; ++k) copy_indices(in, 64 * k, lo, cnt, L.raw[k][w]);
+            wait_copies<0>();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) rows_from_indices(in, 64 * k, lo, cnt, L.raw[k][w], L.rows[k][w]);
         }
         __syncthreads();
 
@@ -160,6 +162,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
             } else {
                 po[0] = 2 * (p0 + 8 * tchunk < A.N ? p0 + 8 * tchunk : 0);
             }
+
             if (!kQT) {
                 const int rr = 8 * w + (l >> 3);
                 qo = (uint32_t)(perm64<MODE>(rr >> 4, rr & 15) * ldq) + 16 * chunk;
@@ -167,6 +170,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
                 const int col = q0 + 8 * tchunk < Qn ? q0 + 8 * tchunk : 0;
                 qo = (MODE == kDx ? (uint32_t)(tc * ldq) : 0) + 2 * col;
             }
+            if (kDwMode) po[1] = (uint32_t)((l >> 5) * lda) + po[0], po[2] = (uint32_t)((l >> 5) * ldq) + qo;
         }
         const float *ws = nullptr;
         uint32_t xo = 0;         // this thread's row of the scales of a
@@ -178,11 +182,8 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
 
         // copy i of 4 of step k, operands P and Q
         auto copy_p = [&](int i, int k, bool fast) {
-            char *const to = L.p[k & 1] + (kDwMode ? (16 * i + 2 * w) * 512 : (prow + 32 * i) * 128);
-            if (kDwMode) {
-                const int fl = fresh_lane(), s = L.rows[k & 3][0][16 * i + 2 * w + (fl >> 5)];
-                copy_or_zeros(s >= 0, A.a.base + (size_t)s * lda + po[0], to);
-            } else if (fast) {
+            char *const to = L.p[k & 1] + (prow + 32 * i) * 128;
+            if (fast) {
                 lds_dma16(scalar_base(A.a.base + (size_t)k * 128) + here(po[i]), to);
             } else {
                 const int fl = fresh_lane(), chunk = (fl & 7) ^ (fl >> 3);
@@ -193,10 +194,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
         };
         auto copy_q = [&](int i, int k, bool fast) {
             char *const to = L.q[k & 1] + (kQT ? (16 * i + 2 * w) * 512 : (64 * i + 8 * w) * 128);
-            if (kDwMode) {
-                const int fl = fresh_lane(), s = L.rows[k & 3][1][16 * i + 2 * w + (fl >> 5)];
-                copy_or_zeros(s >= 0, qb + (size_t)s * ldq + qo, to);
-            } else if (MODE == kDx) {
+            if (MODE == kDx) {
                 const char *const from = scalar_base(qb + (size_t)(k * CK + 16 * i) * ldq) + here(qo);
                 if (fast) lds_dma16(from, to);
                 else copy_or_zeros(k * CK + 16 * i + 2 * w + (fresh_lane() >> 5) < C, from, to);
@@ -210,6 +208,16 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
                               to);
             }
         };
+        // dw: copies i and i + 1 of both
+        auto copy_both = [&](int i, int k) {
+            const bool full = 64 * (k + 1) <= cnt;
+            const int c = 16 * i + 2 * w, fl = fresh_lane();
+            const size_t first = (size_t)(lo + 64 * k + c);
+            copy_rows<2, 512>(full && !A.a.idx, A.a, first, lda, po[1], po[0], &L.rows[k & 3][0][c + (fl >> 5)],
+                              L.p[k & 1] + c * 512);
+            copy_rows<2, 512>(full && !A.b.idx, A.b, first, ldq, po[2], qo, &L.rows[k & 3][1][c + (fl >> 5)],
+                              L.q[k & 1] + c * 512);
+        };
         auto copy_xs = [&](int k) {
             if (MODE == kFwdFp8 && w < kBP / kWave)
                 lds_dma4(A.a_s + (size_t)here(xo) * KB + k, &L.xs[k & 3][64 * w]);
@@ -220,14 +228,6 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
-        auto frag_q = [&](const char *buf, int j, int s) {
-            return kQT ? frag_t<kDwMode>(buf, 512, wq, j, s, g, r) : frag_n(buf, 64 * wq + 16 * j, s, g, r);
-        };
-        auto frag_p = [&](const char *buf, int i, int s) {
-            return kDwMode ? frag_t<kDwMode>(buf, 512, 2 * wp + (i >> 2), i & 3, s, g, r)
-                           : frag_n(buf, 128 * wp + 16 * i, s, g, r);
-        };
 
         // A step is two clusters of 32 matrix instructions; cluster 0 / 1 takes
         // the first / second 64 p rows of the wavefront with all of q (dw: all
@@ -245,7 +245,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
         // copies issued since may stay in flight.
         auto first = [&](int k, bool fast) {      // 6 copies (dw: 4)
             if (kDwMode) {
-                copy_p(0, k, fast), copy_q(0, k, fast), copy_p(1, k, fast), copy_q(1, k, fast);
+                copy_both(0, k);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) copy_q(i, k, fast);
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
             }
         };
         auto second = [&](int k, bool fast) {     // 2 copies (dw: 4)
-            if (kDwMode) copy_p(2, k, fast), copy_q(2, k, fast), copy_p(3, k, fast), copy_q(3, k, fast);
+            if (kDwMode) copy_both(2, k);
             else copy_p(2, k, fast), copy_p(3, k, fast);
         };
         auto copy_first = [&](int k) {
@@ -281,37 +281,63 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
         for (int k = 0; k < steps; ++k) {
             const char *const bp = L.p[k & 1], *const bq = L.q[k & 1];
             constexpr int NF = kDwMode ? 8 : 4;      // p fragments of a cluster
-            u32x4 qf[4][2], pf[NF][2];
+            u32x4 qf[2][4], pf[NF][2];
             float sc[4] = {0, 0, 0, 0};
             const float wsk = MODE == kFwdFp8 ? as_scalar(ws)[k] : 0.0f;
-            int next = -1;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const bool work0 = nc > 2 * c, work1 = nc > 2 * c + 1;   // 32 rows each
-                if (kDwMode) {
+                // indices of step k + 4, which land by the next step's first wait, and
+                // the rows of step k + 3, for the copies of the next step's cluster 1
+                if (kDwMode && w < 2) {
+                    const RowsIn &in = w == 0 ? A.a : A.b;
+                    if (c == 0 && k + 4 < steps) copy_indices(in, 64 * (k + 4), lo, cnt, L.raw[k & 3][w]);
+                    if (c == 1 && k > 0 && k + 3 < steps)
+                        rows_from_indices(in, 64 * (k + 3), lo, cnt, L.raw[(k + 3) & 3][w], L.rows[(k + 3) & 3][w]);
+                }
+                auto read = [&]() {
+                uint32_t qa[4], pa[4];
+                if (kQT && (kDwMode || c == 0))
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) qf[j][0] = frag_q(bq, j, c);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) pf[i % NF][0] = frag_p(bp, i, c);
-                    // rows of step k + 3
-                    if (w < 2 && c == 0) {
-                        const int cc = 64 * (k + 3) + l;
-                        if (cc < cnt) next = source_row(w == 0 ? A.a : A.b, lo + cc);
+                    for (int j = 0; j < 4; ++j) {
+                        qa[j] = frag_t_at<kDwMode, 512>(bq, wq, j, g, r);
+                        if (kDwMode) pa[j] = frag_t_at<kDwMode, 512>(bp, 2 * wp, j, g, r);
                     }
-                    if (w < 2 && c == 1) L.rows[(k + 3) & 3][w][l] = next;
+                if (kDwMode) {
+                    u32x4 p0f[4], p1f[4];
+                    if (c == 0) {
+                        frags_t<512, 0>(qa, qf[0]);
+                        frags_t2<512, 0, 128>(pa, p0f, p1f);
+                    } else {
+                        frags_t<512, 32 * 512>(qa, qf[0]);
+                        frags_t2<512, 32 * 512, 32 * 512 + 128>(pa, p0f, p1f);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) pf[i][0] = p0f[i], pf[(4 + i) % NF][0] = p1f[i];
                 } else {
                     if (c == 0) {
+                        if (kQT) {
+                            frags_t2<512, 0, 32 * 512>(qa, qf[0], qf[1]);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) qf[j][0] = frag_q(bq, j, 0), qf[j][1] = frag_q(bq, j, 1);
+                            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                for (int s = 0; s < 2; ++s)
+                                    qf[s][j] = frag_n(bq, 64 * wq + 16 * j, s, g, r);
+                        }
                     }
                     if (work0) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            pf[i][0] = frag_p(bp, 4 * c + i, 0), pf[i][1] = frag_p(bp, 4 * c + i, 1);
+                            pf[i][0] = frag_n(bp, 128 * wp + 64 * c + 16 * i, 0, g, r);
+                            pf[i][1] = frag_n(bp, 128 * wp + 64 * c + 16 * i, 1, g, r);
                             if (MODE == kFwdFp8) sc[i] = L.xs[k & 3][128 * wp + 64 * c + 16 * i + r] * wsk;
                         }
                     }
                 }
+                };
+                // (the transposing reads wait where they stand: the copies go first)
+                if (!kQT) read();
                 if (c == 0) {
                     if (k + 1 < steps) {
                         copy_second(k + 1);
@@ -329,6 +355,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
                         wait_copies<0>();
                     }
                 }
+                if (kQT) read();
                 wait_lds();
                 phase_barrier();
                 __builtin_amdgcn_s_setprio(1);
@@ -338,7 +365,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                as_bf16x8(pf[i % NF][0]), as_bf16x8(qf[j][0]), acc[i][j], 0, 0, 0);
+                                as_bf16x8(pf[i % NF][0]), as_bf16x8(qf[0][j]), acc[i][j], 0, 0, 0);
                 } else {
                     auto multiply = [&](int i0) {     // p tiles i0, i0 + 1 of the cluster
                         if (MODE == kFwdFp8) {
@@ -348,7 +375,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)
                                     part[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                        as_i32x8(qf[j][0], qf[j][1]),
+                                        as_i32x8(qf[0][j], qf[1][j]),
                                         as_i32x8(pf[(i0 + i) % NF][0], pf[(i0 + i) % NF][1]),
                                         f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
 #pragma unroll
@@ -367,8 +394,8 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
 #pragma unroll
                                     for (int j = 0; j < 4; ++j)
                                         acc[4 * c + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                            as_bf16x8(q_is_row(MODE) ? qf[j][s] : pf[i % NF][s]),
-                                            as_bf16x8(q_is_row(MODE) ? pf[i % NF][s] : qf[j][s]),
+                                            as_bf16x8(q_is_row(MODE) ? qf[s][j] : pf[i % NF][s]),
+                                            as_bf16x8(q_is_row(MODE) ? pf[i % NF][s] : qf[s][j]),
                                             acc[4 * c + i][j], 0, 0, 0);
                         }
                     };

@@ -81,13 +81,16 @@ __device__ __forceinline__ void group_of_lane(const ProductArgs &a, int e, int &
     cnt = hi > lo ? hi - lo : 0;
 }
 
-// Source row of sorted row i, or -1 where the index is not a row of r.
+// The row that index v stands for, or -1 where it is not a row of r.
+__device__ __forceinline__ int row_of_index(const RowsIn &r, int v) {
+    const uint32_t u = (uint32_t)v;
+    const int q = (int)(r.mul ? __umulhi(u, r.mul) >> r.shift : u);
+    return v >= 0 && q < r.n ? q : -1;
+}
+
+// Source row of sorted row i, or -1.
 __device__ __forceinline__ int source_row(const RowsIn &r, int i) {
-    if (!r.idx) return i;
-    int v = r.idx[i];
-    if (v < 0) return -1;
-    if (r.mul) v = (int)(__umulhi((uint32_t)v, r.mul) >> r.shift);
-    return v < r.n ? v : -1;
+    return r.idx ? row_of_index(r, r.idx[i]) : i;
 }
 
 __device__ __forceinline__ const char *mat_of(const ProductArgs &a, int e, int elem) {
@@ -125,6 +128,42 @@ __device__ __forceinline__ const char *scalar_base(const char *p) {
 __device__ __forceinline__ uint32_t here(uint32_t o) {
     asm volatile("" : "+v"(o));
     return o;
+}
+
+// dw: the indices of 64 rows of sorted order from lo + c, of an expert's cnt, go
+// into LDS by a copy (through a register, the wait for one would be a wait for
+// every copy issued before it), and a step later one lane a row makes them the
+// rows' numbers, -1 past the last one.
+__device__ __forceinline__ void copy_indices(const RowsIn &r, int c, int lo, int cnt, int *to) {
+    const int i = c + lane_id();
+    if (r.idx) lds_dma4(r.idx + lo + (i < cnt ? i : cnt - 1), to);
+}
+
+__device__ __forceinline__ void rows_from_indices(const RowsIn &r, int c, int lo, int cnt, const int *raw,
+                                                  int *rows) {
+    const int l = lane_id();
+    const int row = r.idx ? row_of_index(r, raw[l]) : lo + c + l;
+    rows[l] = c + l < cnt ? row : -1;
+}
+
+// dw: N copies of one operand, 16 rows of a step apart: rows in place that all
+// exist (a uniform base and a lane's offset), or the rows that `rows` lists (-1:
+// zeros). One branch for all: a branch a copy took as long as the multiplications.
+template <int N, int STRIDE>
+__device__ __forceinline__ void copy_rows(bool in_place, const RowsIn &r, size_t first, size_t ld, uint32_t off,
+                                          uint32_t col, const int *rows, char *to) {
+    if (in_place) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            lds_dma16(scalar_base(r.base + (first + 16 * i) * ld) + here(off), to + 16 * i * STRIDE);
+    } else {
+        int row[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) row[i] = rows[16 * i];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            copy_or_zeros(row[i] >= 0, r.base + (size_t)(uint32_t)row[i] * ld + col, to + 16 * i * STRIDE);
+    }
 }
 
 // This lane's index, which the compiler takes for a new value.
@@ -196,26 +235,82 @@ __device__ __forceinline__ void place_of(int li, int mp, int tq, int &p, int &q)
     p = gi * gp + rest - q * gl;
 }
 
-typedef __attribute__((ext_vector_type(4))) short s16x4;
-typedef __attribute__((ext_vector_type(8))) short s16x8;
-
 // Fragments of a matrix instruction from LDS, lane (g, r) = (l / 16, l % 16): 8
-// consecutive c (16 bytes), half s of a step, of
-//   row `row` + r of c-contiguous data (rows of 128 bytes, chunks XORed with the row), or
-//   tile j of 64-column block blk of c-major data with rows of `stride` bytes
-//   (dw: columns 16 j + 0..15).
+// consecutive c (16 bytes), half s of a step.
+// Row `row` + r of c-contiguous data (rows of 128 bytes, chunks XORed with the row):
 __device__ __forceinline__ u32x4 frag_n(const char *buf, int row, int s, int g, int r) {
     return *(const MOE_LDS u32x4 *)(buf + (row + r) * 128 + (((4 * s + g) ^ (r & 7)) << 4));
 }
-template <bool DW>
-__device__ __forceinline__ u32x4 frag_t(const char *buf, int stride, int blk, int j, int s, int g, int r) {
+
+// Tile j of 64-column block blk of c-major data with rows of STRIDE bytes (dw:
+// columns 16 j + 0..15): the address of its first transposing read in half 0; the
+// second is 4 rows on, half 1 32 rows, the next block 128 bytes.
+template <bool DW, int STRIDE>
+__device__ __forceinline__ uint32_t frag_t_at(const char *buf, int blk, int j, int g, int r) {
     const int ci = r >> 2, tt = r & 3;
     const int ch = (DW ? 8 * blk + 2 * j + (tt >> 1) : 8 * blk + 2 * tt + (j >> 1)) ^ t_key<DW>(ci);
-    const char *a = buf + (32 * s + 8 * g + ci) * stride + ch * 16 + (DW ? tt & 1 : j & 1) * 8;
-    const s16x4 lo4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4 *)(a));
-    const s16x4 hi4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4 *)(a + 4 * stride));
-    const s16x8 v = {lo4[0], lo4[1], lo4[2], lo4[3], hi4[0], hi4[1], hi4[2], hi4[3]};
-    return __builtin_bit_cast(u32x4, v);
+    const char *const a = buf + (8 * g + ci) * STRIDE + ch * 16 + (DW ? tt & 1 : j & 1) * 8;
+    return (uint32_t)(uintptr_t)(const MOE_LDS char *)a;
+}
+
+// The fragments of the four tiles at `at`, OFF bytes on. The reads and their wait
+// are one block of assembly: for the builtin the compiler waits until every copy
+// into LDS has landed, also those of later steps.
+template <int STRIDE, int OFF>
+__device__ __forceinline__ void frags_t(const uint32_t (&at)[4], u32x4 (&f)[4]) {
+    typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+    u32x2 a0, a1, b0, b1, c0, c1, d0, d1;
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %8 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %2, %9 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %4, %10 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %6, %11 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(a0), "=&v"(a1), "=&v"(b0), "=&v"(b1), "=&v"(c0), "=&v"(c1), "=&v"(d0), "=&v"(d1)
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(OFF), "n"(OFF + 4 * STRIDE)
+        : "memory");
+    f[0] = u32x4{a0[0], a0[1], a1[0], a1[1]}, f[1] = u32x4{b0[0], b0[1], b1[0], b1[1]};
+    f[2] = u32x4{c0[0], c0[1], c1[0], c1[1]}, f[3] = u32x4{d0[0], d0[1], d1[0], d1[1]};
+}
+
+// Two such groups (OFF0, OFF1) with one wait.
+template <int STRIDE, int OFF0, int OFF1>
+__device__ __forceinline__ void frags_t2(const uint32_t (&at)[4], u32x4 (&f)[4], u32x4 (&h)[4]) {
+    typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+    u32x2 v[16];
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %16 offset:%20\n\t"
+        "ds_read_b64_tr_b16 %1, %16 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %2, %17 offset:%20\n\t"
+        "ds_read_b64_tr_b16 %3, %17 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %4, %18 offset:%20\n\t"
+        "ds_read_b64_tr_b16 %5, %18 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %6, %19 offset:%20\n\t"
+        "ds_read_b64_tr_b16 %7, %19 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %8, %16 offset:%22\n\t"
+        "ds_read_b64_tr_b16 %9, %16 offset:%23\n\t"
+        "ds_read_b64_tr_b16 %10, %17 offset:%22\n\t"
+        "ds_read_b64_tr_b16 %11, %17 offset:%23\n\t"
+        "ds_read_b64_tr_b16 %12, %18 offset:%22\n\t"
+        "ds_read_b64_tr_b16 %13, %18 offset:%23\n\t"
+        "ds_read_b64_tr_b16 %14, %19 offset:%22\n\t"
+        "ds_read_b64_tr_b16 %15, %19 offset:%23\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]),
+          "=&v"(v[7]), "=&v"(v[8]), "=&v"(v[9]), "=&v"(v[10]), "=&v"(v[11]), "=&v"(v[12]), "=&v"(v[13]),
+          "=&v"(v[14]), "=&v"(v[15])
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(OFF0), "n"(OFF0 + 4 * STRIDE), "n"(OFF1),
+          "n"(OFF1 + 4 * STRIDE)
+        : "memory");
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[j] = u32x4{v[2 * j][0], v[2 * j][1], v[2 * j + 1][0], v[2 * j + 1][1]};
+        h[j] = u32x4{v[8 + 2 * j][0], v[8 + 2 * j][1], v[9 + 2 * j][0], v[9 + 2 * j][1]};
+    }
 }
 
 // p tiles before each expert (base[0 .. E]), for tiles of bp rows; by all THREADS

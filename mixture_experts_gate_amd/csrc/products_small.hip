@@ -18,7 +18,8 @@ struct SmallLds {
     int src[kT];              // source row of each LDS row of p (forward, dx)
     int dst[kT];              // row of out, or -1
     float xs[S][kT];          // FP8: scales of the p rows, by step
-    int rows[S + 1][2][64];   // dw: source rows of dy and x, by step
+    int raw[S + 3][2][64];    // dw: indices of the rows of dy and x, by step,
+    int rows[S + 3][2][64];   // and the rows
     int base[kMaxE + 1];  // p tiles before each expert
     int wsum[4];
 };
@@ -89,12 +90,13 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
                 L.src[t] = s < 0 ? 0 : s;
                 L.dst[t] = d;
             }
-        } else if (t < 128) {
+        } else if (w < 2 && cnt > 0) {
+            const RowsIn &in = w == 0 ? A.a : A.b;
 #pragma unroll
-            for (int k = 0; k < S; ++k) {
-                const int c = 64 * k + l;
-                L.rows[k][w][l] = c < cnt ? source_row(w == 0 ? A.a : A.b, lo + c) : -1;
-            }
+            for (int k = 0; k < S + 2; ++k) copy_indices(in, 64 * k, lo, cnt, L.raw[k][w]);
+            wait_copies<0>();
+#pragma unroll
+            for (int k = 0; k < S + 2; ++k) rows_from_indices(in, 64 * k, lo, cnt, L.raw[k][w], L.rows[k][w]);
         }
         __syncthreads();
 
@@ -125,26 +127,31 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
         auto fetch = [&](int k) {
             char *const P = L.p[k % S], *const Q = L.q[k % S];
             const bool full = (k + 1) * CK <= C;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                char *const tn = P + (32 * i + 8 * w) * 128, *const tt = P + (16 * i + 4 * w) * 256;
-                if (kDwMode) {
-                    const int s = L.rows[k % (S + 1)][0][16 * i + tc];
-                    copy_or_zeros(s >= 0, A.a.base + (size_t)s * lda + pcol, tt);
-                } else {
-                    copy_or_zeros(full || k * CK + chunk * (16 / ES) < C, pp[i] + (size_t)k * 128, tn);
-                }
+            if (kDwMode) {
+                const size_t first = (size_t)(lo + 64 * k + 4 * w);
+                copy_rows<4, 256>(full && !A.a.idx, A.a, first, lda, (uint32_t)((l >> 4) * lda + pcol),
+                                  (uint32_t)pcol, &L.rows[k % (S + 3)][0][tc], P + 4 * w * 256);
+                copy_rows<4, 256>(full && !A.b.idx, A.b, first, ldq, (uint32_t)((l >> 4) * ldq + qcol),
+                                  (uint32_t)qcol, &L.rows[k % (S + 3)][1][tc], Q + 4 * w * 256);
+                return;
             }
+            if (full) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                char *const tn = Q + (32 * i + 8 * w) * 128, *const tt = Q + (16 * i + 4 * w) * 256;
-                if (kDwMode) {
-                    const int s = L.rows[k % (S + 1)][1][16 * i + tc];
-                    copy_or_zeros(s >= 0, mat + (size_t)s * ldq + qcol, tt);
-                } else if (MODE == kDx) {
-                    copy_or_zeros(full || k * CK + 16 * i + tc < C, qp[i] + (size_t)k * CK * ldq, tt);
-                } else {
-                    copy_or_zeros(full || k * CK + chunk * (16 / ES) < C, qp[i] + (size_t)k * 128, tn);
+                for (int i = 0; i < 4; ++i) {
+                    lds_dma16(pp[i] + (size_t)k * 128, P + (32 * i + 8 * w) * 128);
+                    if (MODE == kDx) lds_dma16(qp[i] + (size_t)k * CK * ldq, Q + (16 * i + 4 * w) * 256);
+                    else lds_dma16(qp[i] + (size_t)k * 128, Q + (32 * i + 8 * w) * 128);
+                }
+            } else {
+                const bool in = k * CK + chunk * (16 / ES) < C;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    copy_or_zeros(in, pp[i] + (size_t)k * 128, P + (32 * i + 8 * w) * 128);
+                    if (MODE == kDx)
+                        copy_or_zeros(k * CK + 16 * i + tc < C, qp[i] + (size_t)k * CK * ldq,
+                                      Q + (16 * i + 4 * w) * 256);
+                    else
+                        copy_or_zeros(in, qp[i] + (size_t)k * 128, Q + (32 * i + 8 * w) * 128);
                 }
             }
             if (MODE == kFwdFp8 && w < 2)
@@ -156,20 +163,15 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-        int next = -1;      // dw: a source row of step k + S
-        auto look = [&](int k) {
-            if (kDwMode && t < 128) {
-                next = -1;
-                if (64 * k + l < cnt) next = source_row(w == 0 ? A.a : A.b, lo + 64 * k + l);
-            }
-        };
 #pragma unroll
         for (int k = 0; k < S - 1; ++k)
             if (k < steps) fetch(k);
         for (int k = 0; k < steps; ++k) {
             if (S == 1) fetch(k);
             const char *const bp = L.p[k % S], *const bq = L.q[k % S];
-            look(k + S);
+            // the indices of step k + S + 2, which have landed by the wait of step k + 2
+            if (kDwMode && w < 2 && k + S + 2 < steps)
+                copy_indices(w == 0 ? A.a : A.b, 64 * (k + S + 2), lo, cnt, L.raw[(k + S + 2) % (S + 3)][w]);
             // step k is in LDS (of the S - 2 steps after it, those copied may be in
             // flight), and step k - 1 is read
             const int later = steps - 1 - k < S - 2 ? steps - 1 - k : S - 2;
@@ -178,7 +180,10 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
             else wait_copies<0>();
             wait_lds();
             bare_barrier();
-            if (kDwMode && t < 128) L.rows[(k + S) % (S + 1)][w][l] = next;
+            // the rows of step k + S, for the next step's copies
+            if (kDwMode && w < 2 && k >= 2 && k + S < steps)
+                rows_from_indices(w == 0 ? A.a : A.b, 64 * (k + S), lo, cnt, L.raw[(k + S) % (S + 3)][w],
+                                  L.rows[(k + S) % (S + 3)][w]);
             if (S > 1 && k + S - 1 < steps) fetch(k + S - 1);
             const float wsk = MODE == kFwdFp8 ? as_scalar(ws)[k] : 0.0f;
             if (MODE == kFwdFp8) {
@@ -201,26 +206,46 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
                     }
                 }
             } else {
+                // the transposing reads: with one wait for both halves, or (S = 1, whose
+                // registers are few) one for each
+                constexpr int H = S > 1 ? 2 : 1;
+                u32x4 qf[H][4], pf[H][4];
+                uint32_t qa[4], pa[4];
+                if (kQT)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) qa[j] = frag_t_at<kDwMode, 256>(bq, wq, j, g, r);
+                if (kDwMode)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) pa[j] = frag_t_at<kDwMode, 256>(bp, wp, j, g, r);
+                if (kQT && S > 1) frags_t2<256, 0, 32 * 256>(qa, qf[0], qf[H - 1]);
+                if (kDwMode && S > 1) frags_t2<256, 0, 32 * 256>(pa, pf[0], pf[H - 1]);
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    bf16x8 qf[4];
+                    if (kQT && S == 1) {
+                        if (s == 0) frags_t<256, 0>(qa, qf[0]);
+                        else frags_t<256, 32 * 256>(qa, qf[0]);
+                    }
+                    if (kDwMode && S == 1) {
+                        if (s == 0) frags_t<256, 0>(pa, pf[0]);
+                        else frags_t<256, 32 * 256>(pa, pf[0]);
+                    }
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        qf[j] = as_bf16x8(kQT ? frag_t<kDwMode>(bq, 256, wq, j, s, g, r)
-                                              : frag_n(bq, 64 * wq + 16 * j, s, g, r));
+                        if (!kQT) qf[s % H][j] = frag_n(bq, 64 * wq + 16 * j, s, g, r);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (i >= np) continue;
-                        const bf16x8 pf = as_bf16x8(kDwMode ? frag_t<kDwMode>(bp, 256, wp, i, s, g, r)
-                                                            : frag_n(bp, 64 * wp + 16 * i, s, g, r));
+                        if (!kDwMode) pf[s % H][i] = frag_n(bp, 64 * wp + 16 * i, s, g, r);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[i][j] = q_is_row(MODE)
-                                            ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[j], pf, acc[i][j], 0, 0, 0)
-                                            : __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf, qf[j], acc[i][j], 0, 0, 0);
+                        for (int j = 0; j < 4; ++j) {
+                            const bf16x8 p = as_bf16x8(pf[s % H][i]), q = as_bf16x8(qf[s % H][j]);
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                q_is_row(MODE) ? q : p, q_is_row(MODE) ? p : q, acc[i][j], 0, 0, 0);
+                        }
                     }
                 }
             }
+
             if (S == 1) {
                 wait_lds();
                 bare_barrier();     // the step is read
