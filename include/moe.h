@@ -444,8 +444,17 @@ int moe_timing_query(int kernel_id, long long *launches, double *total_ms);
  * of the two is given. Matrices and rows start 16-byte aligned.
  * Sums are fp32. Results do not depend on timing: the same call gives the same
  * bits. All sizes 1 <= E <= 512; R = 0 does nothing (dw writes its zeros).
- * Neither these calls nor the ones after them need a workspace. */
+ * ws (16-byte aligned, may be NULL): with at least the bytes that
+ * moe_grouped_gemm_workspace gives, a call with few output tiles and a long
+ * sum cuts the sum into parts and adds them in a second launch (fp32, in a
+ * fixed order); with less it runs whole. Calls that may overlap need
+ * workspaces of their own. */
 enum { MOE_MAT_W13 = 0, MOE_MAT_W2 = 1 };
+
+/* moe_grouped_gemm_workspace -- (host) bytes of workspace that a product of
+ * these sizes can use, often 0; kind: MOE_GEMM_*. */
+enum { MOE_GEMM_BF16 = 0, MOE_GEMM_FP8 = 1, MOE_GEMM_DX = 2, MOE_GEMM_DW = 3 };
+int moe_grouped_gemm_workspace(int kind, int R, int N, int K, int E, size_t *bytes);
 
 /* moe_grouped_gemm -- y[i] = W_e x[i] for every row i of sorted order and its
  * expert e: x [x_n][K] bf16, y [y_n][N] bf16 (y_is_fp32 = 0, rounded once) or
@@ -453,7 +462,7 @@ enum { MOE_MAT_W13 = 0, MOE_MAT_W2 = 1 };
 int moe_grouped_gemm(const uint16_t *x_bf16, const int32_t *x_rows, int x_div, int x_n,
                      const int32_t *offsets, const uint16_t *w_bf16, const moe_expert_w *experts,
                      int mat, int R, int N, int K, int E, void *y, const int32_t *y_rows, int y_n,
-                     int y_is_fp32, void *stream);
+                     int y_is_fp32, void *ws, size_t ws_bytes, void *stream);
 
 /* moe_grouped_gemm_dx -- the product's gradient by its rows: dx[i] = W_e^T
  * dy[i]; dy [dy_n][N] bf16, dx [dx_n][K] bf16 or fp32. (Tokens read by several
@@ -462,7 +471,8 @@ int moe_grouped_gemm(const uint16_t *x_bf16, const int32_t *x_rows, int x_div, i
 int moe_grouped_gemm_dx(const uint16_t *dy_bf16, const int32_t *dy_rows, int dy_div, int dy_n,
                         const int32_t *offsets, const uint16_t *w_bf16,
                         const moe_expert_w *experts, int mat, int R, int N, int K, int E, void *dx,
-                        const int32_t *dx_rows, int dx_n, int dx_is_fp32, void *stream);
+                        const int32_t *dx_rows, int dx_n, int dx_is_fp32, void *ws,
+                        size_t ws_bytes, void *stream);
 
 /* moe_grouped_gemm_dw -- the product's gradient by its matrices: dw_e = sum
  * over the expert's rows i of dy[i] x[i]^T; dy [dy_n][N], x [x_n][K] bf16, dw
@@ -471,7 +481,7 @@ int moe_grouped_gemm_dx(const uint16_t *dy_bf16, const int32_t *dy_rows, int dy_
 int moe_grouped_gemm_dw(const uint16_t *dy_bf16, const int32_t *dy_rows, int dy_div, int dy_n,
                         const uint16_t *x_bf16, const int32_t *x_rows, int x_div, int x_n,
                         const int32_t *offsets, int R, int N, int K, int E, void *dw,
-                        int dw_is_fp32, int accumulate, void *stream);
+                        int dw_is_fp32, int accumulate, void *ws, size_t ws_bytes, void *stream);
 
 /* moe_grouped_gemm_fp8 -- moe_grouped_gemm from block-scaled FP8:
  *   y[i][n] = sum_b x_scale[i][b] w_scale[e][n/128][b]
@@ -484,7 +494,7 @@ int moe_grouped_gemm_fp8(const uint8_t *x_e4m3, const float *x_scale, const int3
                          int x_div, int x_n, const int32_t *offsets, const uint8_t *w_e4m3,
                          const float *w_scale, const moe_expert_w *experts, int mat, int R, int N,
                          int K, int E, void *y, const int32_t *y_rows, int y_n, int y_is_fp32,
-                         void *stream);
+                         void *ws, size_t ws_bytes, void *stream);
 
 /* moe_swiglu -- a[r] = w_r silu(g) u of rows h[r] = [g (I) | u (I)], bf16 in
  * and out, fp32 between. w (optional, fp32 [w_n]): the row's weight, w[r] or

@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(_PKG, "libmoe.so")
 MOE_OK, MOE_EINVAL, MOE_ENOMEM, MOE_EHIP, MOE_EUNSUPPORTED, MOE_EBUSY = 0, -1, -2, -3, -4, -5
 MOE_W_BF16, MOE_W_MXFP4, MOE_W_NVFP4, MOE_W_FP8 = 0, 1, 2, 3
 MOE_MAT_W13, MOE_MAT_W2 = 0, 1
+MOE_GEMM_BF16, MOE_GEMM_FP8, MOE_GEMM_DX, MOE_GEMM_DW = 0, 1, 2, 3
 MOE_OPT_FFN_PATH = 1
 MOE_OPT_TIMING = 2
 MOE_OPT_DEC_SPLIT = 3
@@ -35,7 +36,7 @@ EXPORTS = [
     "moe_micro_read", "moe_micro_mfma", "expert_cache_bandwidth", "expert_cache_prefetch_qstar",
     "moe_permute_split", "moe_cpu_expert_ffn", "moe_scatter_rows", "moe_permute_ffn_combine",
     "moe_layer_fused", "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw",
-    "moe_grouped_gemm_fp8", "moe_swiglu", "moe_swiglu_grad", "moe_quant_fp8",
+    "moe_grouped_gemm_fp8", "moe_grouped_gemm_workspace", "moe_swiglu", "moe_swiglu_grad", "moe_quant_fp8",
     "moe_swiglu_quant_fp8",
 ]
 
@@ -105,10 +106,11 @@ def load(path: str | None = None):
         "moe_permute_split": (I, [P, P, I, P, P, P, P, C.POINTER(I)]),
         "moe_cpu_expert_ffn": (I, [I, P, P, P, P, I, I, P, I, P, I]),
         "moe_scatter_rows": (I, [P, P, I, Z, P, P]),
-        "moe_grouped_gemm": (I, [P, P, I, I, P, P, P, I, I, I, I, I, P, P, I, I, P]),
-        "moe_grouped_gemm_dx": (I, [P, P, I, I, P, P, P, I, I, I, I, I, P, P, I, I, P]),
-        "moe_grouped_gemm_dw": (I, [P, P, I, I, P, P, I, I, P, I, I, I, I, P, I, I, P]),
-        "moe_grouped_gemm_fp8": (I, [P, P, P, I, I, P, P, P, P, I, I, I, I, I, P, P, I, I, P]),
+        "moe_grouped_gemm": (I, [P, P, I, I, P, P, P, I, I, I, I, I, P, P, I, I, P, Z, P]),
+        "moe_grouped_gemm_dx": (I, [P, P, I, I, P, P, P, I, I, I, I, I, P, P, I, I, P, Z, P]),
+        "moe_grouped_gemm_dw": (I, [P, P, I, I, P, P, I, I, P, I, I, I, I, P, I, I, P, Z, P]),
+        "moe_grouped_gemm_fp8": (I, [P, P, P, I, I, P, P, P, P, I, I, I, I, I, P, P, I, I, P, Z, P]),
+        "moe_grouped_gemm_workspace": (I, [I, I, I, I, I, C.POINTER(Z)]),
         "moe_swiglu": (I, [P, P, P, I, P, I, I, P, P]),
         "moe_swiglu_grad": (I, [P, P, P, P, I, P, I, I, P, P, P, P]),
         "moe_quant_fp8": (I, [P, P, I, I, P, P, P]),
@@ -264,6 +266,14 @@ def moe_workspace_size(T, k, H, I, E):
     a, b = C.c_size_t(0), C.c_size_t(0)
     _check("moe_workspace_size", load().moe_workspace_size(T, k, H, I, E, C.byref(a), C.byref(b)))
     return a.value, b.value
+
+
+def moe_grouped_gemm_workspace(kind, R, N, K, E):
+    """Bytes of workspace a product of these sizes can use (often 0)."""
+    b = C.c_size_t(0)
+    _check("moe_grouped_gemm_workspace",
+           load().moe_grouped_gemm_workspace(kind, R, N, K, E, C.byref(b)))
+    return b.value
 
 
 def moe_set_option(option, value):

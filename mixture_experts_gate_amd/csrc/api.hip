@@ -58,7 +58,7 @@ static const char *const g_kernel_names[K_COUNT] = {
     "ffn_decode_gate_up", "ffn_decode_down", "ffn_prefill_gate_up", "ffn_prefill_down",
     "combine", "cache_table", "pack_mxfp4", "route_permute", "ffn_prefill_split",
     "cache_move", "micro_read", "micro_mfma", "scatter_rows", "layer_fused", "product",
-    "product_fp8", "product_dx", "product_dw", "gated", "gated_grad", "to_fp8"};
+    "product_fp8", "product_dx", "product_dw", "product_join", "gated", "gated_grad", "to_fp8"};
 
 static hipEvent_t pool_event() {
     if (!g_evpool.empty()) {

@@ -456,9 +456,25 @@ static bool product_small(const ProductArgs &a, int mode) {
     return (mode == kDx || mode == kDw) && a.R < 384L * a.E;
 }
 
+// Parts that the call cuts c into when it has the workspace for their sums.
+static int product_slices(const ProductArgs &a, int mode) {
+    const bool forward = mode == kFwd || mode == kFwdFp8;
+    if (a.R == 0 || (forward && product_streams(a)) || !product_small(a, mode)) return 1;
+    return small_slices(a, mode);
+}
+
+static size_t part_bytes(const ProductArgs &a, int mode, int slices) {
+    const bool forward = mode == kFwd || mode == kFwdFp8;
+    return slices < 2 ? 0 : (size_t)slices * (mode == kDw ? (size_t)a.E * a.N : (size_t)a.R) *
+                                (forward ? a.N : a.K) * sizeof(float);
+}
+
 template <int MODE>
-static void launch_product(const ProductArgs &a, hipStream_t s) {
+static void launch_product(ProductArgs &a, void *ws, size_t ws_bytes, hipStream_t s) {
     const int cu = compute_units();
+    a.slices = product_slices(a, MODE);
+    a.part = (float *)ws;
+    if (!ws || ws_bytes < part_bytes(a, MODE, a.slices)) a.slices = 1;
     if ((MODE == kFwd || MODE == kFwdFp8) && product_streams(a)) {
         launch_product_stream(a, MODE == kFwdFp8, s);
         return;
@@ -499,19 +515,20 @@ extern "C" int moe_grouped_gemm(const uint16_t *x_bf16, const int32_t *x_rows, i
                                 const int32_t *offsets, const uint16_t *w_bf16,
                                 const moe_expert_w *experts, int mat, int R, int N, int K, int E,
                                 void *y, const int32_t *y_rows, int y_n, int y_is_fp32,
-                                void *stream) {
+                                void *ws, size_t ws_bytes, void *stream) {
     const int rc = check_sizes(R, N, K, E, offsets, 8);
     if (rc != MOE_OK) return rc;
     if (mat != MOE_MAT_W13 && mat != MOE_MAT_W2) return MOE_EINVAL;
     if (R == 0) return MOE_OK;
-    if ((!w_bf16) == (!experts) || !aligned16(w_bf16) || !y || !aligned16(y)) return MOE_EINVAL;
+    if ((!w_bf16) == (!experts) || !aligned16(w_bf16) || !y || !aligned16(y) || !aligned16(ws))
+        return MOE_EINVAL;
     if (!rows_ok(x_bf16, x_rows, x_div, x_n, R) || y_n < (y_rows ? 1 : R)) return MOE_EINVAL;
     ProductArgs a{};
     a.offsets = offsets, a.E = E, a.R = R, a.N = N, a.K = K;
     a.a = rows_in(x_bf16, x_rows, x_div, x_n);
     a.m = Mats{(const char *)w_bf16, nullptr, experts, mat};
     a.out = y, a.out_rows = y_rows, a.out_n = y_n, a.out_f32 = y_is_fp32 != 0;
-    launch_product<kFwd>(a, (hipStream_t)stream);
+    launch_product<kFwd>(a, ws, ws_bytes, (hipStream_t)stream);
     return check_launch();
 }
 
@@ -520,12 +537,14 @@ extern "C" int moe_grouped_gemm_fp8(const uint8_t *x_e4m3, const float *x_scale,
                                     const int32_t *offsets, const uint8_t *w_e4m3,
                                     const float *w_scale, const moe_expert_w *experts, int mat,
                                     int R, int N, int K, int E, void *y, const int32_t *y_rows,
-                                    int y_n, int y_is_fp32, void *stream) {
+                                    int y_n, int y_is_fp32, void *ws, size_t ws_bytes,
+                                    void *stream) {
     const int rc = check_sizes(R, N, K, E, offsets, 16);
     if (rc != MOE_OK) return rc;
     if (mat != MOE_MAT_W13 && mat != MOE_MAT_W2) return MOE_EINVAL;
     if (R == 0) return MOE_OK;
-    if ((!w_e4m3) == (!experts) || (!w_e4m3) != (!w_scale) || !aligned16(w_e4m3) || !y || !aligned16(y))
+    if ((!w_e4m3) == (!experts) || (!w_e4m3) != (!w_scale) || !aligned16(w_e4m3) || !y || !aligned16(y) ||
+        !aligned16(ws))
         return MOE_EINVAL;
     if (!x_scale || !rows_ok(x_e4m3, x_rows, x_div, x_n, R) || y_n < (y_rows ? 1 : R))
         return MOE_EINVAL;
@@ -535,7 +554,7 @@ extern "C" int moe_grouped_gemm_fp8(const uint8_t *x_e4m3, const float *x_scale,
     a.a_s = x_scale;
     a.m = Mats{(const char *)w_e4m3, w_scale, experts, mat};
     a.out = y, a.out_rows = y_rows, a.out_n = y_n, a.out_f32 = y_is_fp32 != 0;
-    launch_product<kFwdFp8>(a, (hipStream_t)stream);
+    launch_product<kFwdFp8>(a, ws, ws_bytes, (hipStream_t)stream);
     return check_launch();
 }
 
@@ -543,30 +562,32 @@ extern "C" int moe_grouped_gemm_dx(const uint16_t *dy_bf16, const int32_t *dy_ro
                                    int dy_n, const int32_t *offsets, const uint16_t *w_bf16,
                                    const moe_expert_w *experts, int mat, int R, int N, int K,
                                    int E, void *dx, const int32_t *dx_rows, int dx_n,
-                                   int dx_is_fp32, void *stream) {
+                                   int dx_is_fp32, void *ws, size_t ws_bytes, void *stream) {
     const int rc = check_sizes(R, N, K, E, offsets, 8);
     if (rc != MOE_OK) return rc;
     if (mat != MOE_MAT_W13 && mat != MOE_MAT_W2) return MOE_EINVAL;
     if (R == 0) return MOE_OK;
-    if ((!w_bf16) == (!experts) || !aligned16(w_bf16) || !dx || !aligned16(dx)) return MOE_EINVAL;
+    if ((!w_bf16) == (!experts) || !aligned16(w_bf16) || !dx || !aligned16(dx) || !aligned16(ws))
+        return MOE_EINVAL;
     if (!rows_ok(dy_bf16, dy_rows, dy_div, dy_n, R) || dx_n < (dx_rows ? 1 : R)) return MOE_EINVAL;
     ProductArgs a{};
     a.offsets = offsets, a.E = E, a.R = R, a.N = N, a.K = K;
     a.a = rows_in(dy_bf16, dy_rows, dy_div, dy_n);
     a.m = Mats{(const char *)w_bf16, nullptr, experts, mat};
     a.out = dx, a.out_rows = dx_rows, a.out_n = dx_n, a.out_f32 = dx_is_fp32 != 0;
-    launch_product<kDx>(a, (hipStream_t)stream);
+    launch_product<kDx>(a, ws, ws_bytes, (hipStream_t)stream);
     return check_launch();
 }
 
 extern "C" int moe_grouped_gemm_dw(const uint16_t *dy_bf16, const int32_t *dy_rows, int dy_div,
                                    int dy_n, const uint16_t *x_bf16, const int32_t *x_rows,
                                    int x_div, int x_n, const int32_t *offsets, int R, int N, int K,
-                                   int E, void *dw, int dw_is_fp32, int accumulate, void *stream) {
+                                   int E, void *dw, int dw_is_fp32, int accumulate, void *ws,
+                                   size_t ws_bytes, void *stream) {
     const int rc = check_sizes(R, N, K, E, offsets, 8);
     if (rc != MOE_OK) return rc;
     if (accumulate && !dw_is_fp32) return MOE_EINVAL;
-    if (!dw || !aligned16(dw)) return MOE_EINVAL;
+    if (!dw || !aligned16(dw) || !aligned16(ws)) return MOE_EINVAL;
     if (R > 0 && (!rows_ok(dy_bf16, dy_rows, dy_div, dy_n, R) || !rows_ok(x_bf16, x_rows, x_div, x_n, R)))
         return MOE_EINVAL;
     ProductArgs a{};
@@ -574,6 +595,16 @@ extern "C" int moe_grouped_gemm_dw(const uint16_t *dy_bf16, const int32_t *dy_ro
     a.a = rows_in(dy_bf16, dy_rows, dy_div, dy_n);
     a.b = rows_in(x_bf16, x_rows, x_div, x_n);
     a.out = dw, a.out_n = E * N, a.out_f32 = dw_is_fp32 != 0, a.accumulate = accumulate != 0;
-    launch_product<kDw>(a, (hipStream_t)stream);
+    launch_product<kDw>(a, ws, ws_bytes, (hipStream_t)stream);
     return check_launch();
+}
+
+extern "C" int moe_grouped_gemm_workspace(int kind, int R, int N, int K, int E, size_t *bytes) {
+    if (kind < kFwd || kind > kDw || !bytes) return MOE_EINVAL;
+    const int rc = check_sizes(R, N, K, E, E == 1 ? nullptr : (const int32_t *)16, kind == kFwdFp8 ? 16 : 8);
+    if (rc != MOE_OK) return rc;
+    ProductArgs a{};
+    a.E = E, a.R = R, a.N = N, a.K = K;
+    *bytes = part_bytes(a, kind, product_slices(a, kind));
+    return MOE_OK;
 }

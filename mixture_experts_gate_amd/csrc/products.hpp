@@ -54,6 +54,8 @@ struct ProductArgs {
     int out_n;
     int out_f32;
     int accumulate;            // dw: add to what is there (fp32)
+    float *part;               // sums of `slices` parts of c, [slices][R or E N][q] (slices > 1)
+    int slices;
 };
 
 enum ProductMode { kFwd = 0, kFwdFp8 = 1, kDx = 2, kDw = 3 };
@@ -423,6 +425,7 @@ void launch_product_stream(const ProductArgs &a, bool fp8, hipStream_t s);
 // products_small.hip: any product in tiles of 128 x 128, two workgroups a
 // compute unit
 void launch_product_small(const ProductArgs &a, int mode, hipStream_t s);
+int small_slices(const ProductArgs &a, int mode);   // parts that c is worth being cut into
 
 int kernel_of(int mode);   // timing id of a product
 int compute_units();   // of the current device (256 on MI355X)

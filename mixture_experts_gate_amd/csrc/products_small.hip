@@ -50,10 +50,13 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
         total_tiles<kTThreads>(A, kT, L.base, L.wsum);
         total = L.base[A.E] * tq;
     }
+    const int ns = A.slices;
+    total *= ns;
     const int nx = gridDim.x >= 8 ? 8 : 1;
     const int xcd = blockIdx.x % nx, per = ((int)gridDim.x - xcd + nx - 1) / nx;
     const int t0 = (int)((long)total * xcd / nx), t1 = (int)((long)total * (xcd + 1) / nx);
-    for (int ti = t0 + (int)blockIdx.x / nx; ti < t1; ti += per) {
+    for (int si = t0 + (int)blockIdx.x / nx; si < t1; si += per) {
+        const int ti = ns > 1 ? si / ns : si, slice = si - ti * ns;     // tile, part of its c
         int e, p0, q0, lo, cnt, half = 64;
         if (kDwMode) {
             e = ti / (tpw * tq);
@@ -74,6 +77,7 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
         const int np = half / 16;    // p tiles of a wavefront with work
         const int C = kDwMode ? cnt : MODE == kDx ? A.N : A.K;
         const int steps = (C + CK - 1) / CK;
+        const int kb = (int)((long)steps * slice / ns), ke = (int)((long)steps * (slice + 1) / ns);
 
         __syncthreads();   // the last tile's readers of L are done
         if (!kDwMode) {
@@ -85,7 +89,7 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
                 int d = -1;
                 if (in && s >= 0) {
                     d = A.out_rows ? A.out_rows[i] : i;
-                    if (d < 0 || d >= A.out_n) d = -1;
+                    d = d < 0 || d >= A.out_n ? -1 : ns > 1 ? i : d;     // (parts keep sorted order)
                 }
                 L.src[t] = s < 0 ? 0 : s;
                 L.dst[t] = d;
@@ -93,10 +97,12 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
         } else if (w < 2 && cnt > 0) {
             const RowsIn &in = w == 0 ? A.a : A.b;
 #pragma unroll
-            for (int k = 0; k < S + 2; ++k) copy_indices(in, 64 * k, lo, cnt, L.raw[k][w]);
+            for (int k = kb; k < kb + S + 2; ++k)
+                copy_indices(in, 64 * k, lo, cnt, L.raw[k % (S + 3)][w]);
             wait_copies<0>();
 #pragma unroll
-            for (int k = 0; k < S + 2; ++k) rows_from_indices(in, 64 * k, lo, cnt, L.raw[k][w], L.rows[k][w]);
+            for (int k = kb; k < kb + S + 2; ++k)
+                rows_from_indices(in, 64 * k, lo, cnt, L.raw[k % (S + 3)][w], L.rows[k % (S + 3)][w]);
         }
         __syncthreads();
 
@@ -165,26 +171,26 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
             for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < S - 1; ++k)
-            if (k < steps) fetch(k);
-        for (int k = 0; k < steps; ++k) {
+            if (kb + k < ke) fetch(kb + k);
+        for (int k = kb; k < ke; ++k) {
             if (S == 1) fetch(k);
             const char *const bp = L.p[k % S], *const bq = L.q[k % S];
             // the indices of step k + S + 2, which have landed by the wait of step k + 2
-            if (kDwMode && w < 2 && k + S + 2 < steps)
+            if (kDwMode && w < 2 && k + S + 2 < ke)
                 copy_indices(w == 0 ? A.a : A.b, 64 * (k + S + 2), lo, cnt, L.raw[(k + S + 2) % (S + 3)][w]);
             // step k is in LDS (of the S - 2 steps after it, those copied may be in
             // flight), and step k - 1 is read
-            const int later = steps - 1 - k < S - 2 ? steps - 1 - k : S - 2;
+            const int later = ke - 1 - k < S - 2 ? ke - 1 - k : S - 2;
             if (later >= 2) wait_copies<16>();
             else if (later == 1) wait_copies<8>();
             else wait_copies<0>();
             wait_lds();
             bare_barrier();
             // the rows of step k + S, for the next step's copies
-            if (kDwMode && w < 2 && k >= 2 && k + S < steps)
+            if (kDwMode && w < 2 && k >= kb + 2 && k + S < ke)
                 rows_from_indices(w == 0 ? A.a : A.b, 64 * (k + S), lo, cnt, L.raw[(k + S) % (S + 3)][w],
                                   L.rows[(k + S) % (S + 3)][w]);
-            if (S > 1 && k + S - 1 < steps) fetch(k + S - 1);
+            if (S > 1 && k + S - 1 < ke) fetch(k + S - 1);
             const float wsk = MODE == kFwdFp8 ? as_scalar(ws)[k] : 0.0f;
             if (MODE == kFwdFp8) {
                 u32x4 qf[4][2];
@@ -252,10 +258,15 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
             }
         }
 
+        ProductArgs to = A;
+        if (ns > 1) {
+            to.out = A.part + (size_t)slice * (kDwMode ? (size_t)A.E * A.N : (size_t)A.R) * Qn;
+            to.out_f32 = 1, to.accumulate = 0;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i >= np) continue;
-            store_tile<MODE>(A, q0 + 64 * wq, Qn, g, r, acc[i], [&](int p) -> long {
+            store_tile<MODE>(to, q0 + 64 * wq, Qn, g, r, acc[i], [&](int p) -> long {
                 if (!kDwMode) return L.dst[64 * wp + 16 * i + p];
                 const int n = p0 + 64 * wp + 16 * i + p;
                 return n < A.N ? (long)e * A.N + n : -1;
@@ -264,11 +275,59 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
     }
 }
 
-void launch_product_small(const ProductArgs &a, int mode, hipStream_t s) {
+// The sum of the parts, in order, to out: 4 q a thread.
+template <bool DW>
+__global__ __launch_bounds__(256) void join_kernel(ProductArgs A, int Qn) {
+    const int per = Qn / 4;
+    const long id = (long)blockIdx.x * blockDim.x + threadIdx.x;
+    const long row = id / per;
+    const int q = (int)(id - row * per) * 4;
+    const long rows = DW ? (long)A.E * A.N : A.R;
+    if (row >= rows) return;
+    long to = row;
+    if (!DW) {
+        const int i = (int)row;
+        if (A.offsets && (i < A.offsets[0] || i >= A.offsets[A.E])) return;
+        to = A.out_rows ? A.out_rows[i] : i;
+        if (to < 0 || to >= A.out_n || source_row(A.a, i) < 0) return;
+    }
+    f32x4 v = {0, 0, 0, 0};
+    for (int k = 0; k < A.slices; ++k)
+        v += *(const MOE_GLOBAL f32x4 *)(A.part + ((size_t)k * rows + row) * Qn + q);
+    if (A.out_f32) {
+        MOE_GLOBAL f32x4 *const o = (MOE_GLOBAL f32x4 *)((float *)A.out + (size_t)to * Qn + q);
+        *o = DW && A.accumulate ? *o + v : v;
+    } else {
+        typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+        *(MOE_GLOBAL u32x2 *)((uint16_t *)A.out + (size_t)to * Qn + q) =
+            u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    }
+}
+
+static long small_tiles(const ProductArgs &a, int mode) {
     const int Qn = mode == kFwd || mode == kFwdFp8 ? a.N : a.K;
     const long tq = (Qn + kT - 1) / kT;
-    const long tiles = mode == kDw ? (long)a.E * ((a.N + kT - 1) / kT) * tq
-                                   : (a.R / kT + (a.R < a.E ? a.R : a.E)) * tq;
+    return mode == kDw ? (long)a.E * ((a.N + kT - 1) / kT) * tq
+                       : (a.R / kT + (a.R < a.E ? a.R : a.E)) * tq;
+}
+
+// With few tiles and many steps (64 c, FP8 128) each, c is cut into parts whose
+// sums are added afterwards in their order: as many as give two workgroups a compute
+// unit, of six steps at least. (A step takes 0.8 us of a workgroup, the
+// addition's launch 2 to 3: the forward of 261 rows, K = 3648, N = 112, 48 us
+// whole.)
+int small_slices(const ProductArgs &a, int mode) {
+    const long tiles = small_tiles(a, mode);
+    const long c = mode == kDw ? a.R / a.E : mode == kDx ? a.N : a.K;
+    const long steps = c / (mode == kFwdFp8 ? 128 : 64);
+    long n = 2L * compute_units() / (tiles < 1 ? 1 : tiles);
+    n = n < steps / 6 ? n : steps / 6;
+    return n < 2 ? 1 : n > 16 ? 16 : (int)n;
+}
+
+void launch_product_small(const ProductArgs &a, int mode, hipStream_t s) {
+    const int Qn = mode == kFwd || mode == kFwdFp8 ? a.N : a.K;
+    const long tiles = small_tiles(a, mode) * a.slices;
     const int cu = compute_units();
     const bool deep = tiles <= 2L * cu;
     const dim3 grid((unsigned)(tiles < 4L * cu ? tiles : 4L * cu)), block(kTThreads);
@@ -283,6 +342,12 @@ void launch_product_small(const ProductArgs &a, int mode, hipStream_t s) {
     else if (mode == kDx) MOE_SMALL_LAUNCH(kDx);
     else MOE_SMALL_LAUNCH(kDw);
 #undef MOE_SMALL_LAUNCH
+    if (a.slices > 1) {
+        const long n = (mode == kDw ? (long)a.E * a.N : (long)a.R) * (Qn / 4);
+        const dim3 blocks((unsigned)((n + 255) / 256));
+        if (mode == kDw) MOE_LAUNCH(K_PROD_JOIN, join_kernel<true>, blocks, dim3(256), 0, s, a, Qn);
+        else MOE_LAUNCH(K_PROD_JOIN, join_kernel<false>, blocks, dim3(256), 0, s, a, Qn);
+    }
 }
 
 }  // namespace moe

@@ -145,6 +145,26 @@ def _rows_output(out, name, R, n, out_rows, dtypes, dev, stream):
 
 
 _calls = {}      # the library's functions, once looked up
+_sizes = {}      # workspace bytes by (kind, R, N, K, E, GPU)
+
+
+def _workspace(kind, R, N, K, E, dev, stream):
+    """(tensor or None, address, bytes) of the workspace the product can use."""
+    key = (kind, R, N, K, E, dev)
+    n = _sizes.get(key)
+    if n is None:
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        if torch._C._cuda_getDevice() != dev:
+            with torch.cuda.device(dev):
+                n = _lib.moe_grouped_gemm_workspace(kind, R, N, K, E)
+        else:
+            n = _lib.moe_grouped_gemm_workspace(kind, R, N, K, E)
+        _sizes[key] = n
+    if n == 0 or isinstance(stream, int):
+        return None, None, 0
+    ws = _output(None, "workspace", (n,), (torch.uint8,), dev, stream)
+    return ws, ws.data_ptr(), n
 
 
 def _run(fn, dev, stream, *args):
@@ -175,9 +195,11 @@ def grouped_matmul(x, w, offsets=None, *, rows=None, div=1, out_rows=None, out=N
         _fail(f"x: {x.shape[1]} columns, w has {K}")
     R = _count(x, rows, "rows")
     out = _rows_output(out, "out", R, N, out_rows, _OUT, dev, stream)
+    ws, pws, nws = _workspace(_lib.MOE_GEMM_BF16, R, N, K, E, dev, stream)
     _run("moe_grouped_gemm", dev, stream, x.data_ptr(), _index(rows, "rows", R, dev), div,
          x.shape[0], _offsets(offsets, E, dev), pw, tab, mat, R, N, K, E, out.data_ptr(),
-         _index(out_rows, "out_rows", R, dev), out.shape[0], int(out.dtype is torch.float32))
+         _index(out_rows, "out_rows", R, dev), out.shape[0],
+         int(out.dtype is torch.float32), pws, nws)
     return out
 
 
@@ -195,10 +217,11 @@ def grouped_matmul_fp8(x, x_scale, w, w_scale=None, offsets=None, *, rows=None, 
         _fail(f"x_scale: {tuple(x_scale.shape)}, [{x.shape[0]}, {-(-K // 128)}] is needed")
     R = _count(x, rows, "rows")
     out = _rows_output(out, "out", R, N, out_rows, _OUT, dev, stream)
+    ws, pws, nws = _workspace(_lib.MOE_GEMM_FP8, R, N, K, E, dev, stream)
     _run("moe_grouped_gemm_fp8", dev, stream, x.data_ptr(), x_scale.data_ptr(),
          _index(rows, "rows", R, dev), div, x.shape[0], _offsets(offsets, E, dev), pw, ps, tab,
          mat, R, N, K, E, out.data_ptr(), _index(out_rows, "out_rows", R, dev), out.shape[0],
-         int(out.dtype is torch.float32))
+         int(out.dtype is torch.float32), pws, nws)
     return out
 
 
@@ -212,9 +235,11 @@ def grouped_matmul_dx(dy, w, offsets=None, *, rows=None, div=1, out_rows=None, o
         _fail(f"dy: {dy.shape[1]} columns, w has {N} rows")
     R = _count(dy, rows, "rows")
     out = _rows_output(out, "out", R, K, out_rows, _OUT, dev, stream)
+    ws, pws, nws = _workspace(_lib.MOE_GEMM_DX, R, N, K, E, dev, stream)
     _run("moe_grouped_gemm_dx", dev, stream, dy.data_ptr(), _index(rows, "rows", R, dev), div,
          dy.shape[0], _offsets(offsets, E, dev), pw, tab, mat, R, N, K, E, out.data_ptr(),
-         _index(out_rows, "out_rows", R, dev), out.shape[0], int(out.dtype is torch.float32))
+         _index(out_rows, "out_rows", R, dev), out.shape[0],
+         int(out.dtype is torch.float32), pws, nws)
     return out
 
 
@@ -235,10 +260,11 @@ def grouped_matmul_dw(dy, x, offsets=None, *, dy_rows=None, dy_div=1, x_rows=Non
     out = _output(out, "out", (E, N, K), (torch.float32, torch.bfloat16), dev, stream)
     if out.shape[-2:] != (N, K) or out.numel() != E * N * K:
         _fail(f"out: {tuple(out.shape)}, [{E}, {N}, {K}] is needed")
+    ws, pws, nws = _workspace(_lib.MOE_GEMM_DW, R, N, K, E, dev, stream)
     _run("moe_grouped_gemm_dw", dev, stream, dy.data_ptr(), _index(dy_rows, "dy_rows", R, dev),
          dy_div, dy.shape[0], x.data_ptr(), _index(x_rows, "x_rows", R, dev), x_div, x.shape[0],
          _offsets(offsets, E, dev), R, N, K, E, out.data_ptr(), int(out.dtype is torch.float32),
-         int(bool(accumulate)))
+         int(bool(accumulate)), pws, nws)
     return out
 
 

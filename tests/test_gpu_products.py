@@ -93,6 +93,9 @@ SHAPES = [
     ([1000, 3], 1536, 512),
     ([150, 61, 0, 97] * 14, 768, 768),
     ([0, 40, 1, 16, 17, 0, 3] + [0] * 9, 136, 4672),
+    ([261, 130], 112, 3648),
+    ([2500], 136, 1040),
+    ([0, 1600, 3, 1200], 1544, 144),
     ([60, 0, 2, 16] + [1] * 20, 208, 2240),
     ([1300, 513, 1, 900, 1255], 2056, 1168),
     ([1300, 513, 1, 900, 1255], 1160, 2064),

@@ -217,20 +217,20 @@ def test_products_reject_bad_arguments(lib):
     L, d, bad = lib.load(), 0x1000, lib.MOE_EINVAL
 
     def gemm(fn, x=d, rows=None, div=1, n=8, off=d, w=d, tab=None, mat=0, R=8, N=16, K=16, E=2,
-             y=d, y_rows=None, y_n=8):
-        return fn(x, rows, div, n, off, w, tab, mat, R, N, K, E, y, y_rows, y_n, 0, None)
+             y=d, y_rows=None, y_n=8, ws=None):
+        return fn(x, rows, div, n, off, w, tab, mat, R, N, K, E, y, y_rows, y_n, 0, ws, 0, None)
 
     for fn in (L.moe_grouped_gemm, L.moe_grouped_gemm_dx):
         for kw in (dict(R=-1), dict(E=0), dict(E=513), dict(N=12), dict(K=12), dict(N=0),
                    dict(off=None), dict(w=None), dict(tab=d), dict(mat=2), dict(y=None),
                    dict(y=d + 8), dict(x=None), dict(x=d + 2), dict(n=7), dict(rows=d, n=0),
-                   dict(rows=d, div=0), dict(y_n=7), dict(y_rows=d, y_n=0)):
+                   dict(rows=d, div=0), dict(y_n=7), dict(y_rows=d, y_n=0), dict(ws=d + 4)):
             assert gemm(fn, **kw) == bad, kw
         assert gemm(fn, R=0, x=None, y=None) == lib.MOE_OK
 
     def fp8(x=d, xs=d, n=8, w=d, ws=d, tab=None, K=16, N=16, y=d):
         return L.moe_grouped_gemm_fp8(x, xs, None, 1, n, d, w, ws, tab, 0, 8, N, K, 2, y, None, 8,
-                                      0, None)
+                                      0, None, 0, None)
 
     for kw in (dict(x=None), dict(xs=None), dict(ws=None), dict(w=None), dict(tab=d), dict(K=24),
                dict(K=8), dict(N=12), dict(y=None), dict(n=3), dict(x=d + 8)):
@@ -238,7 +238,7 @@ def test_products_reject_bad_arguments(lib):
 
     def dw(dy=d, n=8, x=d, m=8, off=d, R=8, N=16, K=16, E=2, out=d, f32=1, acc=0):
         return L.moe_grouped_gemm_dw(dy, None, 1, n, x, None, 1, m, off, R, N, K, E, out, f32, acc,
-                                     None)
+                                     None, 0, None)
 
     for kw in (dict(dy=None), dict(x=None), dict(n=7), dict(m=7), dict(off=None), dict(out=None),
                dict(f32=0, acc=1), dict(N=4), dict(K=20), dict(out=d + 4), dict(E=600)):
@@ -259,6 +259,22 @@ def test_products_reject_bad_arguments(lib):
         assert fn(d, None, 4, 16, d, None, None) == bad
         assert fn(d, None, 4, 16, d + 4, d, None) == bad
         assert fn(d, None, 0, 16, None, None, None) == lib.MOE_OK
+
+
+def test_product_workspace_sizes(lib):
+    ws = lib.moe_grouped_gemm_workspace
+    # 3 x 1 tiles of 128 x 128 over K = 3648: at least two parts of [261][112] fp32
+    assert ws(lib.MOE_GEMM_BF16, 261, 112, 3648, 1) >= 2 * 261 * 112 * 4
+    assert ws(lib.MOE_GEMM_DW, 6546, 3320, 280, 1) % (3320 * 280 * 4) == 0
+    # many tiles, few steps, a handful of rows, none: whole
+    assert ws(lib.MOE_GEMM_BF16, 65536, 1536, 2048, 128) == 0
+    assert ws(lib.MOE_GEMM_DX, 300, 64, 256, 1) == 0
+    assert ws(lib.MOE_GEMM_BF16, 8, 1536, 2048, 128) == 0
+    assert ws(lib.MOE_GEMM_DW, 0, 64, 64, 4) == 0
+    for bad in ((4, 8, 64, 64, 1), (0, -1, 64, 64, 1), (0, 8, 60, 64, 1), (1, 8, 64, 24, 1),
+                (0, 8, 64, 64, 513)):
+        with pytest.raises(lib.MoeError):
+            ws(*bad)
 
 
 def test_products_module_needs_device_tensors():
