@@ -422,8 +422,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs &A, int q0, int Qn,
 bool product_streams(const ProductArgs &a);
 void launch_product_stream(const ProductArgs &a, bool fp8, hipStream_t s);
 
-// products_small.hip: any product in tiles of 128 x 128, two workgroups a
-// compute unit
+// products_small.hip: any product in tiles of 128 x 128
 void launch_product_small(const ProductArgs &a, int mode, hipStream_t s);
 int small_slices(const ProductArgs &a, int mode);   // parts that c is worth being cut into
 

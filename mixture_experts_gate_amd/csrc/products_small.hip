@@ -1,9 +1,9 @@
 // The products of products.hip in tiles of 128 x 128, for calls in which tiles of
-// 256 x 256 are too few to fill the device, or in which a tile has so few
-// steps that reading its first rows and writing its results is most of it: a
-// workgroup of four wavefronts (64 x 64 each) takes 70 KB of LDS, so two share a
-// compute unit, and one loads or stores while the other multiplies. Operand
-// layouts as there; one step is copied while the one before is multiplied.
+// 256 x 256 are too few to fill the device. Four wavefronts take 64 x 64 each;
+// LDS holds four steps, three of them copied ahead, so that a step costs its
+// matrix instructions, reads and one barrier (0.8 us) and not a copy's latency.
+// Operand layouts as there. Where even these tiles are few and the sums long,
+// c is cut into parts that join_kernel adds up.
 #include "products.hpp"
 
 namespace moe {
@@ -11,7 +11,8 @@ namespace moe {
 constexpr int kTThreads = 256;
 constexpr int kT = 128;          // p and q per tile
 
-template <int S>
+constexpr int S = 4;             // steps in LDS
+
 struct SmallLds {
     char p[S][kT * 128];
     char q[S][kT * 128];
@@ -24,14 +25,12 @@ struct SmallLds {
     int wsum[4];
 };
 
-// S: steps that LDS holds, of which S - 1 are copied ahead (S = 1: none; four workgroups share a
-// compute unit then).
-template <int MODE, int S>
-__global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) void product_small_kernel(ProductArgs A) {
+template <int MODE>
+__global__ __launch_bounds__(kTThreads) void product_small_kernel(ProductArgs A) {
     constexpr bool kDwMode = MODE == kDw, kQT = MODE == kDx || MODE == kDw;
     constexpr int ES = MODE == kFwdFp8 ? 1 : 2;       // bytes of an element
     constexpr int CK = 128 / ES;                       // c per step
-    __shared__ SmallLds<S> L;
+    __shared__ SmallLds L;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l = lane_id(), t = threadIdx.x, g = l >> 4, r = l & 15;
     const int wq = w & 1, wp = w >> 1;
@@ -173,7 +172,6 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
         for (int k = 0; k < S - 1; ++k)
             if (kb + k < ke) fetch(kb + k);
         for (int k = kb; k < ke; ++k) {
-            if (S == 1) fetch(k);
             const char *const bp = L.p[k % S], *const bq = L.q[k % S];
             // the indices of step k + S + 2, which have landed by the wait of step k + 2
             if (kDwMode && w < 2 && k + S + 2 < ke)
@@ -190,7 +188,7 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
             if (kDwMode && w < 2 && k >= kb + 2 && k + S < ke)
                 rows_from_indices(w == 0 ? A.a : A.b, 64 * (k + S), lo, cnt, L.raw[(k + S) % (S + 3)][w],
                                   L.rows[(k + S) % (S + 3)][w]);
-            if (S > 1 && k + S - 1 < ke) fetch(k + S - 1);
+            if (k + S - 1 < ke) fetch(k + S - 1);
             const float wsk = MODE == kFwdFp8 ? as_scalar(ws)[k] : 0.0f;
             if (MODE == kFwdFp8) {
                 u32x4 qf[4][2];
@@ -212,49 +210,35 @@ __global__ __launch_bounds__(kTThreads, S > 1 ? 1 : MODE == kFwdFp8 ? 3 : 4) voi
                     }
                 }
             } else {
-                // the transposing reads: with one wait for both halves, or (S = 1, whose
-                // registers are few) one for each
-                constexpr int H = S > 1 ? 2 : 1;
-                u32x4 qf[H][4], pf[H][4];
-                uint32_t qa[4], pa[4];
-                if (kQT)
+                u32x4 qf[2][4], pf[2][4];
+                uint32_t at[4];
+                if (kQT) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) qa[j] = frag_t_at<kDwMode, 256>(bq, wq, j, g, r);
-                if (kDwMode)
+                    for (int j = 0; j < 4; ++j) at[j] = frag_t_at<kDwMode, 256>(bq, wq, j, g, r);
+                    frags_t2<256, 0, 32 * 256>(at, qf[0], qf[1]);
+                }
+                if (kDwMode) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) pa[j] = frag_t_at<kDwMode, 256>(bp, wp, j, g, r);
-                if (kQT && S > 1) frags_t2<256, 0, 32 * 256>(qa, qf[0], qf[H - 1]);
-                if (kDwMode && S > 1) frags_t2<256, 0, 32 * 256>(pa, pf[0], pf[H - 1]);
+                    for (int j = 0; j < 4; ++j) at[j] = frag_t_at<kDwMode, 256>(bp, wp, j, g, r);
+                    frags_t2<256, 0, 32 * 256>(at, pf[0], pf[1]);
+                }
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    if (kQT && S == 1) {
-                        if (s == 0) frags_t<256, 0>(qa, qf[0]);
-                        else frags_t<256, 32 * 256>(qa, qf[0]);
-                    }
-                    if (kDwMode && S == 1) {
-                        if (s == 0) frags_t<256, 0>(pa, pf[0]);
-                        else frags_t<256, 32 * 256>(pa, pf[0]);
-                    }
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (!kQT) qf[s % H][j] = frag_n(bq, 64 * wq + 16 * j, s, g, r);
+                        if (!kQT) qf[s][j] = frag_n(bq, 64 * wq + 16 * j, s, g, r);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (i >= np) continue;
-                        if (!kDwMode) pf[s % H][i] = frag_n(bp, 64 * wp + 16 * i, s, g, r);
+                        if (!kDwMode) pf[s][i] = frag_n(bp, 64 * wp + 16 * i, s, g, r);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const bf16x8 p = as_bf16x8(pf[s % H][i]), q = as_bf16x8(qf[s % H][j]);
+                            const bf16x8 p = as_bf16x8(pf[s][i]), q = as_bf16x8(qf[s][j]);
                             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                                 q_is_row(MODE) ? q : p, q_is_row(MODE) ? p : q, acc[i][j], 0, 0, 0);
                         }
                     }
                 }
-            }
-
-            if (S == 1) {
-                wait_lds();
-                bare_barrier();     // the step is read
             }
         }
 
@@ -312,10 +296,10 @@ static long small_tiles(const ProductArgs &a, int mode) {
 }
 
 // With few tiles and many steps (64 c, FP8 128) each, c is cut into parts whose
-// sums are added afterwards in their order: as many as give two workgroups a compute
-// unit, of six steps at least. (A step takes 0.8 us of a workgroup, the
-// addition's launch 2 to 3: the forward of 261 rows, K = 3648, N = 112, 48 us
-// whole.)
+// sums are added afterwards in their order: as many as give every compute unit two
+// (dw and dx of 6546 rows, 3320 x 280: 118 us; with one each, 185 us, since 156
+// tiles are then not cut at all), of six steps at least. (A step takes 0.8 us, the addition's launch 2
+// to 3 us. Forward of 261 rows, K = 3648, N = 112: 48 us whole, 17 us in parts.)
 int small_slices(const ProductArgs &a, int mode) {
     const long tiles = small_tiles(a, mode);
     const long c = mode == kDw ? a.R / a.E : mode == kDx ? a.N : a.K;
@@ -329,19 +313,12 @@ void launch_product_small(const ProductArgs &a, int mode, hipStream_t s) {
     const int Qn = mode == kFwd || mode == kFwdFp8 ? a.N : a.K;
     const long tiles = small_tiles(a, mode) * a.slices;
     const int cu = compute_units();
-    const bool deep = tiles <= 2L * cu;
-    const dim3 grid((unsigned)(tiles < 4L * cu ? tiles : 4L * cu)), block(kTThreads);
+    const dim3 grid((unsigned)(tiles < 2L * cu ? tiles : 2L * cu)), block(kTThreads);
     const int kid = kernel_of(mode);
-#define MOE_SMALL_LAUNCH(MODE)                                                                     \
-    do {                                                                                           \
-        if (deep) MOE_LAUNCH(kid, (product_small_kernel<MODE, 4>), grid, block, 0, s, a);          \
-        else MOE_LAUNCH(kid, (product_small_kernel<MODE, 1>), grid, block, 0, s, a);               \
-    } while (0)
-    if (mode == kFwd) MOE_SMALL_LAUNCH(kFwd);
-    else if (mode == kFwdFp8) MOE_SMALL_LAUNCH(kFwdFp8);
-    else if (mode == kDx) MOE_SMALL_LAUNCH(kDx);
-    else MOE_SMALL_LAUNCH(kDw);
-#undef MOE_SMALL_LAUNCH
+    if (mode == kFwd) MOE_LAUNCH(kid, product_small_kernel<kFwd>, grid, block, 0, s, a);
+    else if (mode == kFwdFp8) MOE_LAUNCH(kid, product_small_kernel<kFwdFp8>, grid, block, 0, s, a);
+    else if (mode == kDx) MOE_LAUNCH(kid, product_small_kernel<kDx>, grid, block, 0, s, a);
+    else MOE_LAUNCH(kid, product_small_kernel<kDw>, grid, block, 0, s, a);
     if (a.slices > 1) {
         const long n = (mode == kDw ? (long)a.E * a.N : (long)a.R) * (Qn / 4);
         const dim3 blocks((unsigned)((n + 255) / 256));

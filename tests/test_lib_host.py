@@ -221,7 +221,7 @@ def test_products_reject_bad_arguments(lib):
         return fn(x, rows, div, n, off, w, tab, mat, R, N, K, E, y, y_rows, y_n, 0, ws, 0, None)
 
     for fn in (L.moe_grouped_gemm, L.moe_grouped_gemm_dx):
-        for kw in (dict(R=-1), dict(E=0), dict(E=513), dict(N=12), dict(K=12), dict(N=0),
+        for kw in (dict(R=-1), dict(E=0), dict(E=513), dict(N=12), dict(K=12), dict(N=0), dict(N=1 << 21), dict(N=1 << 20, K=1 << 20, E=4),
                    dict(off=None), dict(w=None), dict(tab=d), dict(mat=2), dict(y=None),
                    dict(y=d + 8), dict(x=None), dict(x=d + 2), dict(n=7), dict(rows=d, n=0),
                    dict(rows=d, div=0), dict(y_n=7), dict(y_rows=d, y_n=0), dict(ws=d + 4)):
