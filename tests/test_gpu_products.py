@@ -585,3 +585,51 @@ def test_refusals_on_device_tensors():
                 lambda: P.quant_fp8(x[:, :20].contiguous())):
         with pytest.raises(_lib.MoeError):
             bad()
+
+
+def test_rows_past_32_bit_offsets():
+    """Gathered and scattered rows beyond 4 GiB of their matrices (a handful of
+    rows, small tiles, large tiles)."""
+    g = _gen(21)
+    n = (5 << 30) // (2 * 64)                       # 5 GiB of 64 bf16 columns
+    x = torch.zeros(n, 64, device=DEV, dtype=torch.bfloat16)
+    for R, N in ((16, 64), (300, 128), (4096, 4096)):
+        at = torch.cat([torch.arange(R - R // 2, device=DEV),
+                        n - 1 - torch.arange(R // 2, device=DEV)]).to(torch.int32)
+        rows = at[torch.randperm(R, generator=g, device=DEV)]
+        x[rows.long()] = _randn(g, R, 64)
+        w = _randn(g, 1, N, 64)
+        y = P.grouped_matmul(x, w, rows=rows)
+        close = x[rows.long()].contiguous()
+        assert torch.equal(y, P.grouped_matmul(close, w)), R
+        assert torch.equal(P.grouped_matmul_dw(y, x, x_rows=rows), P.grouped_matmul_dw(y, close)), R
+        # dx [R, 64] scattered over the large matrix
+        dx = P.grouped_matmul_dx(y, w)
+        P.grouped_matmul_dx(y, w, out_rows=rows, out=x)
+        assert torch.equal(x[rows.long()], dx), R
+    del x
+
+
+def test_calls_on_two_streams_with_cut_sums():
+    """Calls that cut their sums, at the same time on two streams: workspaces of
+    their own, the same bits."""
+    g = _gen(22)
+    x, w = _randn(g, 261, 3648), _randn(g, 1, 112, 3648)
+    assert _lib.moe_grouped_gemm_workspace(_lib.MOE_GEMM_BF16, 261, 112, 3648, 1) > 0
+    want = P.grouped_matmul(x, w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(20):
+        for s, o in zip(streams, outs):
+            o.append(P.grouped_matmul(x, w, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(want, y) for o in outs for y in o)
+    # without a workspace the call runs whole: within one rounding of the other order
+    whole = torch.empty_like(want)
+    L = _lib.load()
+    assert L.moe_grouped_gemm(x.data_ptr(), None, 1, 261, None, w.data_ptr(), None, 0, 261, 112, 3648,
+                              1, whole.data_ptr(), None, 261, 0, None, 0,
+                              torch.cuda.current_stream().cuda_stream) == 0
+    ref, mag = _ref_product(x.double(), w.double(), [261], torch.arange(261, device=DEV))
+    _within(whole, ref, _round(ref, 3648 * SUM * mag, torch.bfloat16), "whole")
