@@ -443,7 +443,8 @@ int moe_timing_query(int kernel_id, long long *launches, double *total_ms);
  * (w2, s2), for matrices that live in an expert cache or in blobs; exactly one
  * of the two is given. Matrices and rows start 16-byte aligned.
  * Sums are fp32. Results do not depend on timing: the same call gives the same
- * bits. All sizes 1 <= E <= 512; R = 0 does nothing (dw writes its zeros).
+ * bits. All sizes 1 <= E <= 512, R <= 2^31 - 256; R = 0 does nothing (dw
+ * writes its zeros).
  * ws (16-byte aligned, may be NULL): with at least the bytes that
  * moe_grouped_gemm_workspace gives, a call with few output tiles and a long
  * sum cuts the sum into parts and adds them in a second launch (fp32, in a

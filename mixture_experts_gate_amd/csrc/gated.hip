@@ -165,7 +165,9 @@ __global__ __launch_bounds__(256) void to_fp8_kernel(const uint16_t *__restrict_
     *(MOE_GLOBAL i32x2 *)(q + (size_t)r * K + c) = i32x2{lo, hi};
 }
 
-static bool sizes_ok(int R, int I) { return R >= 0 && I >= 8 && I % 8 == 0 && I <= (1 << 24); }
+static bool sizes_ok(int R, int I) {
+    return R >= 0 && R <= kMaxRows && I >= 8 && I % 8 == 0 && I <= (1 << 24);
+}
 static bool al(const void *p) { return p && ((uintptr_t)p & 15) == 0; }
 static bool blocks_ok(long n) { return n <= 0x7FFFFFFFL; }
 

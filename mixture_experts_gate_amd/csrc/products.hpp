@@ -7,6 +7,7 @@
 namespace moe {
 
 constexpr int kMaxE = 512;       // experts of a product
+constexpr int kMaxRows = 0x7FFFFF00;    // rows: those of a last tile or workgroup fit an int
 
 // A matrix whose rows a product reads: row i of the sorted order is row
 // idx[i] / div of the matrix (row i where idx is NULL); n rows exist.

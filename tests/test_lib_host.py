@@ -288,3 +288,41 @@ def test_products_module_needs_device_tensors():
                  lambda: P.grouped_matmul_fp8(x, x, w)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_products_reject_rows_past_32_bits(lib):
+    """The threads of a last workgroup and the rows of a last tile have to fit
+    an int: R = 2^31 - 1 is refused by every entry point."""
+    L, d, R = lib.load(), 0x1000, 2 ** 31 - 1
+    for fn in (L.moe_grouped_gemm, L.moe_grouped_gemm_dx):
+        assert fn(d, None, 1, R, None, d, None, 0, R, 16, 16, 1, d, None, R, 0, None, 0,
+                  None) == lib.MOE_EINVAL
+    assert L.moe_grouped_gemm_fp8(d, d, None, 1, R, None, d, d, None, 0, R, 16, 16, 1, d, None, R,
+                                  0, None, 0, None) == lib.MOE_EINVAL
+    assert L.moe_grouped_gemm_dw(d, None, 1, R, d, None, 1, R, None, R, 16, 16, 1, d, 1, 0, None,
+                                 0, None) == lib.MOE_EINVAL
+    assert L.moe_swiglu(d, None, None, 0, None, R, 8, d, None) == lib.MOE_EINVAL
+    assert L.moe_swiglu_grad(d, d, None, None, 0, None, R, 8, d, None, None, None) == lib.MOE_EINVAL
+    for fn in (L.moe_quant_fp8, L.moe_swiglu_quant_fp8):
+        assert fn(d, None, R, 8, d, d, None) == lib.MOE_EINVAL
+    with pytest.raises(lib.MoeError):
+        lib.moe_grouped_gemm_workspace(lib.MOE_GEMM_BF16, R, 16, 16, 1)
+
+
+def test_product_layers_need_device_tensors():
+    """Host tensors are refused before anything is enqueued, and a refused
+    forward leaves no state for a backward."""
+    import torch
+    from mixture_experts_gate_amd.layer import Fp8BlockLayer
+    from mixture_experts_gate_amd.train import TrainExperts
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    ids, w = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    m = TrainExperts(64, 4, 2, 32, 4, device="cpu")
+    with pytest.raises(ValueError):
+        m.forward(x, ids, w, torch.zeros(4, 64, 64, dtype=torch.bfloat16),
+                  torch.zeros(4, 64, 32, dtype=torch.bfloat16))
+    with pytest.raises(RuntimeError):
+        m.backward(x)
+    layer = Fp8BlockLayer(64, 4, 2, 32, 4, device="cpu")
+    with pytest.raises(ValueError):
+        layer.forward(4, x, None, logits=torch.zeros(4, 4))
