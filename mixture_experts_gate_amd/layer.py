@@ -431,6 +431,18 @@ class Fp8BlockLayer:
         """route -> permute -> experts -> combine; returns out[:T] (bf16)."""
         if T > self.T_max:
             raise ValueError("T exceeds the buffers' T_max")
+        for t, name, n, cols, dtype in ((x, "x", T, self.H, torch.bfloat16),
+                                        (logits, "logits", T, self.E, torch.float32),
+                                        (wg, "wg", self.E, self.H, torch.bfloat16)):
+            if t is None and name != "x":
+                continue
+            if (t.dim() != 2 or t.shape[0] < n or t.shape[1] != cols or t.dtype != dtype
+                    or not t.is_contiguous() or not t.is_cuda or t.device != self.out.device):
+                raise ValueError(f"{name}: contiguous {dtype} [{n}, {cols}] on {self.out.device} "
+                                 "is needed")
+        if x.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(x.device):
+                return self.forward(T, x, table, logits, wg, shared_table, renormalize, stream)
         if T == 0:
             return self.out[:0]
         _lib.moe_route_permute(x, wg, logits, None if logits is not None else self.logits, T, self.H,

@@ -5,7 +5,8 @@ with a scale per 128 x 128 block: the products grouped by expert, the gated
 activation between them with its gradient, and rows to FP8. Every call checks
 its tensors (types, shapes, contiguity, one device), allocates what it is not
 given, and enqueues one kernel of ``libmoe.so`` on the current stream of the
-tensors' device, or on ``stream``. Nothing is computed by PyTorch.
+tensors' device, or on ``stream`` (two kernels and a workspace for a product
+whose sums are cut into parts). Nothing is computed by PyTorch.
 
 Rows are in *sorted order*: grouped by expert, expert e owning rows
 ``offsets[e]`` .. ``offsets[e+1] - 1`` (``offsets`` int32 [E+1] on the device,
@@ -64,9 +65,17 @@ def _need(t, name, dtypes, dev=None):
     _fail(f"{name}: on GPU {t.get_device()}, the others are on {dev}")
 
 
+def _int(n, name):
+    """n, as the library's 32-bit int takes it."""
+    if n > 0x7FFFFFFF:
+        _fail(f"{name}: {n} is past 32 bits")
+    return n
+
+
 def _matrix(t, name, dtype, dev=None):
     if _need(t, name, dtype, dev).dim() != 2:
         _fail(f"{name}: two dimensions are needed, got {tuple(t.shape)}")
+    _int(max(t.shape), name)
     return t
 
 
@@ -86,6 +95,7 @@ def _weights(w, ws, dtype, dev):
     if w.dim() not in (2, 3):
         _fail(f"w: [E, N, K] or [N, K] is needed, got {tuple(w.shape)}")
     E, N, K = (1, *w.shape) if w.dim() == 2 else w.shape
+    _int(max(w.shape), "w")
     if dtype is _BF16:
         return w.data_ptr(), None, None, 0, E, N, K
     _need(ws, "w_scale", _F32, dev)
@@ -121,7 +131,7 @@ def _count(x, rows, name):
         return x.shape[0]
     if not isinstance(rows, torch.Tensor):
         _fail(f"{name}: an int32 tensor is needed")
-    return rows.numel()
+    return _int(rows.numel(), name)
 
 
 def _output(out, name, shape, dtypes, dev, stream):
@@ -141,6 +151,7 @@ def _rows_output(out, name, R, n, out_rows, dtypes, dev, stream):
     out = _output(out, name, (R, n), dtypes, dev, stream)
     if out.dim() != 2 or out.shape[1] != n or (out_rows is None and out.shape[0] < R):
         _fail(f"{name}: {tuple(out.shape)}, [{R}, {n}] is needed")
+    _int(out.shape[0], name)
     return out
 
 
@@ -276,7 +287,7 @@ def _row_weights(w, w_rows, R, dev):
     _need(w, "w", _F32, dev)
     if w_rows is None and w.numel() < R:
         _fail(f"w: {w.numel()} weights for {R} rows")
-    return w.data_ptr(), _index(w_rows, "w_rows", R, dev), w.numel()
+    return w.data_ptr(), _index(w_rows, "w_rows", R, dev), _int(w.numel(), "w")
 
 
 def _limit(n_rows, dev):
@@ -308,16 +319,20 @@ def swiglu(h, w=None, w_rows=None, n_rows=None, out=None, stream=None):
 
 def swiglu_grad(h, da, w=None, w_rows=None, n_rows=None, dh=None, dw=None, a=None, stream=None):
     """Gradients of ``swiglu`` for da [R, I]: (dh [R, 2I] bf16, dw fp32 of w's
-    shape at the rows' indices, or None without w). ``a`` (bf16 [R, I], optional) receives
-    swiglu's result again."""
+    shape, or None without w). dw is written at the rows' indices, which must be
+    distinct; a ``dw`` that is not given is zero elsewhere. ``a`` (bf16 [R, I],
+    optional) receives swiglu's result again."""
     R, I, dev = _halves(h)
     if _matrix(da, "da", _BF16, dev).shape != (R, I):
         _fail(f"da: {tuple(da.shape)}, [{R}, {I}] is needed")
     pw, pr, wn = _row_weights(w, w_rows, R, dev)
     dh = _rows_output(dh, "dh", R, 2 * I, None, _BF16, dev, stream)
     if w is not None:
-        dw = _output(dw, "dw", w.shape, _F32, dev, stream)
-        if dw.numel() != wn:
+        if dw is None:
+            dw = _output(dw, "dw", w.shape, _F32, dev, stream)
+            with torch.cuda.stream(stream):
+                dw.zero_()
+        elif _need(dw, "dw", _F32, dev).numel() != wn:
             _fail(f"dw: {tuple(dw.shape)}, {tuple(w.shape)} is needed")
     elif dw is not None:
         _fail("dw: given without w")

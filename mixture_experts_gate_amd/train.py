@@ -42,8 +42,15 @@ class TrainExperts:
 
     def forward(self, x, topk_ids, topk_w, w13, w2):
         """out [T, H] bf16 of x [T, H] bf16, the router's topk_ids [T, k] int32
-        (distinct experts of a token) and topk_w [T, k] fp32, w13 [E, 2I, H] and
-        w2 [E, H, I] bf16."""
+        (distinct experts of a token, all of them in [0, E): the caller's to see
+        to; a padding token has any of them, with weights 0) and topk_w [T, k]
+        fp32, w13 [E, 2I, H] and w2 [E, H, I] bf16."""
+        self._saved = None
+        if not x.is_cuda or x.device != self.out.device:
+            raise ValueError(f"x: on {x.device}, the buffers are on {self.out.device}")
+        if x.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(x.device):
+                return self.forward(x, topk_ids, topk_w, w13, w2)
         T, k = x.shape[0], self.k
         if T > self.T_max or x.shape[1] != self.H:
             raise ValueError(f"x: {tuple(x.shape)}, at most [{self.T_max}, {self.H}]")
@@ -53,8 +60,8 @@ class TrainExperts:
         if w13.shape != (self.E, 2 * self.I, self.H) or w2.shape != (self.E, self.H, self.I):
             raise ValueError(f"w13, w2: {tuple(w13.shape)}, {tuple(w2.shape)}")
         n = T * k
-        self._saved = (x, topk_w, w13, w2)
         if T == 0:
+            self._saved = (x, topk_w, w13, w2)
             return self.out[:0]
         pair, off = self.sorted_pair[:n], self.offsets
         _lib.moe_permute(topk_ids, T, k, self.E, off, self.sorted_pair, self.pair_row, self.ws,
@@ -63,6 +70,7 @@ class TrainExperts:
         P.swiglu(self.h[:n], topk_w, pair, off[self.E:], out=self.a[:n])
         P.grouped_matmul(self.a[:n], w2, off, out_rows=pair, out=self.y[:n])
         _lib.moe_combine(self.y, False, self.ones, None, T, k, self.H, self.out)
+        self._saved = (x, topk_w, w13, w2)
         return self.out[:T]
 
     def backward(self, dout, accumulate=False):
@@ -72,6 +80,9 @@ class TrainExperts:
         if self._saved is None:
             raise RuntimeError("backward without a forward")
         x, topk_w, w13, w2 = self._saved
+        if x.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(x.device):
+                return self.backward(dout, accumulate)
         T, k = x.shape[0], self.k
         if dout.shape != x.shape:
             raise ValueError(f"dout: {tuple(dout.shape)}, {tuple(x.shape)} is needed")

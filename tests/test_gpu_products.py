@@ -445,6 +445,24 @@ def test_activation_limits_rows_and_weights():
     _within(a[0], gd * torch.sigmoid(gd), (gd * torch.sigmoid(gd)).abs() * (BF16 + 2.0 ** -14) + 1e-36, "far")
 
 
+def test_weight_gradient_without_rows_is_zero():
+    """A weight that no row points to has gradient 0 in a dw that the call makes,
+    whatever its memory held."""
+    g = _gen(10)
+    R, I, n = 5, 64, 4096
+    h, da = _randn(g, R, 2 * I), _randn(g, R, I)
+    w = torch.rand(n, generator=g, device=DEV)
+    rows = torch.tensor([7, 0, 4095, 12, -1], dtype=torch.int32, device=DEV)
+    old = [torch.full((n,), float("nan"), device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    del old
+    _, dw = P.swiglu_grad(h, da, w, rows)
+    _, some = P.swiglu_grad(h, da, w[:R].contiguous())      # (dw does not depend on w)
+    want = torch.zeros(n, device=DEV)
+    want[rows[:4].long()] = some[:4]
+    assert torch.equal(dw, want)
+
+
 # ------------------------------------------------------------ rows to FP8 --
 
 def _ref_quant(x, K):

@@ -197,6 +197,21 @@ def test_training_step_in_a_graph():
             assert torch.equal(a, b), k
 
 
+def test_fp8_block_layer_refuses_its_inputs():
+    """Tokens, logits and gate matrices of other shapes or types, before the
+    router reads them."""
+    layer = LY.Fp8BlockLayer(64, 4, 2, 64, 4)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV)
+    logits = torch.zeros(4, 4, device=DEV)
+    wg = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV)
+    for kw in (dict(x=x[:3], logits=logits), dict(x=x[:, :32], logits=logits),
+               dict(x=x.float(), logits=logits), dict(x=x, logits=logits[:2]),
+               dict(x=x, logits=logits.double()), dict(x=x, logits=logits.cpu()),
+               dict(x=x, wg=wg[:3]), dict(x=x, wg=wg.t())):
+        with pytest.raises(ValueError):
+            layer.forward(4, table=None, **kw)
+
+
 def test_refusals():
     x, ids, w, w13, w2, dout = _train_case(4, 4, 2, 64, 32, 1)
     m = TrainExperts(64, 4, 2, 32, 4)
