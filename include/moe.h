@@ -436,7 +436,8 @@ int moe_timing_query(int kernel_id, long long *launches, double *total_ms);
  * without, row i. An output with rows != NULL takes row i at its row rows[i]
  * (rows = sorted_pair writes pair order), which must be distinct. *_n is the
  * number of rows the matrix has; a row whose index is outside it is skipped:
- * its output row is left as it is, and it adds nothing to dw.
+ * its output row is left as it is, and it adds nothing to dw (outside either
+ * matrix, whatever its row of the other one holds).
  * Matrices [N][K] row-major, one per expert: either w_* = [E][N][K]
  * contiguous (and w_scale [E][ceil(N/128)][ceil(K/128)]), or experts = device
  * array [E] of moe_expert_w with mat = MOE_MAT_W13 (w13, s13) or MOE_MAT_W2

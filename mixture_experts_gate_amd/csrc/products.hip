@@ -210,13 +210,14 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
         };
         // dw: copies i and i + 1 of both
         auto copy_both = [&](int i, int k) {
-            const bool full = 64 * (k + 1) <= cnt;
+            const bool in_place = 64 * (k + 1) <= cnt && !A.a.idx && !A.b.idx;
             const int c = 16 * i + 2 * w, fl = fresh_lane();
             const size_t first = (size_t)(lo + 64 * k + c);
-            copy_rows<2, 512>(full && !A.a.idx, A.a, first, lda, po[1], po[0], &L.rows[k & 3][0][c + (fl >> 5)],
-                              L.p[k & 1] + c * 512);
-            copy_rows<2, 512>(full && !A.b.idx, A.b, first, ldq, po[2], qo, &L.rows[k & 3][1][c + (fl >> 5)],
-                              L.q[k & 1] + c * 512);
+            copy_rows<2, 512>(in_place,
+                              Rows{A.a, first, lda, po[1], po[0], &L.rows[k & 3][0][c + (fl >> 5)],
+                                   L.p[k & 1] + c * 512},
+                              Rows{A.b, first, ldq, po[2], qo, &L.rows[k & 3][1][c + (fl >> 5)],
+                                   L.q[k & 1] + c * 512});
         };
         auto copy_xs = [&](int k) {
             if (MODE == kFwdFp8 && w < kBP / kWave)

@@ -149,23 +149,43 @@ __device__ __forceinline__ void rows_from_indices(const RowsIn &r, int c, int lo
     rows[l] = c + l < cnt ? row : -1;
 }
 
-// dw: N copies of one operand, 16 rows of a step apart: rows in place that all
-// exist (a uniform base and a lane's offset), or the rows that `rows` lists (-1:
-// zeros). One branch for all: a branch a copy took as long as the multiplications.
+// dw: an operand's part in the copies of a step: the row of the first copy where
+// rows are in place, bytes of a row, the lane's offset from that row (in place)
+// and in a row, the list of rows (first one of this lane), the place in LDS.
+struct Rows {
+    const RowsIn &r;
+    size_t first, ld;
+    uint32_t off, col;
+    const int *rows;
+    char *to;
+};
+
+// dw: N copies of each operand, 16 rows of a step apart: rows in place that all
+// exist (a uniform base and a lane's offset), or the rows that the lists give. A
+// row that is -1 in one list is zeros in both operands: a zero beside a row that
+// is read would still give NaN where that one is not finite. One branch for all:
+// a branch a copy took as long as the multiplications.
 template <int N, int STRIDE>
-__device__ __forceinline__ void copy_rows(bool in_place, const RowsIn &r, size_t first, size_t ld, uint32_t off,
-                                          uint32_t col, const int *rows, char *to) {
+__device__ __forceinline__ void copy_rows(bool in_place, const Rows &p, const Rows &q) {
     if (in_place) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            lds_dma16(scalar_base(r.base + (first + 16 * i) * ld) + here(off), to + 16 * i * STRIDE);
-    } else {
-        int row[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) row[i] = rows[16 * i];
+            lds_dma16(scalar_base(p.r.base + (p.first + 16 * i) * p.ld) + here(p.off), p.to + 16 * i * STRIDE);
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            copy_or_zeros(row[i] >= 0, r.base + (size_t)(uint32_t)row[i] * ld + col, to + 16 * i * STRIDE);
+            lds_dma16(scalar_base(q.r.base + (q.first + 16 * i) * q.ld) + here(q.off), q.to + 16 * i * STRIDE);
+    } else {
+        int a[N], b[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) a[i] = p.rows[16 * i], b[i] = q.rows[16 * i];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            copy_or_zeros((a[i] | b[i]) >= 0, p.r.base + (size_t)(uint32_t)a[i] * p.ld + p.col,
+                          p.to + 16 * i * STRIDE);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            copy_or_zeros((a[i] | b[i]) >= 0, q.r.base + (size_t)(uint32_t)b[i] * q.ld + q.col,
+                          q.to + 16 * i * STRIDE);
     }
 }
 

@@ -134,10 +134,11 @@ __global__ __launch_bounds__(kTThreads) void product_small_kernel(ProductArgs A)
             const bool full = (k + 1) * CK <= C;
             if (kDwMode) {
                 const size_t first = (size_t)(lo + 64 * k + 4 * w);
-                copy_rows<4, 256>(full && !A.a.idx, A.a, first, lda, (uint32_t)((l >> 4) * lda + pcol),
-                                  (uint32_t)pcol, &L.rows[k % (S + 3)][0][tc], P + 4 * w * 256);
-                copy_rows<4, 256>(full && !A.b.idx, A.b, first, ldq, (uint32_t)((l >> 4) * ldq + qcol),
-                                  (uint32_t)qcol, &L.rows[k % (S + 3)][1][tc], Q + 4 * w * 256);
+                copy_rows<4, 256>(full && !A.a.idx && !A.b.idx,
+                                  Rows{A.a, first, lda, (uint32_t)((l >> 4) * lda + pcol), (uint32_t)pcol,
+                                       &L.rows[k % (S + 3)][0][tc], P + 4 * w * 256},
+                                  Rows{A.b, first, ldq, (uint32_t)((l >> 4) * ldq + qcol), (uint32_t)qcol,
+                                       &L.rows[k % (S + 3)][1][tc], Q + 4 * w * 256});
                 return;
             }
             if (full) {

@@ -1,0 +1,86 @@
+"""The expert products at the edges of what their calls allow: rows whose index
+is outside its matrix next to values that are not finite.
+
+Tolerance of a sum of n products of bf16 values in fp32: every addition is off
+by at most one unit in the last place of a result that is at most the sum of the
+terms' magnitudes, |error| <= n 2^-23 sum |a||b|.
+"""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_gate_amd import _lib, products as P
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+SUM = 2.0 ** -23
+
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(g, *shape, dtype=torch.bfloat16):
+    return torch.randn(*shape, device=DEV, generator=g).to(dtype)
+
+
+def _offsets(counts):
+    return torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device=DEV)
+
+
+# counts per expert, N, K and what the sizes select: 128 x 128 tiles, those with
+# the sum cut into parts, 256 x 256 tiles (more than half of 256 compute units)
+DW_PATHS = {
+    "small": ([40, 0, 90, 700], 72, 80),
+    "parts": ([1500], 256, 136),
+    "large": ([700, 0, 1, 130, 64], 1544, 1288),
+}
+
+
+@pytest.mark.parametrize("side", ["x", "dy", "both", "x_of_indexed", "dy_of_indexed"])
+@pytest.mark.parametrize("path", list(DW_PATHS))
+def test_dw_row_without_a_partner_adds_nothing(path, side):
+    """A sorted row whose index is outside one matrix adds nothing to dw, also
+    where its row of the other matrix holds NaN or an infinity; every step of
+    64 rows has such rows but one."""
+    counts, N, K = DW_PATHS[path]
+    g = _gen(sum(map(ord, path + side)))
+    R, E, div = sum(counts), len(counts), 3
+    parts = _lib.moe_grouped_gemm_workspace(_lib.MOE_GEMM_DW, R, N, K, E) > 0
+    assert parts == (path == "parts")
+    dy, x = _randn(g, R, N), _randn(g, R, K)
+    pos = torch.arange(R, device=DEV)
+    bad_x, bad_y = (pos * 7 % 61 == 3) & (pos // 64 != 2), (pos * 5 % 83 == 9) & (pos // 64 != 2)
+    if side.startswith("x"):
+        bad_y[:] = False
+    if side.startswith("dy"):
+        bad_x[:] = False
+    bad = bad_x | bad_y
+    assert bool(bad.any())
+    # the row's place in each matrix: through an index or its own
+    index_x, index_y = side != "dy", side != "x"
+    at_x = torch.randperm(R, generator=g, device=DEV) if index_x else pos
+    at_y = torch.randperm(R, generator=g, device=DEV) if index_y else pos
+    dy[at_y[bad]] = float("nan")
+    x[at_x[bad], ::2] = float("inf")
+    kw = {}
+    outside = torch.tensor([-1, R * div, -2 ** 31, 2 ** 31 - 1], device=DEV)
+    if index_x:
+        rows = at_x * div + pos % div
+        rows[bad_x] = outside[pos[bad_x] % 4]
+        kw.update(x_rows=rows.to(torch.int32), x_div=div)
+    if index_y:
+        rows = at_y * div + pos % div
+        rows[bad_y] = outside[pos[bad_y] % 4]
+        kw.update(dy_rows=rows.to(torch.int32), dy_div=div)
+    yd, xd = dy.double()[at_y], x.double()[at_x]
+    yd[bad], xd[bad] = 0, 0
+    dw = P.grouped_matmul_dw(dy, x, _offsets(counts), **kw)
+    lo = 0
+    for e, n in enumerate(counts):
+        a, b = yd[lo:lo + n].t().contiguous(), xd[lo:lo + n]
+        lo += n
+        err, bound = (dw[e].double() - a @ b).abs(), n * SUM * (a.abs() @ b.abs())
+        assert bool((err <= bound).all()), f"expert {e}: {int((~(err <= bound)).sum())} values off"
