@@ -37,6 +37,11 @@ __device__ __forceinline__ int row_count(const int32_t *n_rows, int R) {
     return n < 0 ? 0 : n < R ? n : R;
 }
 
+// Number of this workgroup: a launch's threads along x have to fit 32 bits (a
+// product past them wraps without an error), so the rest go along y.
+constexpr long kBlocksX = 1 << 23;
+__device__ __forceinline__ long block_id() { return (long)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Weight's place of row r: -1 where the index is outside the weights.
 __device__ __forceinline__ int weight_at(const int32_t *w_rows, int w_n, int r) {
     const int i = w_rows ? w_rows[r] : r;
@@ -49,9 +54,9 @@ __global__ __launch_bounds__(256) void gated_kernel(const uint16_t *__restrict__
                                                     const int32_t *__restrict__ n_rows, int R,
                                                     int I, uint16_t *__restrict__ a) {
     const int per = I / 8;
-    const long id = (long)blockIdx.x * blockDim.x + threadIdx.x;
-    const int r = (int)(id / per);
-    if (r >= row_count(n_rows, R)) return;
+    const long id = block_id() * blockDim.x + threadIdx.x, row = id / per;
+    if (row >= row_count(n_rows, R)) return;
+    const int r = (int)row;
     const int c = (int)(id - (long)r * per) * 8;
     float w = 1.0f;
     if (wt) {
@@ -72,8 +77,9 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(
     const uint16_t *__restrict__ h, const uint16_t *__restrict__ da, const float *__restrict__ wt,
     const int32_t *__restrict__ w_rows, int w_n, const int32_t *__restrict__ n_rows, int R, int I,
     uint16_t *__restrict__ dh, float *__restrict__ dw, uint16_t *__restrict__ a) {
-    const int r = blockIdx.x * (blockDim.x / kWave) + threadIdx.x / kWave, l = lane_id();
-    if (r >= row_count(n_rows, R)) return;
+    const long row = block_id() * (blockDim.x / kWave) + threadIdx.x / kWave;
+    if (row >= row_count(n_rows, R)) return;
+    const int r = (int)row, l = lane_id();
     float w = 1.0f;
     int at = -1;
     if (wt) {
@@ -114,9 +120,9 @@ __global__ __launch_bounds__(256) void to_fp8_kernel(const uint16_t *__restrict_
                                                      int K, uint8_t *__restrict__ q,
                                                      float *__restrict__ s) {
     const int kb = (K + 127) / 128;
-    const long id = ((long)blockIdx.x * blockDim.x + threadIdx.x) >> 4;
-    const int r = (int)(id / kb);
-    if (r >= row_count(n_rows, R)) return;
+    const long id = (block_id() * blockDim.x + threadIdx.x) >> 4, row = id / kb;
+    if (row >= row_count(n_rows, R)) return;
+    const int r = (int)row;
     const int b = (int)(id - (long)r * kb), l = threadIdx.x & 15, c = 128 * b + 8 * l;
     const bool in = c < K;
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -170,6 +176,9 @@ static bool sizes_ok(int R, int I) {
 }
 static bool al(const void *p) { return p && ((uintptr_t)p & 15) == 0; }
 static bool blocks_ok(long n) { return n <= 0x7FFFFFFFL; }
+static dim3 blocks_of(long n) {
+    return n <= kBlocksX ? dim3((unsigned)n) : dim3((unsigned)kBlocksX, (unsigned)((n + kBlocksX - 1) / kBlocksX));
+}
 
 }  // namespace moe
 
@@ -183,7 +192,7 @@ extern "C" int moe_swiglu(const uint16_t *h_bf16, const float *w, const int32_t 
         return MOE_EINVAL;
     const long blocks = ((long)R * (I / 8) + 255) / 256;
     if (!blocks_ok(blocks)) return MOE_EINVAL;
-    MOE_LAUNCH(K_GATED, gated_kernel, dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream,
+    MOE_LAUNCH(K_GATED, gated_kernel, blocks_of(blocks), dim3(256), 0, (hipStream_t)stream,
                h_bf16, w, w_rows, w_n, n_rows, R, I, a_bf16);
     return check_launch();
 }
@@ -195,7 +204,7 @@ extern "C" int moe_swiglu_grad(const uint16_t *h_bf16, const uint16_t *da_bf16, 
     if (R == 0) return MOE_OK;
     if (!al(h_bf16) || !al(da_bf16) || !al(dh_bf16) || ((uintptr_t)a_bf16 & 15)) return MOE_EINVAL;
     if ((w_rows && !w) || (w && w_n < (w_rows ? 1 : R)) || (dw && !w)) return MOE_EINVAL;
-    MOE_LAUNCH(K_GATED_GRAD, gated_grad_kernel, dim3((unsigned)(((long)R + 3) / 4)), dim3(256), 0,
+    MOE_LAUNCH(K_GATED_GRAD, gated_grad_kernel, blocks_of(((long)R + 3) / 4), dim3(256), 0,
                (hipStream_t)stream, h_bf16, da_bf16, w, w_rows, w_n, n_rows, R, I, dh_bf16, dw,
                a_bf16);
     return check_launch();
@@ -209,7 +218,7 @@ static int to_fp8(const uint16_t *x, const int32_t *n_rows, int R, int K, uint8_
     if (!al(x) || !q || ((uintptr_t)q & 7) || !s) return MOE_EINVAL;
     const long blocks = ((long)R * ((K + 127) / 128) + 15) / 16;
     if (!blocks_ok(blocks)) return MOE_EINVAL;
-    MOE_LAUNCH(K_TO_FP8, (to_fp8_kernel<GATED>), dim3((unsigned)blocks), dim3(256), 0,
+    MOE_LAUNCH(K_TO_FP8, (to_fp8_kernel<GATED>), blocks_of(blocks), dim3(256), 0,
                (hipStream_t)stream, x, n_rows, R, K, q, s);
     return check_launch();
 }

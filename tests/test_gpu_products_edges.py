@@ -84,3 +84,45 @@ def test_dw_row_without_a_partner_adds_nothing(path, side):
         lo += n
         err, bound = (dw[e].double() - a @ b).abs(), n * SUM * (a.abs() @ b.abs())
         assert bool((err <= bound).all()), f"expert {e}: {int((~(err <= bound)).sum())} values off"
+
+
+def _same_rows(got, want, rows, what):
+    for g, w in zip(got, want):
+        assert torch.equal(g[rows], w), what
+
+
+@pytest.mark.parametrize("call", ["swiglu", "swiglu_grad", "quant_fp8", "swiglu_quant_fp8"])
+def test_rows_whose_threads_pass_32_bits(call):
+    """More than 2^32 threads: the first rows, those around the 2^32nd thread and
+    the last ones have the bits that a call on these rows alone gives."""
+    # threads a row: I / 8 (swiglu), 64 (its gradient), 16 a block of 128 (FP8);
+    # bytes of tensors for each of a row's I values
+    R, I, per, size = {"swiglu": ((1 << 20) + 3, 32768, 4096, 6),
+                       "swiglu_grad": ((1 << 26) + 5, 8, 64, 11),
+                       "quant_fp8": ((1 << 28) + 77, 8, 16, 3.5),
+                       "swiglu_quant_fp8": ((1 << 28) + 77, 8, 16, 5.5)}[call]
+    assert R * per > 1 << 32
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < R * I * size + (1 << 30):
+        pytest.skip("not enough free memory")
+    g, edge = _gen(3), (1 << 32) // per
+    rows = torch.tensor(sorted({0, 1, edge // 2, edge - 1, edge, edge + 1, R - 2, R - 1}), device=DEV)
+    width = I if call == "quant_fp8" else 2 * I
+    small = _randn(g, len(rows), width)
+    h = torch.empty(R, width, device=DEV, dtype=torch.bfloat16)
+    h[rows] = small
+    if call == "swiglu":
+        _same_rows([P.swiglu(h)], [P.swiglu(small)], rows, call)
+    elif call == "swiglu_grad":
+        dsmall = _randn(g, len(rows), I)
+        da = torch.empty(R, I, device=DEV, dtype=torch.bfloat16)
+        da[rows] = dsmall
+        w = torch.rand(len(rows), generator=g, device=DEV)
+        wide = torch.empty(R, device=DEV)
+        wide[rows] = w
+        _same_rows(P.swiglu_grad(h, da, wide), P.swiglu_grad(small, dsmall, w), rows, call)
+    else:
+        fn = getattr(P, call)
+        (q, s), (qs, ss) = fn(h), fn(small)
+        _same_rows([q.view(torch.uint8), s], [qs.view(torch.uint8), ss], rows, call)
+    torch.cuda.empty_cache()
