@@ -106,7 +106,7 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
             const int mp = __builtin_amdgcn_readfirstlane(L.base[e + 1] - L.base[e]);
             const int li = ti - __builtin_amdgcn_readfirstlane(L.base[e]) * tq;
             group_of(A, e, lo, cnt);
-            half = 32 * ((cnt + 64 * mp - 1) / (64 * mp));
+            half = 32 * (int)((cnt + 64u * mp - 1) / (64u * mp));    // (cnt + cnt / 4 passes 2^31)
             place_of(li, mp, tq, p0, q0);
             p0 *= 2 * half;
         }

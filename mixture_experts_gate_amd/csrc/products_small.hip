@@ -68,7 +68,7 @@ __global__ __launch_bounds__(kTThreads) void product_small_kernel(ProductArgs A)
             const int mp = __builtin_amdgcn_readfirstlane(L.base[e + 1] - L.base[e]);
             const int li = ti - __builtin_amdgcn_readfirstlane(L.base[e]) * tq;
             group_of(A, e, lo, cnt);
-            half = 16 * ((cnt + 32 * mp - 1) / (32 * mp));
+            half = 16 * (int)((cnt + 32u * mp - 1) / (32u * mp));
             place_of(li, mp, tq, p0, q0);
             p0 *= 2 * half;
         }

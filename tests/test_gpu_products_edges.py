@@ -126,3 +126,33 @@ def test_rows_whose_threads_pass_32_bits(call):
         (q, s), (qs, ss) = fn(h), fn(small)
         _same_rows([q.view(torch.uint8), s], [qs.view(torch.uint8), ss], rows, call)
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", ["product", "dx", "fp8"])
+def test_products_of_nearly_the_most_rows(kind):
+    """One expert of 1.8e9 rows: the first, a middle and the last rows. Small
+    whole numbers, whose sums (at most 16 * 9) are exact in bf16."""
+    R, n = 1800 * 10 ** 6, 16
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < R * n * 4.5 + (1 << 30):
+        pytest.skip("not enough free memory")
+    g = _gen(4)
+    at = torch.tensor([0, 1, R // 3, R - 300, R - 2, R - 1], device=DEV)
+    few = torch.randint(-3, 4, (len(at), n), generator=g, device=DEV)
+    w = torch.randint(-3, 4, (1, n, n), generator=g, device=DEV)
+    ref = few.double() @ (w[0] if kind == "dx" else w[0].t().contiguous()).double()
+    out = torch.zeros(R, n, device=DEV, dtype=torch.bfloat16)
+    if kind == "fp8":
+        e4m3 = torch.float8_e4m3fn
+        x = torch.zeros(R, n, device=DEV, dtype=torch.uint8)
+        x[at] = few.to(torch.float32).to(e4m3).view(torch.uint8)
+        P.grouped_matmul_fp8(x, torch.ones(R, 1, device=DEV), w.to(torch.float32).to(e4m3),
+                             torch.ones(1, 1, 1, device=DEV), out=out)
+    else:
+        x = torch.zeros(R, n, device=DEV, dtype=torch.bfloat16)
+        x[at] = few.to(torch.bfloat16)
+        (P.grouped_matmul if kind == "product" else P.grouped_matmul_dx)(
+            x, w.to(torch.bfloat16), out=out)
+    assert torch.equal(out[at].double(), ref)
+    del x, out
+    torch.cuda.empty_cache()
