@@ -429,8 +429,9 @@ int moe_timing_query(int kernel_id, long long *launches, double *total_ms);
  * Sorted order: the R rows of all experts, grouped by expert; expert e owns
  * rows offsets[e] .. offsets[e+1]-1 (device [E+1], as moe_permute writes it).
  * offsets == NULL: one group of R rows (E must be 1). Rows at and past
- * offsets[E] are left as they are in every output. Offsets are kept inside
- * [0, R] whatever they hold.
+ * offsets[E] are left as they are in every output. Offsets ascend; each is kept
+ * inside [0, R] whatever it holds, and with offsets that do not ascend the
+ * outputs' rows 0 .. R-1 (dw) hold anything, and nothing else is read or written.
  * Row indices: an input matrix with rows != NULL gives row i of sorted order
  * its row rows[i] / div (rows = sorted_pair, div = k reads a pair's token);
  * without, row i. An output with rows != NULL takes row i at its row rows[i]

@@ -106,7 +106,9 @@ __global__ __launch_bounds__(kPThreads) void product_kernel(ProductArgs A) {
             const int mp = __builtin_amdgcn_readfirstlane(L.base[e + 1] - L.base[e]);
             const int li = ti - __builtin_amdgcn_readfirstlane(L.base[e]) * tq;
             group_of(A, e, lo, cnt);
-            half = 32 * (int)((cnt + 64u * mp - 1) / (64u * mp));    // (cnt + cnt / 4 passes 2^31)
+            // (cnt + cnt / 4 passes 2^31; more than 128 only where offsets do not ascend)
+            half = 32 * (int)((cnt + 64u * mp - 1) / (64u * mp));
+            half = half < 128 ? half : 128;
             place_of(li, mp, tq, p0, q0);
             p0 *= 2 * half;
         }

@@ -337,10 +337,11 @@ __device__ __forceinline__ void frags_t2(const uint32_t (&at)[4], u32x4 (&f)[4],
 }
 
 // p tiles before each expert (base[0 .. E]), for tiles of bp rows; by all THREADS
-// threads of a workgroup.
+// threads of a workgroup. No more than ascending offsets can give: with others
+// the sum could pass 32 bits, and tiles would have rows that do not exist.
 template <int THREADS>
 __device__ __forceinline__ void total_tiles(const ProductArgs &A, int bp, int *base, int *wsum) {
-    const int l = lane_id(), w = threadIdx.x / kWave;
+    const int l = lane_id(), w = threadIdx.x / kWave, most = A.R / bp + A.E;
     int run = 0;
     if (threadIdx.x == 0) base[0] = 0;
     for (int e0 = 0; e0 < A.E; e0 += THREADS) {
@@ -357,6 +358,7 @@ __device__ __forceinline__ void total_tiles(const ProductArgs &A, int bp, int *b
             const int o = __shfl_up(incl, d);
             if (l >= d) incl += o;
         }
+        incl = incl < most ? incl : most;      // (64 of at most 2^24 before)
         if (l == kWave - 1) wsum[w] = incl;
         __syncthreads();
         int before = run, all = run;
@@ -364,8 +366,8 @@ __device__ __forceinline__ void total_tiles(const ProductArgs &A, int bp, int *b
             before += i < w ? wsum[i] : 0;
             all += wsum[i];
         }
-        if (e < A.E) base[e + 1] = before + incl;
-        run = all;
+        if (e < A.E) base[e + 1] = before + incl < most ? before + incl : most;
+        run = all < most ? all : most;
         __syncthreads();
     }
 }

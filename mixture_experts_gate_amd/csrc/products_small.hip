@@ -69,6 +69,7 @@ __global__ __launch_bounds__(kTThreads) void product_small_kernel(ProductArgs A)
             const int li = ti - __builtin_amdgcn_readfirstlane(L.base[e]) * tq;
             group_of(A, e, lo, cnt);
             half = 16 * (int)((cnt + 32u * mp - 1) / (32u * mp));
+            half = half < 64 ? half : 64;
             place_of(li, mp, tq, p0, q0);
             p0 *= 2 * half;
         }

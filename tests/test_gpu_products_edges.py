@@ -156,3 +156,66 @@ def test_products_of_nearly_the_most_rows(kind):
     assert torch.equal(out[at].double(), ref)
     del x, out
     torch.cuda.empty_cache()
+
+
+def _guarded(rows, n, dtype):
+    """(a tensor [rows, n] of ones inside a larger one, a check that the rest is as it was)"""
+    big = torch.ones(rows + 600, n, device=DEV, dtype=dtype)
+
+    def rest():
+        return bool((big[:300] == 1).all()) and bool((big[300 + rows:] == 1).all())
+    return big[300:300 + rows], rest
+
+
+# R, E, N, K: the streaming kernel (K held in registers, copied), 128 x 128 tiles,
+# those in parts, 256 x 256 tiles
+ROW_PATHS = {"stream": (150, 16, 64, 256), "stream_long": (150, 16, 64, 4672),
+             "small": (400, 6, 136, 144), "parts": (261, 2, 112, 3648),
+             "large": (4000, 5, 2056, 1168)}
+
+
+@pytest.mark.parametrize("kind", ["product", "dx", "fp8", "dw"])
+@pytest.mark.parametrize("path", list(ROW_PATHS))
+def test_offsets_that_do_not_ascend_stay_inside(path, kind):
+    R, E, N, K = ROW_PATHS[path]
+    g = _gen(len(path))
+    dy, x, w = _randn(g, R, N), _randn(g, R, K), _randn(g, E, N, K)
+    for seed in range(4):
+        h = torch.randint(-R, 2 * R, (E + 1,), generator=g, device=DEV).to(torch.int32)
+        if seed == 3:
+            h[0::2], h[1::2] = 0, R
+        if kind == "dw":
+            out, rest = _guarded(E * N, K, torch.float32)
+            P.grouped_matmul_dw(dy, x, h, out=out.view(E, N, K))
+        else:
+            out, rest = _guarded(R, K if kind == "dx" else N, torch.bfloat16)
+            if kind == "fp8":
+                x8, s8 = P.quant_fp8(x)
+                w8 = w.view(torch.uint8)[:, :, ::2].contiguous() & 0x3F
+                P.grouped_matmul_fp8(x8, s8, w8, torch.ones(E, -(-N // 128), -(-K // 128), device=DEV),
+                                     h, out=out)
+            else:
+                (P.grouped_matmul if kind == "product" else P.grouped_matmul_dx)(
+                    x if kind == "product" else dy, w, h, out=out)
+        assert rest(), (seed, h.tolist())
+
+
+def test_offsets_whose_tiles_pass_32_bits():
+    """256 of 512 experts that claim all of 2^29 rows: 2^29 tiles of 256 rows, and
+    their total is cut to what ascending offsets can give."""
+    R, E, n = 1 << 29, 512, 8
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < R * n * 5:
+        pytest.skip("not enough free memory")
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    off[1::2] = R
+    x = torch.ones(R, n, device=DEV, dtype=torch.bfloat16)
+    w = torch.ones(E, n, n, device=DEV, dtype=torch.bfloat16)
+    out, rest = _guarded(R, n, torch.bfloat16)
+    for fn in (P.grouped_matmul, P.grouped_matmul_dx):
+        out.fill_(1)
+        fn(x, w, off, out=out)
+        # (the first expert's rows are all of them: every row is computed)
+        assert rest() and bool((out == 8).all())
+    del x, out, rest
+    torch.cuda.empty_cache()
