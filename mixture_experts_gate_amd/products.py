@@ -66,8 +66,8 @@ def _need(t, name, dtypes, dev=None):
 
 
 def _int(n, name):
-    """n, as the library's 32-bit int takes it."""
-    if n > 0x7FFFFFFF:
+    """n, as the library's 32-bit int takes it (ctypes would cut it to that)."""
+    if not -0x80000000 <= n <= 0x7FFFFFFF:
         _fail(f"{name}: {n} is past 32 bits")
     return n
 
@@ -84,6 +84,8 @@ def _weights(w, ws, dtype, dev):
     if isinstance(w, TableMatrices):
         if w.mat not in (_lib.MOE_MAT_W13, _lib.MOE_MAT_W2):
             _fail(f"w.mat: {w.mat}")
+        for n, name in zip(w[2:], ("w.E", "w.N", "w.K")):
+            _int(n, name)
         if ws is not None:
             _fail("w_scale: the table of w has the scales")
         if isinstance(w.table, torch.Tensor):
@@ -207,7 +209,7 @@ def grouped_matmul(x, w, offsets=None, *, rows=None, div=1, out_rows=None, out=N
     R = _count(x, rows, "rows")
     out = _rows_output(out, "out", R, N, out_rows, _OUT, dev, stream)
     ws, pws, nws = _workspace(_lib.MOE_GEMM_BF16, R, N, K, E, dev, stream)
-    _run("moe_grouped_gemm", dev, stream, x.data_ptr(), _index(rows, "rows", R, dev), div,
+    _run("moe_grouped_gemm", dev, stream, x.data_ptr(), _index(rows, "rows", R, dev), _int(div, "div"),
          x.shape[0], _offsets(offsets, E, dev), pw, tab, mat, R, N, K, E, out.data_ptr(),
          _index(out_rows, "out_rows", R, dev), out.shape[0],
          int(out.dtype is torch.float32), pws, nws)
@@ -230,7 +232,7 @@ def grouped_matmul_fp8(x, x_scale, w, w_scale=None, offsets=None, *, rows=None, 
     out = _rows_output(out, "out", R, N, out_rows, _OUT, dev, stream)
     ws, pws, nws = _workspace(_lib.MOE_GEMM_FP8, R, N, K, E, dev, stream)
     _run("moe_grouped_gemm_fp8", dev, stream, x.data_ptr(), x_scale.data_ptr(),
-         _index(rows, "rows", R, dev), div, x.shape[0], _offsets(offsets, E, dev), pw, ps, tab,
+         _index(rows, "rows", R, dev), _int(div, "div"), x.shape[0], _offsets(offsets, E, dev), pw, ps, tab,
          mat, R, N, K, E, out.data_ptr(), _index(out_rows, "out_rows", R, dev), out.shape[0],
          int(out.dtype is torch.float32), pws, nws)
     return out
@@ -247,7 +249,7 @@ def grouped_matmul_dx(dy, w, offsets=None, *, rows=None, div=1, out_rows=None, o
     R = _count(dy, rows, "rows")
     out = _rows_output(out, "out", R, K, out_rows, _OUT, dev, stream)
     ws, pws, nws = _workspace(_lib.MOE_GEMM_DX, R, N, K, E, dev, stream)
-    _run("moe_grouped_gemm_dx", dev, stream, dy.data_ptr(), _index(rows, "rows", R, dev), div,
+    _run("moe_grouped_gemm_dx", dev, stream, dy.data_ptr(), _index(rows, "rows", R, dev), _int(div, "div"),
          dy.shape[0], _offsets(offsets, E, dev), pw, tab, mat, R, N, K, E, out.data_ptr(),
          _index(out_rows, "out_rows", R, dev), out.shape[0],
          int(out.dtype is torch.float32), pws, nws)
@@ -273,8 +275,8 @@ def grouped_matmul_dw(dy, x, offsets=None, *, dy_rows=None, dy_div=1, x_rows=Non
         _fail(f"out: {tuple(out.shape)}, [{E}, {N}, {K}] is needed")
     ws, pws, nws = _workspace(_lib.MOE_GEMM_DW, R, N, K, E, dev, stream)
     _run("moe_grouped_gemm_dw", dev, stream, dy.data_ptr(), _index(dy_rows, "dy_rows", R, dev),
-         dy_div, dy.shape[0], x.data_ptr(), _index(x_rows, "x_rows", R, dev), x_div, x.shape[0],
-         _offsets(offsets, E, dev), R, N, K, E, out.data_ptr(), int(out.dtype is torch.float32),
+         _int(dy_div, "dy_div"), dy.shape[0], x.data_ptr(), _index(x_rows, "x_rows", R, dev),
+         _int(x_div, "x_div"), x.shape[0], _offsets(offsets, E, dev), R, N, K, E, out.data_ptr(), int(out.dtype is torch.float32),
          int(bool(accumulate)), pws, nws)
     return out
 

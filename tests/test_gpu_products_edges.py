@@ -219,3 +219,27 @@ def test_offsets_whose_tiles_pass_32_bits():
         assert rest() and bool((out == 8).all())
     del x, out, rest
     torch.cuda.empty_cache()
+
+
+def test_whole_numbers_past_32_bits_are_refused():
+    """Divisors and sizes of a table's matrices that an int would cut to a valid one."""
+    x, w = _randn(_gen(1), 4, 16), _randn(_gen(2), 1, 8, 16)
+    rows = torch.arange(4, dtype=torch.int32, device=DEV)
+    dy, big = _randn(_gen(3), 4, 8), 2 ** 32
+    tab = torch.tensor([w.data_ptr(), 0, 0, 0], dtype=torch.int64, device=DEV)
+    ok = P.TableMatrices(tab, _lib.MOE_MAT_W13, 1, 8, 16)
+    assert torch.equal(P.grouped_matmul(x, ok), P.grouped_matmul(x, w))
+    for div in (big + 1, 1 - big):
+        for bad in (lambda: P.grouped_matmul(x, w, rows=rows, div=div),
+                    lambda: P.grouped_matmul_dx(dy, w, rows=rows, div=div),
+                    lambda: P.grouped_matmul_dw(dy, x, dy_rows=rows, dy_div=div),
+                    lambda: P.grouped_matmul_dw(dy, x, x_rows=rows, x_div=div),
+                    lambda: P.grouped_matmul_fp8(*P.quant_fp8(x), w.view(torch.uint8)[:, :, ::2].contiguous(),
+                                                 torch.ones(1, 1, 1, device=DEV), rows=rows, div=div)):
+            with pytest.raises(ValueError):
+                bad()
+    for bad in (ok._replace(E=big + 1), ok._replace(N=big + 8), ok._replace(K=big + 16)):
+        with pytest.raises(ValueError):
+            P.grouped_matmul(x, bad)
+        with pytest.raises(ValueError):
+            P._weights(bad, None, P._BF16, 0)
