@@ -367,7 +367,8 @@ class Fp8BlockLayer:
     (blobs of ``blob_layout(H, I, "fp8_block")``), with at most T_max tokens:
     route and permute, the tokens to FP8 with a scale per 128 columns, the
     gate/up product, silu(g) u to FP8, the down product and the combine. H and I
-    are multiples of 32.
+    are multiples of 32. For inference: inputs that require grad are refused
+    where gradients are enabled.
 
     ``table`` is a device table of moe_expert_w, as ``expert_table`` makes it
     for resident experts or ``ExpertCache.prefetch`` returns it."""
@@ -440,6 +441,7 @@ class Fp8BlockLayer:
                     or not t.is_contiguous() or not t.is_cuda or t.device != self.out.device):
                 raise ValueError(f"{name}: contiguous {dtype} [{n}, {cols}] on {self.out.device} "
                                  "is needed")
+        products._no_history(x, logits, wg)
         if x.get_device() != torch.cuda.current_device():
             with torch.cuda.device(x.device):
                 return self.forward(T, x, table, logits, wg, shared_table, renormalize, stream)

@@ -18,6 +18,11 @@ read through ``rows`` (int32 [R]) gives sorted row i its row ``rows[i] // div``:
 rows with an index outside their matrix are left as they are in the output.
 Outputs must not overlap inputs.
 
+The calls record nothing for autograd: where gradients are enabled, an input that
+requires one is refused, since its gradient would be lost without a word. Call
+them under ``torch.no_grad()`` or from a ``torch.autograd.Function`` (the
+gradients are calls of their own).
+
 Matrices ``w`` are a tensor [E, N, K] (or [N, K] for one group), or
 ``TableMatrices`` for those a device table of ``moe_expert_w`` points to (an
 expert cache's, or ``expert_table``'s).
@@ -70,6 +75,15 @@ def _int(n, name):
     if not -0x80000000 <= n <= 0x7FFFFFFF:
         _fail(f"{name}: {n} is past 32 bits")
     return n
+
+
+def _no_history(*inputs):
+    """Refuses inputs whose gradient autograd would be expected to find."""
+    if torch.is_grad_enabled():
+        for t in inputs:
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                _fail("an input requires grad, and the result carries no history for autograd: "
+                      "call under torch.no_grad() (the gradients are calls of their own)")
 
 
 def _matrix(t, name, dtype, dev=None):
@@ -203,6 +217,7 @@ def grouped_matmul(x, w, offsets=None, *, rows=None, div=1, out_rows=None, out=N
     """y[i] = W_e x[i] over sorted rows: x bf16 [n, K], w bf16 -> [R, N] (``out``
     may be bf16, the default, or fp32). N and K are multiples of 8."""
     dev = _matrix(x, "x", _BF16).get_device()
+    _no_history(x, w)
     pw, _, tab, mat, E, N, K = _weights(w, None, _BF16, dev)
     if x.shape[1] != K:
         _fail(f"x: {x.shape[1]} columns, w has {K}")
@@ -223,6 +238,7 @@ def grouped_matmul_fp8(x, x_scale, w, w_scale=None, offsets=None, *, rows=None, 
     ``quant_fp8``), w E4M3 with fp32 scales [E, ceil(N/128), ceil(K/128)] ->
     [R, N] bf16 or fp32. N is a multiple of 8, K of 16."""
     dev = _matrix(x, "x", _FP8).get_device()
+    _no_history(x, x_scale, w, w_scale)
     pw, ps, tab, mat, E, N, K = _weights(w, w_scale, _FP8, dev)
     if x.shape[1] != K:
         _fail(f"x: {x.shape[1]} columns, w has {K}")
@@ -243,6 +259,7 @@ def grouped_matmul_dx(dy, w, offsets=None, *, rows=None, div=1, out_rows=None, o
     """dx[i] = W_e^T dy[i] over sorted rows: dy bf16 [n, N], w bf16 -> [R, K]
     bf16 or fp32; ``rows``/``div`` index dy, ``out_rows`` dx."""
     dev = _matrix(dy, "dy", _BF16).get_device()
+    _no_history(dy, w)
     pw, _, tab, mat, E, N, K = _weights(w, None, _BF16, dev)
     if dy.shape[1] != N:
         _fail(f"dy: {dy.shape[1]} columns, w has {N} rows")
@@ -263,6 +280,7 @@ def grouped_matmul_dw(dy, x, offsets=None, *, dy_rows=None, dy_div=1, x_rows=Non
     for an expert without rows. ``accumulate`` adds to fp32 ``out``."""
     dev = _matrix(dy, "dy", _BF16).get_device()
     _matrix(x, "x", _BF16, dev)
+    _no_history(dy, x)
     N, K = dy.shape[1], x.shape[1]
     R = _count(dy, dy_rows, "dy_rows")
     if _count(x, x_rows, "x_rows") != R:
@@ -312,6 +330,7 @@ def swiglu(h, w=None, w_rows=None, n_rows=None, out=None, stream=None):
     ``w``). ``n_rows`` (int32 [1] on the device, e.g. ``offsets[E:]``): only the
     rows below it. I is a multiple of 8."""
     R, I, dev = _halves(h)
+    _no_history(h, w)
     pw, pr, wn = _row_weights(w, w_rows, R, dev)
     out = _rows_output(out, "out", R, I, None, _BF16, dev, stream)
     _run("moe_swiglu", dev, stream, h.data_ptr(), pw, pr, wn, _limit(n_rows, dev), R, I,
@@ -327,6 +346,7 @@ def swiglu_grad(h, da, w=None, w_rows=None, n_rows=None, dh=None, dw=None, a=Non
     R, I, dev = _halves(h)
     if _matrix(da, "da", _BF16, dev).shape != (R, I):
         _fail(f"da: {tuple(da.shape)}, [{R}, {I}] is needed")
+    _no_history(h, da, w)
     pw, pr, wn = _row_weights(w, w_rows, R, dev)
     dh = _rows_output(dh, "dh", R, 2 * I, None, _BF16, dev, stream)
     if w is not None:
@@ -360,10 +380,12 @@ def quant_fp8(x, n_rows=None, q=None, s=None, stream=None):
     scale = max(amax, 2^-100) / 448 over 128 columns of a row, code = x / scale
     to the nearest E4M3. K is a multiple of 8."""
     dev = _matrix(x, "x", _BF16).get_device()
+    _no_history(x)
     return _to_fp8("moe_quant_fp8", x, x.shape[0], x.shape[1], n_rows, q, s, dev, stream)
 
 
 def swiglu_quant_fp8(h, n_rows=None, q=None, s=None, stream=None):
     """``quant_fp8`` of the fp32 values silu(g) u of rows h [R, 2I] = [g | u]."""
     R, I, dev = _halves(h)
+    _no_history(h)
     return _to_fp8("moe_swiglu_quant_fp8", h, R, I, n_rows, q, s, dev, stream)

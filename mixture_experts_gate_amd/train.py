@@ -18,7 +18,11 @@ class TrainExperts:
     """Buffers and call sequence for at most T_max tokens. ``forward`` keeps what
     ``backward`` needs: its inputs must be unchanged until then, and one
     backward belongs to the last forward. Both run on the current stream and
-    allocate nothing, so a training step can be captured into a graph."""
+    allocate nothing, so a training step can be captured into a graph.
+
+    Autograd is not involved: the gradients are ``backward``'s results, and
+    ``forward`` refuses inputs that require grad where gradients are enabled
+    (call it under ``torch.no_grad()``, or from a ``torch.autograd.Function``)."""
 
     def __init__(self, H, E, k, I, T_max, device="cuda"):
         self.H, self.E, self.k, self.I, self.T_max = H, E, k, I, T_max
@@ -57,6 +61,7 @@ class TrainExperts:
         for t, name, dtype in ((topk_ids, "topk_ids", torch.int32), (topk_w, "topk_w", torch.float32)):
             if t.shape != (T, k) or t.dtype != dtype or not t.is_contiguous() or t.device != x.device:
                 raise ValueError(f"{name}: contiguous {dtype} [{T}, {k}] on {x.device} is needed")
+        P._no_history(x, topk_w, w13, w2)
         if w13.shape != (self.E, 2 * self.I, self.H) or w2.shape != (self.E, self.H, self.I):
             raise ValueError(f"w13, w2: {tuple(w13.shape)}, {tuple(w2.shape)}")
         n = T * k
@@ -73,6 +78,7 @@ class TrainExperts:
         self._saved = (x, topk_w, w13, w2)
         return self.out[:T]
 
+    @torch.no_grad()
     def backward(self, dout, accumulate=False):
         """(dx [T, H] bf16, dtopk_w [T, k] fp32, dw13, dw2 fp32) of the last
         forward for dout [T, H] bf16; with ``accumulate`` the matrices' gradients

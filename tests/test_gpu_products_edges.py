@@ -10,6 +10,8 @@ import pytest
 import torch
 
 from mixture_experts_gate_amd import _lib, products as P
+from mixture_experts_gate_amd.layer import Fp8BlockLayer
+from mixture_experts_gate_amd.train import TrainExperts
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -243,3 +245,85 @@ def test_whole_numbers_past_32_bits_are_refused():
             P.grouped_matmul(x, bad)
         with pytest.raises(ValueError):
             P._weights(bad, None, P._BF16, 0)
+
+
+# ------------------------------------------------------------------ autograd --
+
+def test_inputs_that_require_grad_are_refused():
+    """Where gradients are enabled, by every call and for every input that has
+    one; under no_grad the results are those of the plain tensors."""
+    g = _gen(12)
+    x, w, dy = _randn(g, 6, 32), _randn(g, 2, 16, 32), _randn(g, 6, 16)
+    off, wt = _offsets([2, 4]), torch.rand(6, generator=g, device=DEV)
+    w8, ws = w.view(torch.uint8)[:, :, ::2].contiguous(), torch.ones(2, 1, 1, device=DEV)
+    x8, xs = P.quant_fp8(x)
+    da = _randn(g, 6, 16)
+    calls = [(lambda a, b: P.grouped_matmul(a, b, off), (x, w)),
+             (lambda a, b: P.grouped_matmul_dx(a, b, off), (dy, w)),
+             (lambda a, b: P.grouped_matmul_dw(a, b, off), (dy, x)),
+             (lambda a, b: P.grouped_matmul_fp8(x8, a, w8, b, off), (xs, ws)),
+             (lambda a, b: P.swiglu(a, b), (x, wt)),
+             (lambda a, b, c: P.swiglu_grad(a, b, c), (x, da, wt)),
+             (lambda a: P.quant_fp8(a), (x,)), (lambda a: P.swiglu_quant_fp8(a), (x,))]
+    for call, inputs in calls:
+        want = call(*inputs)
+        for i in range(len(inputs)):
+            leaf = [t.detach().requires_grad_(j == i) for j, t in enumerate(inputs)]
+            with pytest.raises(ValueError, match="grad"):
+                call(*leaf)
+            with torch.no_grad():
+                got = call(*leaf)
+            for a, b in zip(*((r if isinstance(r, tuple) else (r,)) for r in (got, want))):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_product_inside_an_autograd_function():
+    """The calls as forward and backward of a Function give autograd the product's
+    gradients."""
+    class Product(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, off):
+            ctx.save_for_backward(x, w, off)
+            return P.grouped_matmul(x, w, off)
+
+        @staticmethod
+        def backward(ctx, dy):
+            x, w, off = ctx.saved_tensors
+            dw = torch.empty_like(w)
+            return (P.grouped_matmul_dx(dy, w, off), P.grouped_matmul_dw(dy, x, off, out=dw), None)
+
+    g = _gen(13)
+    x, w, dy = _randn(g, 40, 32), _randn(g, 2, 16, 32), _randn(g, 40, 16)
+    off = _offsets([15, 25])
+    x.requires_grad_(), w.requires_grad_()
+    Product.apply(x, w, off).backward(dy)
+    with torch.no_grad():
+        assert torch.equal(x.grad, P.grouped_matmul_dx(dy, w, off))
+        out = torch.empty_like(w)
+        assert torch.equal(w.grad, P.grouped_matmul_dw(dy, x, off, out=out))
+
+
+def test_layers_refuse_inputs_that_require_grad():
+    g = _gen(14)
+    T, E, k, H, I = 5, 4, 2, 64, 32
+    x, wg = _randn(g, T, H), _randn(g, E, H)
+    w13, w2 = _randn(g, E, 2 * I, H), _randn(g, E, H, I)
+    ids = torch.tensor([[0, 1], [2, 3], [1, 2], [3, 0], [0, 2]], dtype=torch.int32, device=DEV)
+    w, dout = torch.rand(T, k, generator=g, device=DEV), _randn(g, T, H)
+    m = TrainExperts(H, E, k, I, T)
+    want = m.forward(x, ids, w, w13, w2).clone()
+    grads = [t.clone() for t in m.backward(dout)]
+    for i in range(4):
+        args = [t.detach().requires_grad_(j == i) for j, t in enumerate((x, w, w13, w2))]
+        with pytest.raises(ValueError, match="grad"):
+            m.forward(args[0], ids, *args[1:])
+        with torch.no_grad():
+            assert torch.equal(m.forward(args[0], ids, *args[1:]), want)
+        # (backward's results are the gradients: it runs where gradients are enabled)
+        assert all(torch.equal(a, b) for a, b in zip(m.backward(dout), grads))
+    layer = Fp8BlockLayer(H, E, k, I, T)
+    zeros = torch.zeros(2 * I * H, dtype=torch.uint8, device=DEV)      # codes and scales of all
+    table = torch.full((E, 4), zeros.data_ptr(), dtype=torch.int64, device=DEV)
+    for kw in (dict(x=x.detach().requires_grad_(), wg=wg), dict(x=x, wg=wg.detach().requires_grad_())):
+        with pytest.raises(ValueError, match="grad"):
+            layer.forward(T, table=table, **kw)
