@@ -5,8 +5,15 @@ with a scale per 128 x 128 block: the products grouped by expert, the gated
 activation between them with its gradient, and rows to FP8. Every call checks
 its tensors (types, shapes, contiguity, one device), allocates what it is not
 given, and enqueues one kernel of ``libmoe.so`` on the current stream of the
-tensors' device, or on ``stream`` (two kernels and a workspace for a product
-whose sums are cut into parts). Nothing is computed by PyTorch.
+tensors' device, or on ``stream`` (a torch stream or the handle of one). Nothing
+is computed by PyTorch, but for the zeros of a ``dw`` that ``swiglu_grad`` makes.
+
+A product with few output tiles and a long sum cuts it into parts, which a
+second kernel adds up, where it has a workspace (``ws``, uint8; the bytes are
+``_lib.moe_grouped_gemm_workspace``'s, at most ``workspace_bound``'s). One that
+is not given is allocated, except with a stream handle, with which nothing is:
+without ``ws``, or with a smaller one, the sum runs whole, which takes longer and
+rounds in another order. Calls that may overlap need workspaces of their own.
 
 Rows are in *sorted order*: grouped by expert, expert e owning rows
 ``offsets[e]`` .. ``offsets[e+1] - 1`` (``offsets`` int32 [E+1] on the device,
@@ -175,8 +182,20 @@ _calls = {}      # the library's functions, once looked up
 _sizes = {}      # workspace bytes by (kind, R, N, K, E, GPU)
 
 
-def _workspace(kind, R, N, K, E, dev, stream):
+def workspace_bound(R, N, K, E, device="cuda"):
+    """Bytes of workspace that suffice for every product of at most R rows with
+    matrices [E, N, K], gradients among them: sums are cut into at most 16
+    parts, and their tiles of 128 x 128 fp32 are at most two a compute unit."""
+    device = torch.device(device)
+    cu = torch.cuda.get_device_properties(device).multi_processor_count if device.type == "cuda" else 256
+    return min(16 * 4 * max(R * max(N, K), E * N * K), 2 * cu * 128 * 128 * 4)
+
+
+def _workspace(kind, R, N, K, E, dev, stream, ws):
     """(tensor or None, address, bytes) of the workspace the product can use."""
+    if ws is not None:
+        _need(ws, "ws", (torch.uint8,), dev)
+        return ws, ws.data_ptr(), ws.numel()
     key = (kind, R, N, K, E, dev)
     n = _sizes.get(key)
     if n is None:
@@ -213,7 +232,8 @@ def _run(fn, dev, stream, *args):
         _lib._check(fn, rc)
 
 
-def grouped_matmul(x, w, offsets=None, *, rows=None, div=1, out_rows=None, out=None, stream=None):
+def grouped_matmul(x, w, offsets=None, *, rows=None, div=1, out_rows=None, out=None, ws=None,
+                   stream=None):
     """y[i] = W_e x[i] over sorted rows: x bf16 [n, K], w bf16 -> [R, N] (``out``
     may be bf16, the default, or fp32). N and K are multiples of 8."""
     dev = _matrix(x, "x", _BF16).get_device()
@@ -223,7 +243,7 @@ def grouped_matmul(x, w, offsets=None, *, rows=None, div=1, out_rows=None, out=N
         _fail(f"x: {x.shape[1]} columns, w has {K}")
     R = _count(x, rows, "rows")
     out = _rows_output(out, "out", R, N, out_rows, _OUT, dev, stream)
-    ws, pws, nws = _workspace(_lib.MOE_GEMM_BF16, R, N, K, E, dev, stream)
+    ws, pws, nws = _workspace(_lib.MOE_GEMM_BF16, R, N, K, E, dev, stream, ws)
     _run("moe_grouped_gemm", dev, stream, x.data_ptr(), _index(rows, "rows", R, dev), _int(div, "div"),
          x.shape[0], _offsets(offsets, E, dev), pw, tab, mat, R, N, K, E, out.data_ptr(),
          _index(out_rows, "out_rows", R, dev), out.shape[0],
@@ -232,7 +252,7 @@ def grouped_matmul(x, w, offsets=None, *, rows=None, div=1, out_rows=None, out=N
 
 
 def grouped_matmul_fp8(x, x_scale, w, w_scale=None, offsets=None, *, rows=None, div=1,
-                       out_rows=None, out=None, stream=None):
+                       out_rows=None, out=None, ws=None, stream=None):
     """y[i] = W_e x[i] over sorted rows from block-scaled FP8: x E4M3 [n, K]
     (float8_e4m3fn or uint8 codes) with fp32 scales [n, ceil(K/128)] (from
     ``quant_fp8``), w E4M3 with fp32 scales [E, ceil(N/128), ceil(K/128)] ->
@@ -246,7 +266,7 @@ def grouped_matmul_fp8(x, x_scale, w, w_scale=None, offsets=None, *, rows=None, 
         _fail(f"x_scale: {tuple(x_scale.shape)}, [{x.shape[0]}, {-(-K // 128)}] is needed")
     R = _count(x, rows, "rows")
     out = _rows_output(out, "out", R, N, out_rows, _OUT, dev, stream)
-    ws, pws, nws = _workspace(_lib.MOE_GEMM_FP8, R, N, K, E, dev, stream)
+    ws, pws, nws = _workspace(_lib.MOE_GEMM_FP8, R, N, K, E, dev, stream, ws)
     _run("moe_grouped_gemm_fp8", dev, stream, x.data_ptr(), x_scale.data_ptr(),
          _index(rows, "rows", R, dev), _int(div, "div"), x.shape[0], _offsets(offsets, E, dev), pw, ps, tab,
          mat, R, N, K, E, out.data_ptr(), _index(out_rows, "out_rows", R, dev), out.shape[0],
@@ -255,7 +275,7 @@ def grouped_matmul_fp8(x, x_scale, w, w_scale=None, offsets=None, *, rows=None, 
 
 
 def grouped_matmul_dx(dy, w, offsets=None, *, rows=None, div=1, out_rows=None, out=None,
-                      stream=None):
+                      ws=None, stream=None):
     """dx[i] = W_e^T dy[i] over sorted rows: dy bf16 [n, N], w bf16 -> [R, K]
     bf16 or fp32; ``rows``/``div`` index dy, ``out_rows`` dx."""
     dev = _matrix(dy, "dy", _BF16).get_device()
@@ -265,7 +285,7 @@ def grouped_matmul_dx(dy, w, offsets=None, *, rows=None, div=1, out_rows=None, o
         _fail(f"dy: {dy.shape[1]} columns, w has {N} rows")
     R = _count(dy, rows, "rows")
     out = _rows_output(out, "out", R, K, out_rows, _OUT, dev, stream)
-    ws, pws, nws = _workspace(_lib.MOE_GEMM_DX, R, N, K, E, dev, stream)
+    ws, pws, nws = _workspace(_lib.MOE_GEMM_DX, R, N, K, E, dev, stream, ws)
     _run("moe_grouped_gemm_dx", dev, stream, dy.data_ptr(), _index(rows, "rows", R, dev), _int(div, "div"),
          dy.shape[0], _offsets(offsets, E, dev), pw, tab, mat, R, N, K, E, out.data_ptr(),
          _index(out_rows, "out_rows", R, dev), out.shape[0],
@@ -274,7 +294,7 @@ def grouped_matmul_dx(dy, w, offsets=None, *, rows=None, div=1, out_rows=None, o
 
 
 def grouped_matmul_dw(dy, x, offsets=None, *, dy_rows=None, dy_div=1, x_rows=None, x_div=1,
-                      out=None, accumulate=False, stream=None):
+                      out=None, accumulate=False, ws=None, stream=None):
     """dW_e = sum over the expert's sorted rows i of dy[i] x[i]^T: dy bf16
     [n, N], x bf16 [m, K] -> [E, N, K] fp32 (or bf16, given as ``out``); zeros
     for an expert without rows. ``accumulate`` adds to fp32 ``out``."""
@@ -291,7 +311,7 @@ def grouped_matmul_dw(dy, x, offsets=None, *, dy_rows=None, dy_div=1, x_rows=Non
     out = _output(out, "out", (E, N, K), (torch.float32, torch.bfloat16), dev, stream)
     if out.shape[-2:] != (N, K) or out.numel() != E * N * K:
         _fail(f"out: {tuple(out.shape)}, [{E}, {N}, {K}] is needed")
-    ws, pws, nws = _workspace(_lib.MOE_GEMM_DW, R, N, K, E, dev, stream)
+    ws, pws, nws = _workspace(_lib.MOE_GEMM_DW, R, N, K, E, dev, stream, ws)
     _run("moe_grouped_gemm_dw", dev, stream, dy.data_ptr(), _index(dy_rows, "dy_rows", R, dev),
          _int(dy_div, "dy_div"), dy.shape[0], x.data_ptr(), _index(x_rows, "x_rows", R, dev),
          _int(x_div, "x_div"), x.shape[0], _offsets(offsets, E, dev), R, N, K, E, out.data_ptr(), int(out.dtype is torch.float32),

@@ -327,3 +327,73 @@ def test_layers_refuse_inputs_that_require_grad():
     for kw in (dict(x=x.detach().requires_grad_(), wg=wg), dict(x=x, wg=wg.detach().requires_grad_())):
         with pytest.raises(ValueError, match="grad"):
             layer.forward(T, table=table, **kw)
+
+
+# ---------------------------------------------------- workspaces and streams --
+
+# kind, R, N, K, E of products whose sums are cut
+CUT = {"product": (_lib.MOE_GEMM_BF16, 261, 112, 3648, 1), "dx": (_lib.MOE_GEMM_DX, 300, 2048, 64, 2),
+       "fp8": (_lib.MOE_GEMM_FP8, 261, 112, 3648, 1), "dw": (_lib.MOE_GEMM_DW, 1500, 256, 136, 1)}
+
+
+@pytest.mark.parametrize("kind", list(CUT))
+def test_stream_handle_and_given_workspace(kind):
+    """A call with a workspace has the same bits on a stream, through its handle
+    and with the workspace given; without one the sum runs whole: the same value
+    within the two orders' errors. Nothing is written past the workspace."""
+    gemm, R, N, K, E = CUT[kind]
+    size = _lib.moe_grouped_gemm_workspace(gemm, R, N, K, E)
+    assert 0 < size <= P.workspace_bound(R, N, K, E)
+    g = _gen(31)
+    x, w, dy = _randn(g, R, K), _randn(g, E, N, K), _randn(g, R, N)
+    off = _offsets([R // E] * E)
+    x8, xs = P.quant_fp8(x)
+    w8, ws8 = P.quant_fp8(w.view(E * N, K))
+    ws8 = torch.rand(E, -(-N // 128), -(-K // 128), generator=g, device=DEV)
+    shape = {"product": (R, N), "fp8": (R, N), "dx": (R, K), "dw": (E, N, K)}[kind]
+
+    def call(**kw):
+        out = torch.zeros(shape, device=DEV)
+        torch.cuda.synchronize()
+        if kind == "product":
+            P.grouped_matmul(x, w, off, out=out, **kw)
+        elif kind == "dx":
+            P.grouped_matmul_dx(dy, w, off, out=out, **kw)
+        elif kind == "dw":
+            P.grouped_matmul_dw(dy, x, off, out=out, **kw)
+        else:
+            P.grouped_matmul_fp8(x8, xs, w8.view(E, N, K), ws8, off, out=out, **kw)
+        torch.cuda.synchronize()
+        return out
+
+    want, side = call(), torch.cuda.Stream()
+    big = torch.full((size + 512,), 0x5A, dtype=torch.uint8, device=DEV)
+    ws = big[256:256 + size]
+    assert torch.equal(call(stream=side), want)
+    assert torch.equal(call(ws=ws), want)
+    assert torch.equal(call(ws=ws, stream=side.cuda_stream), want)
+    assert bool((big[:256] == 0x5A).all()) and bool((big[256 + size:] == 0x5A).all())
+    whole = call(stream=side.cuda_stream)
+    assert torch.equal(call(ws=ws[:size - 16]), whole)
+    # each order's additions (one a term): n 2^-23 of the magnitudes, and for FP8 the
+    # scaled sums' 3 2^-24 a term (the instruction's own sums are the same)
+    if kind == "dw":
+        mag, n = dy.double().abs().t().contiguous() @ x.double().abs(), R
+    elif kind == "fp8":
+        a = x8.float().double().abs() * xs.double().repeat_interleave(128, 1)[:, :K]
+        b = w8.float().double().abs() * ws8[0].double().repeat_interleave(128, 0)[:N].repeat_interleave(
+            128, 1)[:, :K]
+        mag, n = a @ b.t().contiguous(), K + 3
+    else:
+        parts = []
+        for e in range(E):
+            a = (x if kind == "product" else dy).double().abs()[e * (R // E):(e + 1) * (R // E)]
+            b = w[e].double().abs()
+            parts.append(a @ (b.t().contiguous() if kind == "product" else b))
+        mag, n = torch.cat(parts), K if kind == "product" else N
+    assert bool(((whole.double() - want.double()).abs() <= 2 * n * SUM * mag).all())
+    for bad in (ws.view(torch.float32), ws[::2], ws.cpu()):
+        with pytest.raises(ValueError):
+            call(ws=bad)
+    with pytest.raises(_lib.MoeError):
+        call(ws=big[8:8 + size])

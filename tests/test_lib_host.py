@@ -326,3 +326,20 @@ def test_product_layers_need_device_tensors():
     layer = Fp8BlockLayer(64, 4, 2, 32, 4, device="cpu")
     with pytest.raises(ValueError):
         layer.forward(4, x, None, logits=torch.zeros(4, 4))
+
+
+def test_product_workspaces_are_within_their_bound(lib):
+    """workspace_bound(R, ...) suffices for every product of at most R rows."""
+    import random
+    from mixture_experts_gate_amd import products as P
+    rng, cut = random.Random(5), 0
+    for _ in range(4000):
+        R, E = int(2 ** rng.uniform(0, 15)), rng.choice((1, 1, 2, 8, 64, 300))
+        N, K = 16 * int(2 ** rng.uniform(0, 9)), 16 * int(2 ** rng.uniform(0, 9))
+        for kind in (lib.MOE_GEMM_BF16, lib.MOE_GEMM_FP8, lib.MOE_GEMM_DX, lib.MOE_GEMM_DW):
+            size = lib.moe_grouped_gemm_workspace(kind, R, N, K, E)
+            assert size <= P.workspace_bound(R, N, K, E, "cpu"), (kind, R, N, K, E)
+            cut += size > 0
+    assert cut > 100
+    # sums that are cut: 2 x 3 tiles over 6546 rows of one expert
+    assert lib.moe_grouped_gemm_workspace(lib.MOE_GEMM_DW, 6546, 3320, 280, 1) >= 2 * 3320 * 280 * 4
