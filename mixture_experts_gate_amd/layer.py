@@ -393,6 +393,8 @@ class Fp8BlockLayer:
         self.h = buf(n, 2 * I, dtype=bf16)
         self.aq, self.a_s = buf(n, I, dtype=torch.uint8), buf(n, -(-I // 128), dtype=torch.float32)
         self.y, self.out = buf(n, H, dtype=bf16), buf(T_max, H, dtype=bf16)
+        # of the products' cut sums, of which the forward product's have R x N values
+        self.ws_sum = buf(products.workspace_bound(n, max(2 * I, H), 0, E, device), dtype=torch.uint8)
         if shared:
             self.h_sh, self.y_sh = buf(T_max, 2 * I, dtype=bf16), buf(T_max, H, dtype=bf16)
             self.aq_sh = buf(T_max, I, dtype=torch.uint8)
@@ -412,19 +414,20 @@ class Fp8BlockLayer:
         w13, w2 = self.matrices(table)
         xq, xs = products.quant_fp8(x[:T], q=self.xq[:T], s=self.xs[:T], stream=stream)
         h = products.grouped_matmul_fp8(xq, xs, w13, None, self.offsets, rows=pair, div=self.k,
-                                        out=self.h[:n], stream=stream)
+                                        out=self.h[:n], ws=self.ws_sum, stream=stream)
         aq, a_s = products.swiglu_quant_fp8(h, n_rows=self.offsets[self.E:], q=self.aq[:n],
                                             s=self.a_s[:n], stream=stream)
         products.grouped_matmul_fp8(aq, a_s, w2, None, self.offsets, out_rows=pair,
-                                    out=self.y[:n], stream=stream)
+                                    out=self.y[:n], ws=self.ws_sum, stream=stream)
         if shared_table is None:
             return self.y[:n], None
         if not self.shared:
             raise ValueError("layer was built without shared-expert buffers")
         s13, s2 = self.matrices(shared_table, 1)
-        h = products.grouped_matmul_fp8(xq, xs, s13, out=self.h_sh[:T], stream=stream)
+        h = products.grouped_matmul_fp8(xq, xs, s13, out=self.h_sh[:T], ws=self.ws_sum,
+                                        stream=stream)
         aq, a_s = products.swiglu_quant_fp8(h, q=self.aq_sh[:T], s=self.as_sh[:T], stream=stream)
-        products.grouped_matmul_fp8(aq, a_s, s2, out=self.y_sh[:T], stream=stream)
+        products.grouped_matmul_fp8(aq, a_s, s2, out=self.y_sh[:T], ws=self.ws_sum, stream=stream)
         return self.y[:n], self.y_sh[:T]
 
     def forward(self, T, x, table, logits=None, wg=None, shared_table=None, renormalize=True,

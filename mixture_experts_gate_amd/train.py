@@ -35,6 +35,8 @@ class TrainExperts:
         self.sorted_pair, self.pair_row = buf(n, dtype=torch.int32), buf(n, dtype=torch.int32)
         self.ws_bytes = max(_lib.moe_workspace_size(T_max, k, H, I, E)[0], 256)
         self.ws = buf(self.ws_bytes, dtype=torch.uint8)
+        self.ws_sum = buf(max(P.workspace_bound(n, 2 * I, H, E, device),
+                              P.workspace_bound(n, H, I, E, device)), dtype=torch.uint8)
         self.ones = torch.ones(T_max, k, dtype=torch.float32, device=device)
         self.h, self.a = buf(n, 2 * I), buf(n, I)
         self.y, self.out = buf(n, H), buf(T_max, H)
@@ -71,9 +73,9 @@ class TrainExperts:
         pair, off = self.sorted_pair[:n], self.offsets
         _lib.moe_permute(topk_ids, T, k, self.E, off, self.sorted_pair, self.pair_row, self.ws,
                          self.ws_bytes)
-        P.grouped_matmul(x, w13, off, rows=pair, div=k, out=self.h[:n])
+        P.grouped_matmul(x, w13, off, rows=pair, div=k, out=self.h[:n], ws=self.ws_sum)
         P.swiglu(self.h[:n], topk_w, pair, off[self.E:], out=self.a[:n])
-        P.grouped_matmul(self.a[:n], w2, off, out_rows=pair, out=self.y[:n])
+        P.grouped_matmul(self.a[:n], w2, off, out_rows=pair, out=self.y[:n], ws=self.ws_sum)
         _lib.moe_combine(self.y, False, self.ones, None, T, k, self.H, self.out)
         self._saved = (x, topk_w, w13, w2)
         return self.out[:T]
@@ -99,12 +101,13 @@ class TrainExperts:
             return self.dx[:0], self.dtopk_w[:0], self.dw13, self.dw2
         pair, off = self.sorted_pair[:n], self.offsets
         da, dh, dxp = self.da[:n], self.dh[:n], self.y[:n]
-        P.grouped_matmul_dx(dout, w2, off, rows=pair, div=k, out=da)
+        P.grouped_matmul_dx(dout, w2, off, rows=pair, div=k, out=da, ws=self.ws_sum)
         P.grouped_matmul_dw(dout, self.a[:n], off, dy_rows=pair, dy_div=k, out=self.dw2,
-                            accumulate=accumulate)
+                            accumulate=accumulate, ws=self.ws_sum)
         P.swiglu_grad(self.h[:n], da, topk_w.view(-1), pair, off[self.E:], dh=dh,
                       dw=self.dtopk_w[:T].view(-1))
-        P.grouped_matmul_dx(dh, w13, off, out_rows=pair, out=dxp)
+        P.grouped_matmul_dx(dh, w13, off, out_rows=pair, out=dxp, ws=self.ws_sum)
         _lib.moe_combine(dxp, False, self.ones, None, T, k, self.H, self.dx)
-        P.grouped_matmul_dw(dh, x, off, x_rows=pair, x_div=k, out=self.dw13, accumulate=accumulate)
+        P.grouped_matmul_dw(dh, x, off, x_rows=pair, x_div=k, out=self.dw13, accumulate=accumulate,
+                            ws=self.ws_sum)
         return self.dx[:T], self.dtopk_w[:T], self.dw13, self.dw2

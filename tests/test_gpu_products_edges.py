@@ -9,8 +9,8 @@ import numpy as np
 import pytest
 import torch
 
-from mixture_experts_gate_amd import _lib, products as P
-from mixture_experts_gate_amd.layer import Fp8BlockLayer
+from mixture_experts_gate_amd import _lib, products as P, synth
+from mixture_experts_gate_amd.layer import DeviceExperts, Fp8BlockLayer
 from mixture_experts_gate_amd.train import TrainExperts
 
 pytestmark = pytest.mark.gpu
@@ -397,3 +397,55 @@ def test_stream_handle_and_given_workspace(kind):
             call(ws=bad)
     with pytest.raises(_lib.MoeError):
         call(ws=big[8:8 + size])
+
+
+def _allocations():
+    return torch.cuda.memory_stats()["allocation.all.allocated"]
+
+
+def test_training_layer_allocates_nothing():
+    """Also at sizes whose sums are cut, forward and backward."""
+    T, E, k, H, I = 260, 1, 1, 2048, 128
+    for gemm, N, K in ((_lib.MOE_GEMM_BF16, 2 * I, H), (_lib.MOE_GEMM_DX, H, I)):
+        assert _lib.moe_grouped_gemm_workspace(gemm, T * k, N, K, E) > 0
+    g = _gen(41)
+    x, dout = _randn(g, T, H), _randn(g, T, H)
+    w13, w2 = _randn(g, E, 2 * I, H), _randn(g, E, H, I)
+    ids = torch.zeros(T, k, dtype=torch.int32, device=DEV)
+    w = torch.rand(T, k, generator=g, device=DEV)
+    m = TrainExperts(H, E, k, I, T)
+    before = _allocations()
+    out = m.forward(x, ids, w, w13, w2)
+    m.backward(dout)
+    assert _allocations() == before
+    # the products one by one, with workspaces of their own
+    h = P.grouped_matmul(x, w13)
+    y = P.grouped_matmul(P.swiglu(h, w.view(-1)), w2)
+    assert torch.equal(out, y)
+    da = P.grouped_matmul_dx(dout, w2)
+    dh, dw = P.swiglu_grad(h, da, w.view(-1))
+    assert torch.equal(m.dx, P.grouped_matmul_dx(dh, w13)) and torch.equal(m.dtopk_w.view(-1), dw)
+    assert torch.equal(m.dw13, P.grouped_matmul_dw(dh, x))
+
+
+def test_fp8_block_layer_allocates_nothing_and_is_the_same_by_handle():
+    T, E, k, H, I = 260, 1, 1, 2048, 128
+    assert _lib.moe_grouped_gemm_workspace(_lib.MOE_GEMM_FP8, T * k, 2 * I, H, E) > 0
+    rng = np.random.default_rng(42)
+    lay = synth.blob_layout(H, I, "fp8_block")
+    ex = DeviceExperts(np.stack([synth._gauss_fp8_block_blob(rng, H, I, 0.05) for _ in range(2)]), lay)
+    g = _gen(43)
+    x, logits = _randn(g, T, H), _randn(g, T, E, dtype=torch.float32)
+    layer = Fp8BlockLayer(H, E, k, I, T, shared=True)
+    kw = dict(logits=logits, shared_table=ex.table[1:])
+    before = _allocations()
+    out = layer.forward(T, x, ex.table, **kw)
+    assert _allocations() == before
+    want = out.clone()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        layer.out.zero_()
+        torch.cuda.synchronize()
+        layer.forward(T, x, ex.table, stream=stream, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(layer.out, want)
