@@ -25,6 +25,8 @@ class TrainExperts:
     (call it under ``torch.no_grad()``, or from a ``torch.autograd.Function``)."""
 
     def __init__(self, H, E, k, I, T_max, device="cuda"):
+        if H % 8 or I % 8 or E > 512:
+            raise ValueError("H and I must be multiples of 8, E at most 512")
         self.H, self.E, self.k, self.I, self.T_max = H, E, k, I, T_max
         n = max(T_max * k, 1)
 
@@ -46,26 +48,35 @@ class TrainExperts:
         self.dw2 = buf(E, H, I, dtype=torch.float32)
         self._saved = None
 
+    def _check(self, t, name, dtype, *shape):
+        """Before the first launch: a refused call leaves every buffer as it was."""
+        if (not isinstance(t, torch.Tensor) or t.device != self.out.device or t.dtype != dtype
+                or tuple(t.shape) != shape or not t.is_contiguous()
+                or (dtype is torch.bfloat16 and t.data_ptr() % 16)):
+            got = (f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor)
+                   else type(t).__name__)
+            raise ValueError(f"{name}: {got}; contiguous {dtype} {list(shape)} on {self.out.device} is "
+                             "needed (bf16: from an address that is a multiple of 16)")
+
     def forward(self, x, topk_ids, topk_w, w13, w2):
         """out [T, H] bf16 of x [T, H] bf16, the router's topk_ids [T, k] int32
         (distinct experts of a token, all of them in [0, E): the caller's to see
         to; a padding token has any of them, with weights 0) and topk_w [T, k]
         fp32, w13 [E, 2I, H] and w2 [E, H, I] bf16."""
         self._saved = None
-        if not x.is_cuda or x.device != self.out.device:
-            raise ValueError(f"x: on {x.device}, the buffers are on {self.out.device}")
+        if not isinstance(x, torch.Tensor) or not x.is_cuda or x.device != self.out.device:
+            raise ValueError(f"x: a tensor on {self.out.device}, where the buffers are, is needed")
         if x.get_device() != torch.cuda.current_device():
             with torch.cuda.device(x.device):
                 return self.forward(x, topk_ids, topk_w, w13, w2)
-        T, k = x.shape[0], self.k
-        if T > self.T_max or x.shape[1] != self.H:
-            raise ValueError(f"x: {tuple(x.shape)}, at most [{self.T_max}, {self.H}]")
-        for t, name, dtype in ((topk_ids, "topk_ids", torch.int32), (topk_w, "topk_w", torch.float32)):
-            if t.shape != (T, k) or t.dtype != dtype or not t.is_contiguous() or t.device != x.device:
-                raise ValueError(f"{name}: contiguous {dtype} [{T}, {k}] on {x.device} is needed")
+        k, bf16 = self.k, torch.bfloat16
+        T = min(x.shape[0], self.T_max) if x.dim() else 0       # (at most T_max)
+        self._check(x, "x", bf16, T, self.H)
+        self._check(topk_ids, "topk_ids", torch.int32, T, k)
+        self._check(topk_w, "topk_w", torch.float32, T, k)
+        self._check(w13, "w13", bf16, self.E, 2 * self.I, self.H)
+        self._check(w2, "w2", bf16, self.E, self.H, self.I)
         P._no_history(x, topk_w, w13, w2)
-        if w13.shape != (self.E, 2 * self.I, self.H) or w2.shape != (self.E, self.H, self.I):
-            raise ValueError(f"w13, w2: {tuple(w13.shape)}, {tuple(w2.shape)}")
         n = T * k
         if T == 0:
             self._saved = (x, topk_w, w13, w2)
@@ -92,8 +103,7 @@ class TrainExperts:
             with torch.cuda.device(x.device):
                 return self.backward(dout, accumulate)
         T, k = x.shape[0], self.k
-        if dout.shape != x.shape:
-            raise ValueError(f"dout: {tuple(dout.shape)}, {tuple(x.shape)} is needed")
+        self._check(dout, "dout", torch.bfloat16, T, self.H)
         n = T * k
         if T == 0:
             if not accumulate:

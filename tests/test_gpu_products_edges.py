@@ -449,3 +449,44 @@ def test_fp8_block_layer_allocates_nothing_and_is_the_same_by_handle():
         layer.forward(T, x, ex.table, stream=stream, **kw)
         torch.cuda.synchronize()
         assert torch.equal(layer.out, want)
+
+
+def test_training_layer_checks_everything_before_the_first_launch():
+    g = _gen(51)
+    T, E, k, H, I = 6, 4, 2, 64, 32
+    x, dout = _randn(g, T, H), _randn(g, T, H)
+    w13, w2 = _randn(g, E, 2 * I, H), _randn(g, E, H, I)
+    ids = torch.randint(0, E, (T, k), generator=g, device=DEV).to(torch.int32)
+    w = torch.rand(T, k, generator=g, device=DEV)
+    m = TrainExperts(H, E, k, I, T)
+    buffers = [m.offsets, m.sorted_pair, m.h, m.a, m.y, m.out, m.da, m.dh, m.dx, m.dtopk_w, m.dw13, m.dw2]
+
+    def untouched(call, error=ValueError):
+        for b in buffers:
+            b.fill_(77)
+        with pytest.raises(error):
+            call()
+        assert all(bool((b == 77).all()) for b in buffers)
+
+    off = torch.zeros(T * H + 4, device=DEV, dtype=torch.bfloat16)[4:].view(T, H)      # 8 bytes on
+    good = dict(x=x, topk_ids=ids, topk_w=w, w13=w13, w2=w2)
+    for name, t in (("x", x.float()), ("x", x.t().contiguous().t()), ("x", x[0]), ("x", off), ("x", x.cpu()),
+                    ("x", torch.cat([x, x])), ("x", None), ("topk_ids", ids.long()), ("topk_ids", ids[:3]),
+                    ("topk_w", w.double()), ("topk_w", w.t().contiguous().t()), ("w13", w13.float()),
+                    ("w13", w13.cpu()), ("w13", w13.transpose(1, 2)), ("w13", w13[:, :I]),
+                    ("w2", w2.half()), ("w2", w2.cpu()), ("w2", w2.transpose(1, 2).contiguous().transpose(1, 2)),
+                    ("w2", None)):
+        untouched(lambda: m.forward(**{**good, name: t}))
+        untouched(lambda: m.backward(dout), RuntimeError)     # no forward to belong to
+    # (an index or weights from any address)
+    w_off = torch.zeros(T * k + 1, device=DEV)[1:].view(T, k).copy_(w)
+    want = m.forward(**good).clone()
+    assert torch.equal(m.forward(**{**good, "topk_w": w_off}), want)
+    m.forward(**good)
+    buffers = [m.da, m.dh, m.dx, m.dtopk_w, m.dw13, m.dw2]
+    for t in (dout.float(), dout[:3], dout.t().contiguous().t(), off, dout.cpu(), None):
+        untouched(lambda: m.backward(t))
+    m.backward(dout)
+    for H_, I_, E_ in ((60, 32, 4), (64, 36, 4), (64, 32, 513)):
+        with pytest.raises(ValueError):
+            TrainExperts(H_, E_, 2, I_, 4)
