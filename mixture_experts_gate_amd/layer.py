@@ -374,8 +374,8 @@ class Fp8BlockLayer:
     for resident experts or ``ExpertCache.prefetch`` returns it."""
 
     def __init__(self, H, E, k, I, T_max, shared=False, device="cuda"):
-        if H % 32 or I % 32:
-            raise ValueError("H and I must be multiples of 32")
+        if H % 32 or I % 32 or E > 512:
+            raise ValueError("H and I must be multiples of 32, E at most 512")
         self.H, self.E, self.k, self.I, self.T_max, self.shared = H, E, k, I, T_max, shared
         n = max(T_max * k, 1)
         bf16, i32 = torch.bfloat16, torch.int32
@@ -406,9 +406,23 @@ class Fp8BlockLayer:
         return (products.TableMatrices(table, _lib.MOE_MAT_W13, E, 2 * self.I, self.H),
                 products.TableMatrices(table, _lib.MOE_MAT_W2, E, self.H, self.I))
 
+    def _check_tables(self, table, shared_table):
+        """Before the first launch: a refused call leaves every buffer as it was."""
+        for t, name, n in ((table, "table", self.E), (shared_table, "shared_table", 1)):
+            if t is None and name == "shared_table":
+                continue
+            if t is None or isinstance(t, int) and t == 0:
+                raise ValueError(f"{name}: a device table of moe_expert_w is needed")
+            if isinstance(t, torch.Tensor) and (t.device != self.out.device or t.dtype != torch.int64
+                                                or t.numel() < 4 * n or not t.is_contiguous()):
+                raise ValueError(f"{name}: contiguous int64 [{n}, 4] on {self.out.device} is needed")
+        if shared_table is not None and not self.shared:
+            raise ValueError("layer was built without shared-expert buffers")
+
     def ffn(self, T, x, table, shared_table=None, stream=None):
         """The experts of the current permutation: y in pair order, and the
         shared expert's rows (or None)."""
+        self._check_tables(table, shared_table)
         n = T * self.k
         pair = self.sorted_pair[:n]
         w13, w2 = self.matrices(table)
@@ -421,8 +435,6 @@ class Fp8BlockLayer:
                                     out=self.y[:n], ws=self.ws_sum, stream=stream)
         if shared_table is None:
             return self.y[:n], None
-        if not self.shared:
-            raise ValueError("layer was built without shared-expert buffers")
         s13, s2 = self.matrices(shared_table, 1)
         h = products.grouped_matmul_fp8(xq, xs, s13, out=self.h_sh[:T], ws=self.ws_sum,
                                         stream=stream)
@@ -445,11 +457,16 @@ class Fp8BlockLayer:
                 raise ValueError(f"{name}: contiguous {dtype} [{n}, {cols}] on {self.out.device} "
                                  "is needed")
         products._no_history(x, logits, wg)
+        if T == 0:
+            return self.out[:0]
+        if logits is None and wg is None:
+            raise ValueError("logits or wg is needed")
+        if x.data_ptr() % 16:
+            raise ValueError("x: must start at a multiple of 16 bytes")
+        self._check_tables(table, shared_table)
         if x.get_device() != torch.cuda.current_device():
             with torch.cuda.device(x.device):
                 return self.forward(T, x, table, logits, wg, shared_table, renormalize, stream)
-        if T == 0:
-            return self.out[:0]
         _lib.moe_route_permute(x, wg, logits, None if logits is not None else self.logits, T, self.H,
                                self.E, self.k, renormalize, self.topk_ids, self.topk_w,
                                self.offsets, self.sorted_pair, self.pair_row, self.ws_perm,

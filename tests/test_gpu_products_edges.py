@@ -490,3 +490,33 @@ def test_training_layer_checks_everything_before_the_first_launch():
     for H_, I_, E_ in ((60, 32, 4), (64, 36, 4), (64, 32, 513)):
         with pytest.raises(ValueError):
             TrainExperts(H_, E_, 2, I_, 4)
+
+
+def test_fp8_block_layer_checks_everything_before_the_first_launch():
+    T, E, k, H, I = 4, 4, 2, 64, 32
+    rng, g = np.random.default_rng(61), _gen(61)
+    lay = synth.blob_layout(H, I, "fp8_block")
+    ex = DeviceExperts(np.stack([synth._gauss_fp8_block_blob(rng, H, I, 0.05) for _ in range(E)]), lay)
+    x, logits = _randn(g, T, H), _randn(g, T, E, dtype=torch.float32)
+    layer = Fp8BlockLayer(H, E, k, I, T)
+    buffers = [layer.topk_ids, layer.topk_w, layer.offsets, layer.sorted_pair, layer.xq, layer.xs, layer.h,
+               layer.aq, layer.y, layer.out]
+    off = torch.zeros(T * H + 4, device=DEV, dtype=torch.bfloat16)[4:].view(T, H)      # 8 bytes on
+    tab = ex.table
+    good = dict(T=T, x=x, table=tab, logits=logits)
+    for kw in (dict(shared_table=tab[:1]), dict(table=None), dict(table=0), dict(table=tab[:3]),
+               dict(table=tab.to(torch.int32)), dict(table=tab.cpu()), dict(table=tab.t()), dict(x=off),
+               dict(logits=None)):
+        for b in buffers:
+            b.fill_(77)
+        with pytest.raises(ValueError):
+            layer.forward(**{**good, **kw})
+        if "logits" not in kw:
+            with pytest.raises((ValueError, _lib.MoeError)):
+                layer.ffn(T, kw.get("x", x), kw.get("table", tab), kw.get("shared_table"))
+        assert all(bool((b == 77).all()) for b in buffers), kw
+    assert layer.forward(0, x, None, logits=logits).shape == (0, H)
+    with pytest.raises(ValueError):
+        Fp8BlockLayer(H, 513, k, I, T)
+    a = layer.forward(**good).clone()
+    assert torch.equal(layer.forward(**{**good, "table": tab.data_ptr()}), a)
