@@ -173,7 +173,7 @@ def _guarded(rows, n, dtype):
 # those in parts, 256 x 256 tiles
 ROW_PATHS = {"stream": (150, 16, 64, 256), "stream_long": (150, 16, 64, 4672),
              "small": (400, 6, 136, 144), "parts": (261, 2, 112, 3648),
-             "large": (4000, 5, 2056, 1168)}
+             "large": (4000, 5, 2056, 2064)}
 
 
 @pytest.mark.parametrize("kind", ["product", "dx", "fp8", "dw"])
@@ -520,3 +520,100 @@ def test_fp8_block_layer_checks_everything_before_the_first_launch():
         Fp8BlockLayer(H, 513, k, I, T)
     a = layer.forward(**good).clone()
     assert torch.equal(layer.forward(**{**good, "table": tab.data_ptr()}), a)
+
+
+# --------------------------------------------- rows that are left, on each path --
+#
+# Whole numbers up to 3: products up to 9 and sums up to 9 * 4672 < 2^24 are exact in
+# fp32 in any order, and the FP8 instruction drops nothing above 2^-13 of 9.
+
+def _whole(g, *shape):
+    return torch.randint(-3, 4, shape, generator=g, device=DEV)
+
+
+def _e4m3(t):
+    return t.to(torch.float32).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def _forward(kind, x, w, off, **kw):
+    """The call of `kind` on whole numbers x (99 stands for NaN) and w."""
+    if kind == "fp8":
+        codes = torch.where(x == 99, torch.tensor(0x7F, dtype=torch.uint8, device=DEV), _e4m3(x.clamp(-3, 3)))
+        E, N, K = w.shape
+        return P.grouped_matmul_fp8(codes, torch.ones(x.shape[0], -(-K // 128), device=DEV), _e4m3(w),
+                                    torch.ones(E, -(-N // 128), -(-K // 128), device=DEV), off, **kw)
+    xb = torch.where(x == 99, torch.tensor(float("nan"), device=DEV), x.float()).to(torch.bfloat16)
+    return (P.grouped_matmul if kind == "product" else P.grouped_matmul_dx)(xb, w.to(torch.bfloat16), off, **kw)
+
+
+@pytest.mark.parametrize("kind", ["product", "dx", "fp8"])
+@pytest.mark.parametrize("path", list(ROW_PATHS))
+def test_rows_that_are_left_on_each_path(path, kind):
+    """Rows before offsets[0] and behind offsets[E], rows whose index is outside x
+    and rows whose place is outside the output are left as they are; the others
+    are right, with NaN in every row of x that none of them reads."""
+    R, E, N, K = ROW_PATHS[path]
+    g = _gen(71 + len(path))
+    gemm = {"product": _lib.MOE_GEMM_BF16, "dx": _lib.MOE_GEMM_DX, "fp8": _lib.MOE_GEMM_FP8}[kind]
+    cut = _lib.moe_grouped_gemm_workspace(gemm, R, N, K, E) > 0
+    assert cut == (path == "parts" and kind != "dx")     # (dx sums over N, which is short there)
+    C, Q = (N, K) if kind == "dx" else (K, N)
+    lo, hi, n, div = 5, R - R // 8, R // 2 + 1, 2
+    # ascending offsets from lo to hi, some experts without rows
+    inner = torch.sort(torch.randint(lo, hi + 1, (E - 1,), generator=g, device=DEV)).values
+    if E > 3:
+        inner[1] = inner[0]
+    off = torch.cat([torch.tensor([lo], device=DEV), inner, torch.tensor([hi], device=DEV)]).to(torch.int32)
+    pos = torch.arange(R, device=DEV)
+    rows = torch.randint(0, n * div, (R,), generator=g, device=DEV)
+    bad = pos % 17 == 7
+    rows[bad] = torch.tensor([-1, n * div, -2 ** 31, 2 ** 31 - 1], device=DEV)[pos[bad] % 4]
+    place = torch.randperm(R, generator=g, device=DEV)
+    lost = pos % 23 == 11
+    target = place.clone()
+    target[lost] = torch.tensor([-1, R, 2 ** 31 - 1], device=DEV)[pos[lost] % 3]
+    live = (pos >= lo) & (pos < hi) & ~bad & ~lost
+    x, w = _whole(g, n, C), _whole(g, E, N, K)
+    used = torch.zeros(n, dtype=torch.bool, device=DEV)
+    used[(rows[live] // div)] = True
+    x[~used] = 99
+    out = torch.full((R, Q), 5.0, device=DEV)
+    _forward(kind, x, w, off, rows=rows.to(torch.int32), div=div, out_rows=target.to(torch.int32), out=out)
+    expert = torch.searchsorted(off[1:].contiguous().long(), pos, right=True).clamp(max=E - 1)
+    wd = w.double()
+    want = torch.full((R, Q), 5.0, dtype=torch.float64, device=DEV)
+    for e in range(E):
+        at = pos[live & (expert == e)]
+        a = x[rows[at] // div].double()
+        want[place[at]] = a @ (wd[e] if kind == "dx" else wd[e].t().contiguous())
+    assert torch.equal(out.double(), want)
+
+
+@pytest.mark.parametrize("kind", ["product", "fp8"])
+@pytest.mark.parametrize("K", [64, 4672])
+@pytest.mark.parametrize("where", ["first", "last", "spread"])
+def test_streaming_kernel_with_all_rows_on_few_experts(kind, K, where):
+    """16 rows per expert on average, the most that this kernel takes, on one
+    expert of 512 or with a row on each of the others: an entry list near its
+    capacity."""
+    E, N = 512, 24
+    counts = [0] * E
+    if where == "spread":
+        counts = [1] * E
+        counts[300] = 16 * E - (E - 1)
+    else:
+        counts[0 if where == "first" else E - 1] = 16 * E
+    g = _gen(81)
+    x, w = _whole(g, 16 * E, K), _whole(g, E, N, K)
+    out = torch.zeros(16 * E, N, device=DEV)
+    _forward(kind, x, w, _offsets(counts), out=out)
+    e = max(range(E), key=lambda i: counts[i])
+    xd, lo = x.double(), sum(counts[:e])
+    want = torch.zeros(16 * E, N, dtype=torch.float64, device=DEV)
+    want[lo:lo + counts[e]] = xd[lo:lo + counts[e]] @ w[e].double().t().contiguous()
+    at = 0
+    for i in range(E):
+        if i != e and counts[i]:
+            want[at] = w[i].double() @ xd[at]
+        at += counts[i]
+    assert torch.equal(out.double(), want)
