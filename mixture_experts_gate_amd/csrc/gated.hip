@@ -13,8 +13,21 @@
 
 namespace moe {
 
-__device__ __forceinline__ float sigmoid(float g) {
-    return __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+// s = 1 / (1 + e^-g) and c = 1 - s, each to a few units of 2^-24, from e^-|g| (so
+// that nothing overflows and c does not cancel). e^-|g| = 2^t e^(-|g| - t ln 2),
+// t the rounded -|g| log2(e): with 2^t alone scales and weights' gradients were up
+// to 57 units off at |g| = 70 (now at most 8). From |g| = 128 on e^-|g| is 0.
+struct Sigmoid {
+    float s, c;
+};
+__device__ __forceinline__ Sigmoid sigmoid(float g) {
+    constexpr float kLn2 = 0.6931471805599453f, kLn2Rest = (float)(0.6931471805599453 - (double)kLn2);
+    const float a = __builtin_amdgcn_fmed3f(fabsf(g), 0.0f, 128.0f);     // (a NaN comes back in by the factor g)
+    const float t = -1.4426950408889634f * a, rest = fmaf(-kLn2Rest, t, fmaf(-kLn2, t, -a));
+    const float e0 = __builtin_amdgcn_exp2f(t), e = fmaf(e0, rest, e0);
+    const float d = 1.0f + e, r0 = __builtin_amdgcn_rcpf(d), r = fmaf(fmaf(-d, r0, 1.0f), r0, r0);
+    const float er = e * r;
+    return g < 0.0f ? Sigmoid{er, r} : Sigmoid{r, er};
 }
 
 __device__ __forceinline__ void unpack8(u32x4 q, float v[8]) {
@@ -42,6 +55,13 @@ __device__ __forceinline__ int row_count(const int32_t *n_rows, int R) {
 constexpr long kBlocksX = 1 << 23;
 __device__ __forceinline__ long block_id() { return (long)blockIdx.y * gridDim.x + blockIdx.x; }
 
+// Row of unit v of `per` to a row, 1 << log units to a workgroup. (A 64-bit
+// division for every thread cost the FP8 conversion of 24576 x 2048 values 8 us of
+// 58, which the arithmetic bounds as much as HBM.)
+__device__ __forceinline__ long row_of_unit(long v, int log, int per, const Divisor &d) {
+    return block_id() < (1L << (31 - log)) ? (long)((uint32_t)v / d) : v / per;
+}
+
 // Weight's place of row r: -1 where the index is outside the weights.
 __device__ __forceinline__ int weight_at(const int32_t *w_rows, int w_n, int r) {
     const int i = w_rows ? w_rows[r] : r;
@@ -52,9 +72,9 @@ __global__ __launch_bounds__(256) void gated_kernel(const uint16_t *__restrict__
                                                     const float *__restrict__ wt,
                                                     const int32_t *__restrict__ w_rows, int w_n,
                                                     const int32_t *__restrict__ n_rows, int R,
-                                                    int I, uint16_t *__restrict__ a) {
+                                                    int I, Divisor by, uint16_t *__restrict__ a) {
     const int per = I / 8;
-    const long id = block_id() * blockDim.x + threadIdx.x, row = id / per;
+    const long id = block_id() * blockDim.x + threadIdx.x, row = row_of_unit(id, 8, per, by);
     if (row >= row_count(n_rows, R)) return;
     const int r = (int)row;
     const int c = (int)(id - (long)r * per) * 8;
@@ -68,7 +88,7 @@ __global__ __launch_bounds__(256) void gated_kernel(const uint16_t *__restrict__
     unpack8(load_nt16(h + (size_t)r * 2 * I + c), g);
     unpack8(load_nt16(h + (size_t)r * 2 * I + I + c), u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = w * (g[i] * sigmoid(g[i]) * u[i]);
+    for (int i = 0; i < 8; ++i) g[i] = w * (g[i] * sigmoid(g[i]).s * u[i]);
     *(MOE_GLOBAL u32x4 *)(a + (size_t)r * I + c) = pack8(g);
 }
 
@@ -95,11 +115,12 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(
         unpack8(load_nt16(da + (size_t)r * I + c), d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float s = sigmoid(g[i]), silu = g[i] * s, wd = w * d[i];
+            const Sigmoid s = sigmoid(g[i]);
+            const float silu = g[i] * s.s, wd = w * d[i];
             act[i] = silu * u[i];
             sum += d[i] * act[i];
             act[i] *= w;
-            g[i] = wd * u[i] * (s * (1.0f + g[i] * (1.0f - s)));
+            g[i] = wd * u[i] * (s.s * (1.0f + g[i] * s.c));
             u[i] = wd * silu;
         }
         *(MOE_GLOBAL u32x4 *)(dh + (size_t)r * 2 * I + c) = pack8(g);
@@ -117,10 +138,11 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(
 template <bool GATED>
 __global__ __launch_bounds__(256) void to_fp8_kernel(const uint16_t *__restrict__ x,
                                                      const int32_t *__restrict__ n_rows, int R,
-                                                     int K, uint8_t *__restrict__ q,
+                                                     int K, Divisor by, uint8_t *__restrict__ q,
                                                      float *__restrict__ s) {
     const int kb = (K + 127) / 128;
-    const long id = (block_id() * blockDim.x + threadIdx.x) >> 4, row = id / kb;
+    const long id = (block_id() * blockDim.x + threadIdx.x) >> 4;
+    const long row = row_of_unit(id, 4, kb, by);
     if (row >= row_count(n_rows, R)) return;
     const int r = (int)row;
     const int b = (int)(id - (long)r * kb), l = threadIdx.x & 15, c = 128 * b + 8 * l;
@@ -132,7 +154,7 @@ __global__ __launch_bounds__(256) void to_fp8_kernel(const uint16_t *__restrict_
             unpack8(load_nt16(x + (size_t)r * 2 * K + c), v);
             unpack8(load_nt16(x + (size_t)r * 2 * K + K + c), u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = v[i] * sigmoid(v[i]) * u[i];
+            for (int i = 0; i < 8; ++i) v[i] = v[i] * sigmoid(v[i]).s * u[i];
         } else {
             unpack8(load_nt16(x + (size_t)r * K + c), v);
         }
@@ -154,9 +176,10 @@ __global__ __launch_bounds__(256) void to_fp8_kernel(const uint16_t *__restrict_
     const float sc = top / 448.0f;
     if (l == 0) s[(size_t)r * kb + b] = sc;
     if (!in) return;
-    // v / sc: quotient by the reciprocal, corrected by its remainder (which
-    // loses the sign of a zero)
-    const float rc = 1.0f / sc;
+    // v / sc: quotient by the reciprocal (from the instruction's, a step of
+    // Newton's; sc is 2^-109 to 2^120), corrected by its remainder (which loses
+    // the sign of a zero)
+    const float r0 = __builtin_amdgcn_rcpf(sc), rc = fmaf(fmaf(-sc, r0, 1.0f), r0, r0);
     float d[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -193,7 +216,7 @@ extern "C" int moe_swiglu(const uint16_t *h_bf16, const float *w, const int32_t 
     const long blocks = ((long)R * (I / 8) + 255) / 256;
     if (!blocks_ok(blocks)) return MOE_EINVAL;
     MOE_LAUNCH(K_GATED, gated_kernel, blocks_of(blocks), dim3(256), 0, (hipStream_t)stream,
-               h_bf16, w, w_rows, w_n, n_rows, R, I, a_bf16);
+               h_bf16, w, w_rows, w_n, n_rows, R, I, divisor(I / 8), a_bf16);
     return check_launch();
 }
 
@@ -219,7 +242,7 @@ static int to_fp8(const uint16_t *x, const int32_t *n_rows, int R, int K, uint8_
     const long blocks = ((long)R * ((K + 127) / 128) + 15) / 16;
     if (!blocks_ok(blocks)) return MOE_EINVAL;
     MOE_LAUNCH(K_TO_FP8, (to_fp8_kernel<GATED>), blocks_of(blocks), dim3(256), 0,
-               (hipStream_t)stream, x, n_rows, R, K, q, s);
+               (hipStream_t)stream, x, n_rows, R, K, divisor((K + 127) / 128), q, s);
     return check_launch();
 }
 

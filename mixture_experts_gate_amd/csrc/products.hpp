@@ -9,29 +9,37 @@ namespace moe {
 constexpr int kMaxE = 512;       // experts of a product
 constexpr int kMaxRows = 0x7FFFFF00;    // rows: those of a last tile or workgroup fit an int
 
+// v / div for 0 <= v < 2^31 as (v mul) >> (32 + shift), mul = floor(2^(31 +
+// l) / div) + 1 and shift = l - 1 for 2^(l-1) < div <= 2^l: mul exceeds the
+// quotient by at most one, which moves v mul by less than 2^31 <= 2^(31 +
+// l) / div, one unit of the result over div. mul = 0: div is 1.
+struct Divisor {
+    uint32_t mul;
+    int shift;
+};
+
+inline Divisor divisor(int div) {
+    if (div <= 1) return Divisor{0, 0};
+    int l = 1;
+    while ((1LL << l) < div) ++l;
+    return Divisor{(uint32_t)((1ULL << (31 + l)) / (uint64_t)div + 1), l - 1};
+}
+
+__device__ __forceinline__ uint32_t operator/(uint32_t v, const Divisor &d) {
+    return d.mul ? __umulhi(v, d.mul) >> d.shift : v;
+}
+
 // A matrix whose rows a product reads: row i of the sorted order is row
 // idx[i] / div of the matrix (row i where idx is NULL); n rows exist.
 struct RowsIn {
     const char *base;
     const int32_t *idx;
     int n;
-    // v / div for 0 <= v < 2^31 as (v mul) >> (32 + shift), mul = floor(2^(31 +
-    // l) / div) + 1 and shift = l - 1 for 2^(l-1) < div <= 2^l: mul exceeds the
-    // quotient by at most one, which moves v mul by less than 2^31 <= 2^(31 +
-    // l) / div, one unit of the result over div. mul = 0: div is 1.
-    uint32_t mul;
-    int shift;
+    Divisor div;
 };
 
 inline RowsIn rows_in(const void *base, const int32_t *idx, int div, int n) {
-    RowsIn r{(const char *)base, idx, n, 0, 0};
-    if (div > 1) {
-        int l = 1;
-        while ((1LL << l) < div) ++l;
-        r.mul = (uint32_t)((1ULL << (31 + l)) / (uint64_t)div + 1);
-        r.shift = l - 1;
-    }
-    return r;
+    return RowsIn{(const char *)base, idx, n, divisor(div)};
 }
 
 // The experts' matrices [N][K]: either one array [E][N][K] (tab NULL) or the
@@ -86,8 +94,7 @@ __device__ __forceinline__ void group_of_lane(const ProductArgs &a, int e, int &
 
 // The row that index v stands for, or -1 where it is not a row of r.
 __device__ __forceinline__ int row_of_index(const RowsIn &r, int v) {
-    const uint32_t u = (uint32_t)v;
-    const int q = (int)(r.mul ? __umulhi(u, r.mul) >> r.shift : u);
+    const int q = (int)((uint32_t)v / r.div);
     return v >= 0 && q < r.n ? q : -1;
 }
 

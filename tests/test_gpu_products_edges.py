@@ -617,3 +617,48 @@ def test_streaming_kernel_with_all_rows_on_few_experts(kind, K, where):
             want[at] = w[i].double() @ xd[at]
         at += counts[i]
     assert torch.equal(out.double(), want)
+
+
+def test_activation_between_roundings_is_held_in_fp32():
+    """The values that are not rounded to bf16 on the way out: the scale of a row
+    with one gate (silu(g) u / 448) and the weight's gradient (da silu(g) u).
+
+    In units of 2^-24: e^-|g| 3 (the exponential instruction's one unit in the last
+    place, and one rounding), 1 + e^-|g| another 1, its reciprocal 1, their product
+    1, times g 1; u and da are 1. The scale adds 1. The errors of e^-|g| in the
+    numerator and in 1 + e^-|g| have opposite signs and count once: 7, 8."""
+    unit = 2.0 ** -24
+    gate = torch.cat([torch.arange(-70 * 32, 70 * 32 + 1) / 32, torch.randn(4000) * 3]).to(torch.bfloat16)
+    gate = gate[gate != 0].to(DEV)
+    h = torch.zeros(len(gate), 16, device=DEV, dtype=torch.bfloat16)
+    h[:, 3], h[:, 8 + 3] = gate, 1
+    g = gate.double()
+    ref = g * torch.sigmoid(g)
+    _, s = P.swiglu_quant_fp8(h)
+    # (against 2^-100 / 448, the smallest scale)
+    want = (ref.abs() / 448).clamp(min=2.0 ** -100 / 448)
+    err = ((s[:, 0].double() - want).abs() / want / unit)
+    assert float(err.max()) <= 8, f"scale: {float(err.max()):.3g} units"
+    _, dw = P.swiglu_grad(h, torch.ones(len(gate), 8, device=DEV, dtype=torch.bfloat16),
+                          torch.ones(len(gate), device=DEV))
+    err = ((dw.double() - ref).abs() / ref.abs() / unit)
+    assert float(err.max()) <= 7, f"dw: {float(err.max()):.3g} units"
+
+
+def test_activation_of_the_largest_gates():
+    """Finite gates of any size: silu(g) u and its gradients without NaN, the
+    derivative 1 and 0 far out; NaN stays in its element's outputs."""
+    top = torch.finfo(torch.bfloat16).max
+    gate = torch.tensor([-top, -1e30, -1e4, -129, -128, -100, -88, 88, 100, 128, 129, 1e4, 1e30, top], device=DEV)
+    h = torch.ones(1, 2 * 16, device=DEV, dtype=torch.bfloat16)
+    h[0, :14] = gate.to(torch.bfloat16)
+    a = P.swiglu(h)[0, :14]
+    assert bool((a[:7].abs() <= 1e-36).all()) and torch.equal(a[7:], h[0, 7:14])
+    da = torch.ones(1, 16, device=DEV, dtype=torch.bfloat16)
+    dh, _ = P.swiglu_grad(h, da)
+    assert bool((dh[0, :7].abs() <= 1e-36).all()) and bool((dh[0, 7:14] == 1).all())
+    assert torch.equal(dh[0, 16:30], a)
+    h[0, 3] = float("nan")
+    a, (dh, _) = P.swiglu(h), P.swiglu_grad(h, da)
+    assert a.isnan().sum() == 1 and bool(a[0, 3].isnan())
+    assert dh.isnan().sum() == 2 and bool(dh[0, 3].isnan()) and bool(dh[0, 19].isnan())
