@@ -134,6 +134,14 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(
     }
 }
 
+// v / d by d's reciprocal r, corrected by the quotient's remainder; in this order
+// of signs a zero keeps its own. The bits of a division (2.7e8 codes compared), and
+// 46.5 us instead of 48.7 for the activation of 24576 x 2048 values with divisions.
+__device__ __forceinline__ float quotient(float v, float d, float r) {
+    const float q = v * r;
+    return fmaf(-fmaf(q, d, -v), r, q);
+}
+
 // 16 lanes a block of 128 columns, 8 columns a lane.
 template <bool GATED>
 __global__ __launch_bounds__(256) void to_fp8_kernel(const uint16_t *__restrict__ x,
@@ -173,19 +181,14 @@ __global__ __launch_bounds__(256) void to_fp8_kernel(const uint16_t *__restrict_
     }
     // an infinity or a NaN makes the whole block NaN (codes and scale)
     const float top = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : fmaxf(__uint_as_float(m), 0x1p-100f);
-    const float sc = top / 448.0f;
+    const float sc = quotient(top, 448.0f, 1.0f / 448.0f);
     if (l == 0) s[(size_t)r * kb + b] = sc;
     if (!in) return;
-    // v / sc: quotient by the reciprocal (from the instruction's, a step of
-    // Newton's; sc is 2^-109 to 2^120), corrected by its remainder (which loses
-    // the sign of a zero)
+    // (the reciprocal from the instruction's, by a step of Newton's; sc is 2^-109 to 2^120)
     const float r0 = __builtin_amdgcn_rcpf(sc), rc = fmaf(fmaf(-sc, r0, 1.0f), r0, r0);
     float d[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float q0 = v[i] * rc;
-        d[i] = copysignf(fmaf(fmaf(-q0, sc, v[i]), rc, q0), v[i]);
-    }
+    for (int i = 0; i < 8; ++i) d[i] = quotient(v[i], sc, rc);
     int lo = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], lo, true);
     int hi = __builtin_amdgcn_cvt_pk_fp8_f32(d[4], d[5], 0, false);
