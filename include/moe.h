@@ -444,9 +444,14 @@ int moe_timing_query(int kernel_id, long long *launches, double *total_ms);
  * array [E] of moe_expert_w with mat = MOE_MAT_W13 (w13, s13) or MOE_MAT_W2
  * (w2, s2), for matrices that live in an expert cache or in blobs; exactly one
  * of the two is given. Matrices and rows start 16-byte aligned.
- * Sums are fp32. Results do not depend on timing: the same call gives the same
- * bits. All sizes 1 <= E <= 512, R <= 2^31 - 256; R = 0 does nothing (dw
- * writes its zeros).
+ * Sums are fp32; inside moe_grouped_gemm_fp8, the products of 8 consecutive
+ * columns are aligned to the largest of them, and what lies 13 bits below its
+ * leading bit is dropped (see there). Results do not depend on timing: the same
+ * call gives the same bits.
+ * Sizes: 1 <= E <= 512, R <= 2^31 - 256, N and K up to 2^20, and at most 2^27
+ * tiles of 128 x 128: (R / 128 + E) ceil(max(N, K) / 128) of the rows, E
+ * ceil(N / 128) ceil(K / 128) of the matrices; others are MOE_EINVAL. R = 0 does
+ * nothing (dw writes its zeros).
  * ws (16-byte aligned, may be NULL): with at least the bytes that
  * moe_grouped_gemm_workspace gives, a call with few output tiles and a long
  * sum cuts the sum into parts and adds them in a second launch (fp32, in a
@@ -492,7 +497,10 @@ int moe_grouped_gemm_dw(const uint16_t *dy_bf16, const int32_t *dy_rows, int dy_
  * over E4M3 codes x [x_n][K] with fp32 scales [x_n][ceil(K/128)] (moe_quant_fp8
  * makes them) and matrices with fp32 scales as above (moe_expert_w's s13 / s2
  * point at them). Both indices of x (codes and scales) go through x_rows. N a
- * multiple of 8, K of 16. */
+ * multiple of 8, K of 16.
+ * The blocks' sums and everything behind them are fp32 (also where y is fp32);
+ * inside a block each group of 8 columns is off by less than 7 2^-13 of its largest
+ * product, next to codes that were rounded to 2^-4 of their values. */
 int moe_grouped_gemm_fp8(const uint8_t *x_e4m3, const float *x_scale, const int32_t *x_rows,
                          int x_div, int x_n, const int32_t *offsets, const uint8_t *w_e4m3,
                          const float *w_scale, const moe_expert_w *experts, int mat, int R, int N,
@@ -504,7 +512,9 @@ int moe_grouped_gemm_fp8(const uint8_t *x_e4m3, const float *x_scale, const int3
  * w[w_rows[r]] (w = topk_w, w_rows = sorted_pair puts the router's weights
  * here, so that the combine adds rows with weight 1); a row whose index is
  * outside w is skipped. n_rows (optional, device): only rows below *n_rows
- * (e.g. offsets + E); the others are left as they are. I a multiple of 8. */
+ * (e.g. offsets + E); the others are left as they are. I a multiple of 8, up to
+ * 2^24. e^-|g| may be 0 below 2^-126, silu(g) with it; an infinite g gives what the
+ * formulas give in fp32 (NaN where 0 meets an infinity). */
 int moe_swiglu(const uint16_t *h_bf16, const float *w, const int32_t *w_rows, int w_n,
                const int32_t *n_rows, int R, int I, uint16_t *a_bf16, void *stream);
 
@@ -520,7 +530,7 @@ int moe_swiglu_grad(const uint16_t *h_bf16, const uint16_t *da_bf16, const float
  * [R][ceil(K/128)]: scale = max(amax, 2^-100) / 448 with amax the largest
  * magnitude of the row's 128 columns, code = x / scale to the nearest E4M3
  * (ties to even). An infinity or NaN makes its block's scale and codes NaN.
- * n_rows as in moe_swiglu. K a multiple of 8. */
+ * n_rows as in moe_swiglu. K a multiple of 8, up to 2^24. */
 int moe_quant_fp8(const uint16_t *x_bf16, const int32_t *n_rows, int R, int K, uint8_t *q_e4m3,
                   float *scale, void *stream);
 

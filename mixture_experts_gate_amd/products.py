@@ -86,11 +86,10 @@ def _int(n, name):
 
 def _no_history(*inputs):
     """Refuses inputs whose gradient autograd would be expected to find."""
-    if torch.is_grad_enabled():
-        for t in inputs:
-            if isinstance(t, torch.Tensor) and t.requires_grad:
-                _fail("an input requires grad, and the result carries no history for autograd: "
-                      "call under torch.no_grad() (the gradients are calls of their own)")
+    for t in inputs:
+        if getattr(t, "requires_grad", False) and torch.is_grad_enabled():
+            _fail("an input requires grad, and the result carries no history for autograd: "
+                  "call under torch.no_grad() (the gradients are calls of their own)")
 
 
 def _matrix(t, name, dtype, dev=None):
