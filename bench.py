@@ -5,7 +5,11 @@ One step = one pass of the routed MoE expert layer (route -> permute ->
 grouped SwiGLU expert FFN -> combine) over one batch of synthetic tokens, all
 inputs resident in HBM. The headline workload is the decode-shaped layer
 (H=2048, 128 experts, top-8, I=768, MXFP4 weights, bf16 activations, uniform
-router logits) at T=64 tokens. The JSON line's sweep also carries T=1, 8, 32
+router logits) at T=64 tokens. The JSON line holds the headline, its roofline and
+the rates of every other workload in a few thousand characters, so that a reader
+who keeps the end of the output has all of it; --full writes the whole record
+(every kernel's launches, counts and times, the references measured on the GPU,
+the oracle's sweep) to a file. The sweep also carries T=1, 8, 32
 and the prefill-shaped T=8192 batch of the same layer; the large sparse layer
 (H=4096, 256 experts + 1 shared, top-6, I=2048, Zipf popularity) at T=1, 64,
 4096; and the 43-layer stack of that layer decoding T=1, 2, 4, 8 and 16 tokens,
@@ -71,7 +75,33 @@ def parse():
                     help="timed steps of the cached 43-layer stack at T=1")
     ap.add_argument("--cfg4-T", default="1,2,64,4096",
                     help="comma list of the large sparse layer's batch sizes to run")
+    ap.add_argument("--full", default="", metavar="PATH",
+                    help="also write the whole record, as JSON, to this file")
     return ap.parse_args()
+
+
+# What the line keeps of a workload.
+RATES = ("tokens_per_s", "ms_per_step", "layer_hbm_frac", "layer_tflops", "mfma_frac_bf16_peak",
+         "hbm_frac", "hit_rate", "h2d_frac_of_link", "overlap_efficiency", "link", "mode")
+
+
+def rates(r):
+    """The rates of a workload's record, six digits each, and of the records in it."""
+    out = {k: float(f"{r[k]:.6g}") if isinstance(r[k], float) else r[k] for k in RATES if k in r}
+    for k, v in r.items():
+        if isinstance(v, dict) and "tokens_per_s" in v:
+            out[k] = rates(v)
+        elif isinstance(v, list) and v and all(isinstance(e, dict) and "tokens_per_s" in e for e in v):
+            out[k] = [rates(e) for e in v]
+    return out
+
+
+def short_line(record):
+    """The record without what only --full writes."""
+    line = {k: v for k, v in record.items() if k not in ("cpu_baseline_sweep", "micro", "sweep")}
+    line["config"] = {k: v for k, v in record["config"].items() if k != "kernels"}
+    line["sweep"] = {k: rates(v) for k, v in record["sweep"].items()}
+    return line
 
 
 def log(msg):
@@ -1105,7 +1135,7 @@ def main():
         if not args.no_sweep:
             cpu_all = cpu_baselines(wl.pool)
     c = wl.cfg
-    line = {
+    record = {
         "metric": "MoE-layer tokens/s at decode T=1..64 & prefill T=8192; % HBM / MFMA roofline",
         "value": head["tokens_per_s"],
         "unit": "tokens/s",
@@ -1133,7 +1163,10 @@ def main():
         "micro": micro_res,
         "sweep": sweep,
     }
-    print(json.dumps(line), flush=True)
+    if args.full:
+        with open(args.full, "w") as f:
+            json.dump(record, f)
+    print(json.dumps(short_line(record)), flush=True)
 
 
 if __name__ == "__main__":
