@@ -1,0 +1,442 @@
+"""What stands around the experts' products, and their product in 4 bits, as cases to measure.
+
+Three operators of the mixture-of-experts layer:
+
+  norm          y = x / sqrt(mean(x^2) + eps) * weight of rows, x = the rows plus
+                a residual, rounded to bf16 ("total"); "norm_fp8": y as E4M3 codes
+                with one scale per 128 columns beside y itself; "norm_gradients":
+                the gradients by the rows and by the weight
+  dispatch      tokens' rows to sorted order; "combine": the experts' rows back to
+                their tokens, sum of w y; "combine_gradients": by y and by w
+  linear_mxfp4  y = W_e x in microscaled 4 bits (E2M1 codes, a power of two per 32
+                columns): rows to MXFP4, then the product with MXFP4 matrices.
+                "gated": of silu(g) u of rows [g | u]. "product_mxfp4": the product
+                of rows that are in MXFP4 already
+
+A pair is (token, one of its k experts), numbered token * k + j. "sorted order"
+is the pairs grouped by expert.
+"""
+import math
+
+import torch
+
+own = False
+
+_EPS = 1e-6
+_MIN_AMAX = 2.0 ** -100          # smallest block maximum an E4M3 scale is made from
+_NORMS = ("norm", "norm_fp8", "norm_gradients")
+_MOVES = ("dispatch", "combine", "combine_gradients")
+
+
+# ------------------------------------------------------------------- cases --
+
+def listed():
+    def norm(name, kind, T, H, residual):
+        return {"name": name, "kind": kind, "T": T, "H": H, "residual": residual}
+
+    def move(name, kind, T, k, E, H, weights=True, add=False):
+        return {"name": name, "kind": kind, "T": T, "k": k, "E": E, "H": H, "weights": weights, "add": add}
+
+    def mx4(name, kind, T, k, E, N, K, gated, skew):
+        return {"name": name, "kind": kind, "T": T, "k": k, "E": E, "N": N, "K": K, "gated": gated, "skew": skew}
+
+    return [
+        # before the layer of a decode step, one token: latency
+        norm("norm of one token to FP8", "norm_fp8", 1, 2048, True),
+        # before the layer of a prompt, with the router's bf16 rows beside the experts' FP8 ones
+        norm("norm of 8192 tokens to FP8", "norm_fp8", 8192, 4096, True),
+        # a small training batch, odd row count
+        norm("norm gradients of 301 tokens", "norm_gradients", 301, 2048, False),
+        # a training batch, with the residual stream's own gradient
+        norm("norm gradients of 8192 tokens", "norm_gradients", 8192, 4096, True),
+        # a prompt's tokens to the experts' order
+        move("dispatch of 8192 tokens", "dispatch", 8192, 8, 128, 2048),
+        # a decode step's pairs back to their tokens, with the always-on expert's row
+        move("combine of 64 tokens", "combine", 64, 6, 256, 4096, add=True),
+        # a training batch: gradients by the experts' rows and by the router's weights
+        move("combine gradients, 4096 tokens", "combine_gradients", 4096, 8, 128, 2048),
+        # one token's gate/up projection in a decode step: latency
+        mx4("MXFP4 gate/up of one token", "linear_mxfp4", 1, 8, 128, 1536, 2048, False, 0.0),
+        # a decode batch on a large sparse layer: one to tens of rows an expert
+        mx4("MXFP4 gate/up of 64 tokens", "linear_mxfp4", 64, 6, 256, 4096, 4096, False, 1.0),
+        # a prompt's gate/up projection: the matrix cores and the result's bytes
+        mx4("MXFP4 gate/up of 8192 tokens", "linear_mxfp4", 8192, 8, 128, 1536, 2048, False, 0.22),
+        # a prompt's down projection on the large sparse layer, with the activation
+        mx4("MXFP4 down of 4096 tokens", "linear_mxfp4", 4096, 6, 256, 4096, 2048, True, 0.22),
+        # the always-on expert of the same layer: one group, an odd row count
+        mx4("MXFP4 gate/up, one expert", "product_mxfp4", 4001, 1, 1, 4096, 4096, False, 0.0),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    kind = rng.choice(_NORMS + _MOVES + ("linear_mxfp4",) * 4 + ("product_mxfp4",) * 2)
+    if kind in _NORMS:
+        H = 8 * _log_int(rng, 8, 1024)
+        return {"kind": kind, "T": _log_int(rng, 1, min(32768, (1 << 25) // H)), "H": H,
+                "residual": rng.random() < 0.5}
+    if kind in _MOVES:
+        E, H = _log_int(rng, 1, 256), 8 * _log_int(rng, 8, 512)
+        k = rng.randint(1, min(E, 8))
+        return {"kind": kind, "T": _log_int(rng, 1, min(8192, (1 << 26) // (k * H))), "k": k, "E": E, "H": H,
+                "weights": kind == "combine_gradients" or rng.random() < 0.7, "add": rng.random() < 0.3}
+    while True:
+        E = _log_int(rng, 1, 256)
+        c = {"kind": kind, "T": _log_int(rng, 1, 8192), "k": rng.randint(1, min(E, 8)), "E": E,
+             "N": 16 * _log_int(rng, 4, 256), "K": 128 * _log_int(rng, 1, 32),
+             "gated": kind == "linear_mxfp4" and rng.random() < 0.5, "skew": rng.choice((0.0, 0.22, 0.5))}
+        if 2.0 * c["T"] * c["k"] * c["N"] * c["K"] <= 400e9 and E * c["N"] * c["K"] <= 2.0e9:
+            return c
+
+
+def work(case):
+    kind, T = case["kind"], case["T"]
+    if kind in _NORMS:
+        n, H, res = T * case["H"], case["H"], case["residual"]
+        if kind == "norm_gradients":
+            return {"bytes": (8 if res else 6) * n + 6 * H, "flops": 10 * n}
+        size = (8 if res else 4) * n + 2 * H
+        if kind == "norm_fp8":
+            return {"bytes": size + n + 4 * T * -(-H // 128), "flops": 8 * n}
+        return {"bytes": size, "flops": 5 * n}
+    k = case["k"]
+    R = T * k
+    if kind in _MOVES:
+        H = case["H"]
+        if kind == "dispatch":
+            return {"bytes": 2 * (T + R) * H + 4 * R, "flops": R * H}
+        if kind == "combine":
+            n_w, n_add = 4 * R if case["weights"] else 0, T if case["add"] else 0
+            return {"bytes": 2 * (T + R + n_add) * H + 4 * R + n_w, "flops": 2 * R * H}
+        return {"bytes": 2 * (T + 2 * R) * H + 12 * R, "flops": 3 * R * H}
+    E, N, K = (case[n] for n in ("E", "N", "K"))
+    live = E * (1.0 - (1.0 - k / E) ** T)
+    n_x = R if case["gated"] else T
+    x = n_x * K * (4 if case["gated"] else 2) if kind == "linear_mxfp4" else n_x * K * 17 / 32
+    return {"bytes": live * N * K * 17 / 32 + x + 2 * R * N + 8 * R + 4 * (E + 1), "flops": 2.0 * R * N * K}
+
+
+# ------------------------------------------------------------------ inputs --
+
+def _routing(gen, T, k, E, skew):
+    """k distinct experts for each token; experts differ in popularity by `skew`."""
+    bias = skew * torch.randn(E, device="cuda", generator=gen)
+    noise = torch.rand(T, E, device="cuda", generator=gen).clamp_(1e-9, 1 - 1e-7)
+    return torch.topk(bias - torch.log(-torch.log(noise)), k, dim=1).indices
+
+
+def _to_mxfp4(x):
+    """(E2M1 codes [.., K/2], even column in the low half, and E8M0 scales [.., K/32]):
+    the scale is 2^(floor(log2 amax) - 2) of 32 columns, a code x / scale to the
+    nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6, ties to the even code, at most 6."""
+    b = x.reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
+    amax = b.abs().amax(-1)
+    e = torch.where(amax > 0, torch.frexp(amax).exponent - 3, -127).clamp(-127, 127)
+    a = b.abs() * torch.exp2(-e.to(x.dtype))[..., None]
+    m = torch.where(a < 2, torch.round(2 * a), torch.where(a < 4, torch.round(a) + 2, torch.round(a / 2) + 4))
+    m = m.clamp_(max=7).to(torch.uint8)
+    m = torch.where(torch.signbit(b) & (m > 0), m + 8, m).reshape(*x.shape[:-1], -1, 2)
+    return m[..., 0] | (m[..., 1] << 4), (e + 127).to(torch.uint8)
+
+
+def _kernel_order(codes, scales):
+    """Matrices [E, N, K/2] and scales [E, N, K/32] in blocks of 16 rows x 128 columns:
+    of a block, 32 columns after 32 columns, row after row."""
+    E, N, half = codes.shape
+    c = codes.view(E, N // 16, 16, half // 64, 4, 16).permute(0, 1, 3, 4, 2, 5).contiguous()
+    s = scales.view(E, N // 16, 16, half // 64, 4).permute(0, 1, 3, 4, 2).contiguous()
+    return c.view(E, N, half), s.view(E, N, half // 16)
+
+
+def _matrices(gen, E, N, K):
+    """Gaussian matrices in MXFP4, row by row and in the kernel's order."""
+    codes = torch.empty(E, N, K // 2, device="cuda", dtype=torch.uint8)
+    scales = torch.empty(E, N, K // 32, device="cuda", dtype=torch.uint8)
+    step = max(1, (1 << 28) // (N * K))
+    for e in range(0, E, step):
+        n = min(step, E - e)
+        codes[e:e + n], scales[e:e + n] = _to_mxfp4(0.02 * torch.randn(n, N, K, device="cuda", generator=gen))
+    return codes, scales, *_kernel_order(codes, scales)
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+
+    def bf16(*shape, sigma=1.0):
+        x = torch.randn(*shape, device="cuda", dtype=torch.bfloat16, generator=gen)
+        return x.mul_(sigma) if sigma != 1.0 else x
+
+    def empty(*shape, dtype=torch.bfloat16):
+        return torch.empty(*shape, device="cuda", dtype=dtype)
+
+    kind, T = case["kind"], case["T"]
+    if kind in _NORMS:
+        H = case["H"]
+        # rows of a residual stream: each of its own size
+        size = torch.exp(torch.randn(T, 1, device="cuda", generator=gen)).to(torch.bfloat16)
+        s = {"kind": kind, "x": bf16(T, H) * size, "residual": None, "total": None,
+             "weight": (1.0 + 0.2 * torch.randn(H, device="cuda", generator=gen)).to(torch.bfloat16)}
+        if kind == "norm_gradients":
+            s["dy"], s["dx"], s["dw"] = bf16(T, H, sigma=0.1), empty(T, H), empty(H, dtype=torch.float32)
+            s["dtotal"] = bf16(T, H, sigma=0.1) if case["residual"] else None
+            return s
+        if case["residual"]:
+            s["residual"], s["total"] = bf16(T, H) * size, empty(T, H)
+        s["y"] = empty(T, H)
+        if kind == "norm_fp8":
+            s["q"] = empty(T, H, dtype=torch.float8_e4m3fn)
+            s["scale"] = empty(T, -(-H // 128), dtype=torch.float32)
+        return s
+
+    k, E = case["k"], case["E"]
+    R = T * k
+    ids = _routing(gen, T, k, E, case.get("skew", 0.22))
+    flat = ids.reshape(-1)
+    order = torch.sort(flat, stable=True).indices
+    row = torch.empty_like(order)
+    row[order] = torch.arange(R, device="cuda")
+    s = {"kind": kind, "T": T, "k": k, "ids": ids, "order": order, "row": row.view(T, k),
+         "pair": order.to(torch.int32), "pair_row": row.to(torch.int32).view(T, k)}
+    if kind in _MOVES:
+        H = case["H"]
+        if kind == "dispatch":
+            return s | {"x": bf16(T, H), "out": empty(R, H)}
+        w = torch.softmax(torch.randn(T, k, device="cuda", generator=gen), 1) if case["weights"] else None
+        s |= {"y": bf16(R, H), "w": w}
+        if kind == "combine":
+            return s | {"add": bf16(T, H) if case["add"] else None, "out": empty(T, H)}
+        return s | {"dout": bf16(T, H, sigma=0.1), "dy": empty(R, H), "dw": empty(T, k, dtype=torch.float32)}
+
+    N, K = case["N"], case["K"]
+    counts = torch.bincount(flat, minlength=E)
+    offsets = torch.zeros(E + 1, dtype=torch.int64, device="cuda")
+    offsets[1:] = torch.cumsum(counts, 0)
+    # the plan of the plain form: the experts with rows, and each row's place
+    # in a batch of as many rows for each of them
+    live = counts.nonzero().reshape(-1)
+    cap = int(counts.max())
+    number = torch.zeros(E, dtype=torch.int64, device="cuda")
+    number[live] = torch.arange(live.numel(), device="cuda")
+    by_row = flat[order]
+    s |= {"gated": case["gated"], "live": live, "cap": cap,
+          "slot": number[by_row] * cap + torch.arange(R, device="cuda") - offsets[by_row],
+          "offsets": offsets.to(torch.int32), "y": empty(R, N)}
+    s["codes"], s["scales"], s["w"], s["ws"] = _matrices(gen, E, N, K)
+    n_x = R if case["gated"] else T
+    if kind == "linear_mxfp4":
+        s["x"] = bf16(n_x, 2 * K if case["gated"] else K)
+        s["xq"], s["xs"] = empty(n_x, K // 2, dtype=torch.uint8), empty(n_x, K // 32, dtype=torch.uint8)
+    else:
+        s["xq"], s["xs"] = _to_mxfp4(torch.randn(n_x, K, device="cuda", generator=gen))
+    return s
+
+
+# ------------------------------------------------------------ plain form ----
+
+def _values(codes, scales):
+    """fp32 values of MXFP4 codes [.., K/2] and scales [.., K/32]."""
+    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, 0, -0.5, -1, -1.5, -2, -3, -4, -6], device=codes.device)
+    both = torch.stack((codes & 15, codes >> 4), -1).reshape(*scales.shape, 32)
+    return (grid[both.int()] * torch.exp2(scales.float() - 127)[..., None]).reshape(*scales.shape[:-1], -1)
+
+
+def _plain_norm(s):
+    x, w = s["x"].float(), s["weight"].float()
+    if s["kind"] == "norm_gradients":
+        dy = s["dy"].float()
+        inv = 1.0 / torch.sqrt((x * x).mean(1, keepdim=True) + _EPS)
+        n = x * inv
+        g = dy * w
+        dx = inv * (g - n * (g * n).mean(1, keepdim=True))
+        if s["dtotal"] is not None:
+            dx = dx + s["dtotal"].float()
+        return dx.to(torch.bfloat16), (dy * n).sum(0)
+    out = {}
+    if s["residual"] is not None:
+        out["total"] = (x + s["residual"].float()).to(torch.bfloat16)
+        x = out["total"].float()
+    y = x * (1.0 / torch.sqrt((x * x).mean(1, keepdim=True) + _EPS)) * w
+    out["y"] = y.to(torch.bfloat16)
+    if s["kind"] == "norm_fp8":
+        R, H = y.shape
+        b = torch.nn.functional.pad(y, (0, -H % 128)).view(R, -1, 128)
+        out["scale"] = b.abs().amax(2).clamp(min=_MIN_AMAX) / 448.0
+        q = (b / out["scale"][:, :, None]).clamp(-448, 448).view(R, -1)[:, :H]
+        out["q"] = q.to(torch.float8_e4m3fn)
+    return out
+
+
+def _plain_move(s):
+    if s["kind"] == "dispatch":
+        return s["x"][s["order"] // s["k"]]
+    y = s["y"].float()[s["row"]]                                  # [T, k, H]
+    if s["kind"] == "combine":
+        out = (y if s["w"] is None else y * s["w"][:, :, None]).sum(1)
+        return (out if s["add"] is None else out + s["add"].float()).to(torch.bfloat16)
+    dout = s["dout"].float()
+    dy = (s["w"].reshape(-1)[s["order"]][:, None] * dout[s["order"] // s["k"]]).to(torch.bfloat16)
+    return dy, (y * dout[:, None, :]).sum(2)
+
+
+def _plain_mxfp4(s):
+    if s["kind"] == "product_mxfp4":
+        x = _values(s["xq"], s["xs"])
+    else:
+        x = s["x"].double()                  # (a value next to a border of the codes)
+        if s["gated"]:
+            g, u = x.chunk(2, dim=1)
+            x = g / (1.0 + torch.exp(-g)) * u
+        x = _values(*_to_mxfp4(x))
+    live, cap, slot = s["live"], s["cap"], s["slot"]
+    rows = x if s["gated"] else x[s["order"] // s["k"]]
+    batch = torch.zeros(live.numel() * cap, x.shape[1], device=x.device)
+    batch[slot] = rows
+    w = _values(s["codes"][live], s["scales"][live])
+    y = torch.bmm(w, batch.view(live.numel(), cap, -1).transpose(1, 2).contiguous()).transpose(1, 2)
+    y = y.reshape(-1, w.shape[1])[slot].to(torch.bfloat16)
+    if not s["gated"]:
+        return y
+    out = torch.empty_like(y)
+    out[s["order"]] = y
+    return out
+
+
+# ------------------------------------------------------------ the kernels ---
+
+def _own(s):
+    from mixture_experts_gate_amd import products as P, rows as R
+
+    kind = s["kind"]
+    if kind == "norm_gradients":
+        return R.rms_norm_grad(s["x"], s["weight"], s["dy"], _EPS, s["dtotal"], dx=s["dx"], dw=s["dw"])
+    if kind == "norm":
+        y = R.rms_norm(s["x"], s["weight"], _EPS, s["residual"], out=s["y"], total=s["total"])
+        return {"y": s["y"]} if s["residual"] is None else {"y": s["y"], "total": s["total"]}
+    if kind == "norm_fp8":
+        R.rms_norm_fp8(s["x"], s["weight"], _EPS, s["residual"], out=s["y"], total=s["total"], q=s["q"],
+                       s=s["scale"])
+        out = {"y": s["y"], "q": s["q"], "scale": s["scale"]}
+        return out if s["residual"] is None else out | {"total": s["total"]}
+    if kind == "dispatch":
+        return R.dispatch(s["x"], s["pair"], s["k"], out=s["out"])
+    if kind == "combine":
+        return R.combine(s["y"], s["pair_row"], s["w"], s["add"], out=s["out"])
+    if kind == "combine_gradients":
+        return R.combine_grad(s["dout"], s["y"], s["pair_row"], s["w"], dy=s["dy"], dw=s["dw"])
+    if kind == "linear_mxfp4":
+        (P.swiglu_quant_mxfp4 if s["gated"] else P.quant_mxfp4)(s["x"], q=s["xq"], s=s["xs"])
+    at = {"out_rows": s["pair"]} if s["gated"] else {"rows": s["pair"], "div": s["k"]}
+    return P.grouped_matmul_mxfp4(s["xq"], s["xs"], s["w"], s["ws"], s["offsets"], out=s["y"], **at)
+
+
+def run(state):
+    if own:
+        return _own(state)
+    kind = state["kind"]
+    return (_plain_norm if kind in _NORMS else _plain_move if kind in _MOVES else _plain_mxfp4)(state)
+
+
+# --------------------------------------------------------- 64-bit values ----
+
+def _e4m3(v):
+    """float64 values rounded to E4M3: 3 mantissa bits, half to even, from 2^-9 up to 448."""
+    e = torch.frexp(v).exponent - 1
+    step = torch.ldexp(torch.ones_like(v), e.clamp(min=-6) - 3)
+    return (torch.round(v / step) * step).clamp(-448, 448)
+
+
+def _nearest_e2m1(v):
+    """float64 values rounded to multiples of 0.5 below 2, of 1 below 4, of 2 above, half to even, up to 6."""
+    e = (torch.frexp(v).exponent - 1).clamp(0, 2)
+    step = torch.ldexp(torch.ones_like(v), e - 1)
+    return (torch.round(v / step) * step).clamp(-6, 6)
+
+
+def _rounded_mxfp4(x):
+    """float64 rows rounded to what MXFP4 holds of them."""
+    out = torch.empty_like(x)
+    for c in range(0, x.shape[1], 32):
+        b = x[:, c:c + 32]
+        top = b.abs().max(dim=1, keepdim=True).values
+        scale = torch.exp2(torch.floor(torch.log2(top.clamp(min=2.0 ** -125))) - 2)
+        out[:, c:c + 32] = _nearest_e2m1(b / scale) * scale
+    return out
+
+
+def _decoded(codes, scales):
+    """float64 values of one matrix's codes and scales, from the codes' bits."""
+    out = torch.empty(codes.shape[0], 2 * codes.shape[1], dtype=torch.float64, device=codes.device)
+    for half in (0, 1):
+        c = ((codes >> (4 * half)) & 15).to(torch.int64)
+        exp, low = (c >> 1) & 3, (c & 1).double()
+        value = torch.where(exp == 0, 0.5 * low, torch.exp2((exp - 1).double()) * (1 + 0.5 * low))
+        out[:, half::2] = torch.where(c >= 8, -value, value)
+    return out * torch.exp2(scales.double() - 127).repeat_interleave(32, 1)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    kind = s["kind"]
+    if kind in _NORMS:
+        x, w = s["x"].double(), s["weight"].double()
+        H = x.shape[1]
+        out = {}
+        if s["residual"] is not None:
+            out["total"] = x + s["residual"].double()
+            x = out["total"].to(torch.float32).to(torch.bfloat16).double()
+        rms = ((x ** 2).sum(1, keepdim=True) / H + _EPS) ** 0.5
+        if kind == "norm_gradients":
+            dy = s["dy"].double()
+            dot = (dy * w * x).sum(1, keepdim=True)
+            dx = dy * w / rms - x * dot / (H * rms ** 3)
+            return (dx if s["dtotal"] is None else dx + s["dtotal"].double()), (dy * x / rms).sum(0)
+        out["y"] = x / rms * w
+        if kind == "norm_fp8":
+            q, scale = torch.empty_like(x), []
+            for c in range(0, H, 128):
+                b = out["y"][:, c:c + 128]
+                top = torch.clamp(b.abs().max(dim=1, keepdim=True).values, min=_MIN_AMAX) / 448
+                q[:, c:c + 128] = _e4m3(b / top)
+                scale.append(top)
+            out["q"], out["scale"] = q, torch.cat(scale, 1)
+        return out
+    T, k = s["T"], s["k"]
+    R = T * k
+    flat = s["ids"].reshape(-1)
+    if kind in _MOVES:
+        # pairs in sorted order: by expert, then by number
+        pair = torch.sort(flat * R + torch.arange(R, device="cuda")).values % R
+        if kind == "dispatch":
+            return s["x"].double()[pair // k]
+        y = torch.empty_like(s["y"], dtype=torch.float64)
+        y[pair] = s["y"].double()                                 # by pair
+        w = torch.ones(T, k, dtype=torch.float64, device="cuda") if s["w"] is None else s["w"].double()
+        if kind == "combine":
+            out = torch.bmm(w[:, None, :], y.view(T, k, -1))[:, 0]
+            return out if s["add"] is None else out + s["add"].double()
+        dout = s["dout"].double()
+        dy = dout.repeat_interleave(k, 0) * w.reshape(-1, 1)
+        return dy[pair], torch.bmm(y.view(T, k, -1), dout[:, :, None])[:, :, 0]
+    if kind == "product_mxfp4":
+        x = _decoded(s["xq"], s["xs"])
+    else:
+        x = s["x"].double()
+        if s["gated"]:
+            K = x.shape[1] // 2
+            x = torch.sigmoid(x[:, :K]) * x[:, :K] * x[:, K:]
+        x = _rounded_mxfp4(x)
+    E, N = s["codes"].shape[:2]
+    y = torch.zeros(R, N, dtype=torch.float64, device="cuda")
+    first = 0
+    for e in range(E):
+        p = (flat == e).nonzero().reshape(-1)
+        here = torch.arange(first, first + p.numel(), device="cuda")      # sorted order
+        first += p.numel()
+        if p.numel():
+            w = _decoded(s["codes"][e], s["scales"][e]).t().contiguous()
+            y[p if s["gated"] else here] = x[here if s["gated"] else p // k] @ w
+    return y
