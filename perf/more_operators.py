@@ -322,7 +322,7 @@ def _own(s):
         out = {"y": s["y"], "q": s["q"], "scale": s["scale"]}
         return out if s["residual"] is None else out | {"total": s["total"]}
     if kind == "dispatch":
-        return R.dispatch(s["x"], s["pair"], s["k"], out=s["out"])
+        return R.dispatch(s["x"], s["pair_row"], out=s["out"])
     if kind == "combine":
         return R.combine(s["y"], s["pair_row"], s["w"], s["add"], out=s["out"])
     if kind == "combine_gradients":
