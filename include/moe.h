@@ -461,7 +461,7 @@ enum { MOE_MAT_W13 = 0, MOE_MAT_W2 = 1 };
 
 /* moe_grouped_gemm_workspace -- (host) bytes of workspace that a product of
  * these sizes can use, often 0; kind: MOE_GEMM_*. */
-enum { MOE_GEMM_BF16 = 0, MOE_GEMM_FP8 = 1, MOE_GEMM_DX = 2, MOE_GEMM_DW = 3 };
+enum { MOE_GEMM_BF16 = 0, MOE_GEMM_FP8 = 1, MOE_GEMM_DX = 2, MOE_GEMM_DW = 3, MOE_GEMM_MXFP4 = 4 };
 int moe_grouped_gemm_workspace(int kind, int R, int N, int K, int E, size_t *bytes);
 
 /* moe_grouped_gemm -- y[i] = W_e x[i] for every row i of sorted order and its
@@ -539,6 +539,100 @@ int moe_quant_fp8(const uint16_t *x_bf16, const int32_t *n_rows, int R, int K, u
  * [R][ceil(I/128)]. */
 int moe_swiglu_quant_fp8(const uint16_t *h_bf16, const int32_t *n_rows, int R, int I,
                          uint8_t *q_e4m3, float *scale, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * MXFP4 rows and the product of MXFP4 rows with MXFP4 matrices: E2M1 codes with
+ * one E8M0 scale per 32 consecutive columns of a row.
+ *
+ * moe_quant_mxfp4 -- rows x [R][K] bf16 as codes [R][K/2], the even column in the
+ * low half of a byte, and scales [R][K/32]. scale = 2^(floor(log2 amax) - 2) with
+ * amax the largest magnitude of the 32 columns, at least 2^-127 (which a block of
+ * zeros has); code = x / scale to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with
+ * its sign (ties to the even code, at most 6; a zero has no sign). An infinity or
+ * NaN makes its block's scale NaN (255), its codes 0. n_rows as in moe_swiglu.
+ * K a multiple of 32, up to 2^24; codes 16-byte aligned. */
+int moe_quant_mxfp4(const uint16_t *x_bf16, const int32_t *n_rows, int R, int K, uint8_t *q_e2m1,
+                    uint8_t *scale_e8m0, void *stream);
+
+/* moe_swiglu_quant_mxfp4 -- moe_quant_mxfp4 of the fp32 values silu(g) u of rows
+ * h [R][2I] = [g | u] (not rounded to bf16 in between): [R][I/2], [R][I/32]. */
+int moe_swiglu_quant_mxfp4(const uint16_t *h_bf16, const int32_t *n_rows, int R, int I,
+                           uint8_t *q_e2m1, uint8_t *scale_e8m0, void *stream);
+
+/* moe_quant_mxfp4_matrices -- matrices w [E][N][K] bf16 as moe_quant_mxfp4 does
+ * their rows, in the kernel MXFP4 layout (above): codes [E][N*K/2], scales
+ * [E][N*K/32]. N a multiple of 16, K of 128, both up to 2^20. */
+int moe_quant_mxfp4_matrices(const uint16_t *w_bf16, int E, int N, int K, uint8_t *q_e2m1,
+                             uint8_t *scale_e8m0, void *stream);
+
+/* moe_grouped_gemm_mxfp4 -- moe_grouped_gemm from MXFP4 rows and matrices:
+ *   y[i][n] = sum_b 2^(x_scale[i][b] - 127) 2^(w_scale[e][n][b] - 127)
+ *             sum_{k in 32 b .. 32 b + 31} x[i][k] w_e[n][k]
+ * over rows x [x_n][K/2] with scales [x_n][K/32] (moe_quant_mxfp4 makes them) and
+ * matrices in the kernel MXFP4 layout: w_e2m1 [E][N*K/2] with w_e8m0 [E][N*K/32],
+ * or a table's MOE_W_MXFP4 blobs. Both indices of x (codes and scales) go through
+ * x_rows. N a multiple of 16, K of 128; x's scales 4-byte aligned. A NaN scale
+ * makes every result that it enters NaN.
+ * The matrix core adds 64 (16 rows per expert and less: 128) columns' products and
+ * the sum so far with an error below 2^-22 of their magnitudes' sum; everything
+ * else as for moe_grouped_gemm (workspace kind MOE_GEMM_MXFP4). */
+int moe_grouped_gemm_mxfp4(const uint8_t *x_e2m1, const uint8_t *x_e8m0, const int32_t *x_rows,
+                           int x_div, int x_n, const int32_t *offsets, const uint8_t *w_e2m1,
+                           const uint8_t *w_e8m0, const moe_expert_w *experts, int mat, int R,
+                           int N, int K, int E, void *y, const int32_t *y_rows, int y_n,
+                           int y_is_fp32, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Rows before and after the experts. bf16 rows start 16-byte aligned, H is a
+ * multiple of 8 up to 2^24, and sums are fp32 (squares past its range make
+ * an infinite sum: values up to 2^51 are safe at every H).
+ *
+ * moe_rms_norm -- t = x (+ residual, rounded to bf16 and written to total where
+ * that is given), y = t / sqrt(mean(t^2) + eps) * weight, for rows x [R][H] and
+ * weight [H] bf16. Outputs: y_bf16 (optional with quant) and
+ *   quant = MOE_QUANT_FP8: codes q [R][H] and fp32 q_scale [R][ceil(H/128)], of
+ *     the unrounded y as moe_quant_fp8 makes them;
+ *   quant = MOE_QUANT_MXFP4: q [R][H/2] and q_scale [R][H/32] as moe_quant_mxfp4
+ *     (H a multiple of 32).
+ * total may be x or residual (in place); total without a residual is refused. */
+enum { MOE_QUANT_NONE = 0, MOE_QUANT_FP8 = 1, MOE_QUANT_MXFP4 = 2 };
+int moe_rms_norm(const uint16_t *x_bf16, const uint16_t *residual_bf16, const uint16_t *weight_bf16,
+                 float eps, int R, int H, uint16_t *total_bf16, uint16_t *y_bf16, int quant,
+                 uint8_t *q, void *q_scale, void *stream);
+
+/* moe_rms_norm_grad -- gradients of y = x / sqrt(mean(x^2) + eps) * weight for dy
+ * [R][H]: dx bf16, to which dtotal (optional, the gradient that comes to x past
+ * the norm; dx may be the same rows) is added, and dw [H] fp32 (optional;
+ * accumulate != 0 adds to it, zeros for R = 0 otherwise). With x = total, dx is
+ * the gradient of the residual and of what was added to it alike. H up to 16384.
+ * ws (16-byte aligned): with dw, at least moe_rms_norm_grad_workspace's bytes;
+ * calls that may overlap need workspaces of their own. */
+int moe_rms_norm_grad_workspace(int R, int H, size_t *bytes);
+int moe_rms_norm_grad(const uint16_t *x_bf16, const uint16_t *weight_bf16, const uint16_t *dy_bf16,
+                      const uint16_t *dtotal_bf16, float eps, int R, int H, uint16_t *dx_bf16,
+                      float *dw, int accumulate, void *ws, size_t ws_bytes, void *stream);
+
+/* moe_dispatch -- tokens to the rows of their pairs: out[pair_row[t*k + j]] =
+ * x[t], x [T][H], out [out_n][H] bf16 (pair_row as moe_permute writes it). A pair
+ * whose row is outside out (-1, say) is left out; rows of out that no pair has are
+ * left as they are; rows are distinct. Its gradient is moe_combine_rows without w. */
+int moe_dispatch(const uint16_t *x_bf16, const int32_t *pair_row, int T, int k, int H,
+                 uint16_t *out_bf16, int out_n, void *stream);
+
+/* moe_combine_rows -- the experts' rows back to their tokens: out[t] = sum_j
+ * w[t*k + j] y[pair_row[t*k + j]] + add[t], j ascending; y [y_n][H] bf16 or fp32 in
+ * sorted order, w (optional, 1 without) fp32, add (optional) and out [T][H] bf16.
+ * A pair whose row is outside y adds nothing. */
+int moe_combine_rows(const void *y, int y_is_fp32, int y_n, const int32_t *pair_row, const float *w,
+                     const uint16_t *add_bf16, int T, int k, int H, uint16_t *out_bf16, void *stream);
+
+/* moe_combine_rows_grad -- its gradients for dout [T][H] bf16: dy[pair_row[p]] =
+ * w[p] dout[t] (optional, bf16 [y_n][H]; rows of no pair are left as they are, rows
+ * are distinct) and dw[p] = <dout[t], y[pair_row[p]]> (optional, fp32 [T*k], of y
+ * bf16; 0 for a pair whose row is outside y). add's gradient is dout. */
+int moe_combine_rows_grad(const uint16_t *dout_bf16, const uint16_t *y_bf16, int y_n,
+                          const int32_t *pair_row, const float *w, int T, int k, int H,
+                          uint16_t *dy_bf16, float *dw, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Measurement helpers (not part of the layer): the references the layer's

@@ -16,7 +16,8 @@ LIB_PATH = os.path.join(_PKG, "libmoe.so")
 MOE_OK, MOE_EINVAL, MOE_ENOMEM, MOE_EHIP, MOE_EUNSUPPORTED, MOE_EBUSY = 0, -1, -2, -3, -4, -5
 MOE_W_BF16, MOE_W_MXFP4, MOE_W_NVFP4, MOE_W_FP8 = 0, 1, 2, 3
 MOE_MAT_W13, MOE_MAT_W2 = 0, 1
-MOE_GEMM_BF16, MOE_GEMM_FP8, MOE_GEMM_DX, MOE_GEMM_DW = 0, 1, 2, 3
+MOE_GEMM_BF16, MOE_GEMM_FP8, MOE_GEMM_DX, MOE_GEMM_DW, MOE_GEMM_MXFP4 = 0, 1, 2, 3, 4
+MOE_QUANT_NONE, MOE_QUANT_FP8, MOE_QUANT_MXFP4 = 0, 1, 2
 MOE_OPT_FFN_PATH = 1
 MOE_OPT_TIMING = 2
 MOE_OPT_DEC_SPLIT = 3
@@ -37,7 +38,9 @@ EXPORTS = [
     "moe_permute_split", "moe_cpu_expert_ffn", "moe_scatter_rows", "moe_permute_ffn_combine",
     "moe_layer_fused", "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw",
     "moe_grouped_gemm_fp8", "moe_grouped_gemm_workspace", "moe_swiglu", "moe_swiglu_grad", "moe_quant_fp8",
-    "moe_swiglu_quant_fp8",
+    "moe_swiglu_quant_fp8", "moe_quant_mxfp4", "moe_swiglu_quant_mxfp4", "moe_quant_mxfp4_matrices",
+    "moe_grouped_gemm_mxfp4", "moe_rms_norm", "moe_rms_norm_grad", "moe_rms_norm_grad_workspace",
+    "moe_dispatch", "moe_combine_rows", "moe_combine_rows_grad",
 ]
 
 
@@ -115,6 +118,16 @@ def load(path: str | None = None):
         "moe_swiglu_grad": (I, [P, P, P, P, I, P, I, I, P, P, P, P]),
         "moe_quant_fp8": (I, [P, P, I, I, P, P, P]),
         "moe_swiglu_quant_fp8": (I, [P, P, I, I, P, P, P]),
+        "moe_quant_mxfp4": (I, [P, P, I, I, P, P, P]),
+        "moe_swiglu_quant_mxfp4": (I, [P, P, I, I, P, P, P]),
+        "moe_quant_mxfp4_matrices": (I, [P, I, I, I, P, P, P]),
+        "moe_grouped_gemm_mxfp4": (I, [P, P, P, I, I, P, P, P, P, I, I, I, I, I, P, P, I, I, P, Z, P]),
+        "moe_rms_norm": (I, [P, P, P, C.c_float, I, I, P, P, I, P, P, P]),
+        "moe_rms_norm_grad": (I, [P, P, P, P, C.c_float, I, I, P, P, I, P, Z, P]),
+        "moe_rms_norm_grad_workspace": (I, [I, I, C.POINTER(Z)]),
+        "moe_dispatch": (I, [P, P, I, I, I, P, I, P]),
+        "moe_combine_rows": (I, [P, I, I, P, P, P, I, I, I, P, P]),
+        "moe_combine_rows_grad": (I, [P, P, I, P, P, I, I, I, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -273,6 +286,13 @@ def moe_grouped_gemm_workspace(kind, R, N, K, E):
     b = C.c_size_t(0)
     _check("moe_grouped_gemm_workspace",
            load().moe_grouped_gemm_workspace(kind, R, N, K, E, C.byref(b)))
+    return b.value
+
+
+def moe_rms_norm_grad_workspace(R, H):
+    """Bytes of workspace that moe_rms_norm_grad needs for the weight's gradient."""
+    b = C.c_size_t(0)
+    _check("moe_rms_norm_grad_workspace", load().moe_rms_norm_grad_workspace(R, H, C.byref(b)))
     return b.value
 
 

@@ -17,7 +17,8 @@ OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ["api.hip", "route.hip", "permute.hip", "ffn_decode.hip", "ffn_decode_shared.hip", "ffn_small.hip",
            "ffn_prefill.hip", "pack.hip", "noalloc.hip", "micro.hip",
            "combine.hip", "cache.hip", "products.hip",
-           "products_small.hip", "products_stream.hip", "gated.hip"]
+           "products_small.hip", "products_stream.hip", "products_mxfp4.hip", "gated.hip",
+           "rows.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

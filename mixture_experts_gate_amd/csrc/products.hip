@@ -494,24 +494,6 @@ static void launch_product(ProductArgs &a, void *ws, size_t ws_bytes, hipStream_
                dim3(kPThreads), 0, s, a);
 }
 
-// Sizes that every product shares; unit: the elements of 16 bytes.
-static int check_sizes(int R, int N, int K, int E, const int32_t *offsets, int unit) {
-    if (R < 0 || R > kMaxRows || E < 1 || E > kMaxE || N < 8 || K < unit || N % 8 || K % unit) return MOE_EINVAL;
-    if (N > (1 << 20) || K > (1 << 20)) return MOE_EINVAL;
-    if (!offsets && E != 1) return MOE_EINVAL;
-    // tiles (of 128 x 128, times 16 parts) are counted in 32 bits
-    const long tn = (N + 127) / 128, tk = (K + 127) / 128, most = 1L << 27;
-    if (((long)R / 128 + E) * (tn > tk ? tn : tk) > most || tn * tk * E > most) return MOE_EINVAL;
-    return MOE_OK;
-}
-
-static bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
-
-// rows: every row is read in place (n >= R), or through an index
-static bool rows_ok(const void *base, const int32_t *idx, int div, int n, int R) {
-    return base && aligned16(base) && div >= 1 && n >= (idx ? 1 : R);
-}
-
 }  // namespace moe
 
 using namespace moe;
@@ -605,9 +587,15 @@ extern "C" int moe_grouped_gemm_dw(const uint16_t *dy_bf16, const int32_t *dy_ro
 }
 
 extern "C" int moe_grouped_gemm_workspace(int kind, int R, int N, int K, int E, size_t *bytes) {
-    if (kind < kFwd || kind > kDw || !bytes) return MOE_EINVAL;
-    const int rc = check_sizes(R, N, K, E, E == 1 ? nullptr : (const int32_t *)16, kind == kFwdFp8 ? 16 : 8);
+    if (kind < kFwd || kind > MOE_GEMM_MXFP4 || !bytes) return MOE_EINVAL;
+    const int unit = kind == MOE_GEMM_MXFP4 ? 128 : kind == kFwdFp8 ? 16 : 8;
+    const int rc = check_sizes(R, N, K, E, E == 1 ? nullptr : (const int32_t *)16, unit);
     if (rc != MOE_OK) return rc;
+    if (kind == MOE_GEMM_MXFP4) {
+        if (N % 16) return MOE_EINVAL;
+        *bytes = mxfp4_part_bytes(R, N, K, E);
+        return MOE_OK;
+    }
     ProductArgs a{};
     a.E = E, a.R = R, a.N = N, a.K = K;
     *bytes = part_bytes(a, kind, product_slices(a, kind));

@@ -456,6 +456,30 @@ void launch_product_stream(const ProductArgs &a, bool fp8, hipStream_t s);
 void launch_product_small(const ProductArgs &a, int mode, hipStream_t s);
 int small_slices(const ProductArgs &a, int mode);   // parts that c is worth being cut into
 
+// The sum of the parts of c, in order, to out with q per row (forward and dx).
+void launch_join(const ProductArgs &a, int Qn, hipStream_t s);
+
+// products_mxfp4.hip: bytes of the parts of its cut sums
+size_t mxfp4_part_bytes(int R, int N, int K, int E);
+
+// Sizes that every product shares; unit: the elements of 16 bytes.
+inline int check_sizes(int R, int N, int K, int E, const int32_t *offsets, int unit) {
+    if (R < 0 || R > kMaxRows || E < 1 || E > kMaxE || N < 8 || K < unit || N % 8 || K % unit) return MOE_EINVAL;
+    if (N > (1 << 20) || K > (1 << 20)) return MOE_EINVAL;
+    if (!offsets && E != 1) return MOE_EINVAL;
+    // tiles (of 128 x 128, times 16 parts) are counted in 32 bits
+    const long tn = (N + 127) / 128, tk = (K + 127) / 128, most = 1L << 27;
+    if (((long)R / 128 + E) * (tn > tk ? tn : tk) > most || tn * tk * E > most) return MOE_EINVAL;
+    return MOE_OK;
+}
+
+inline bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+// rows: every row is read in place (n >= R), or through an index
+inline bool rows_ok(const void *base, const int32_t *idx, int div, int n, int R) {
+    return base && aligned16(base) && div >= 1 && n >= (idx ? 1 : R);
+}
+
 int kernel_of(int mode);   // timing id of a product
 int compute_units();   // of the current device (256 on MI355X)
 

@@ -1,0 +1,425 @@
+// The product grouped by expert from MXFP4: rows of x against matrices, both in
+// E2M1 codes with a power of two per 32 columns, y[i] = W_e x[r(i)] (products.hip
+// has the rows). The matrix core multiplies the scales in, one byte per lane and
+// operand, so nothing is left for the vector units inside the sum.
+//
+// The matrices are in the kernel layout: blocks of 16 rows x 128 columns (a slab of
+// K), 1024 bytes in which 16-byte piece 16 g + r holds row r, columns 32 g + 0..31,
+// with 64 bytes of scales, byte 16 g + r.
+#include "products.hpp"
+
+namespace moe {
+
+struct MxArgs {
+    ProductArgs p;             // a: codes of x, m: codes of the matrices
+    const uint8_t *xs, *ws;    // scales of x's rows, of the matrices (no table)
+};
+
+__device__ __forceinline__ const char *codes_of(const MxArgs &A, int e) {
+    const ProductArgs &a = A.p;
+    if (a.m.tab) return (const char *)(a.m.mat ? as_scalar(a.m.tab)[e].w2 : as_scalar(a.m.tab)[e].w13);
+    return a.m.w + (size_t)e * a.N * (a.K / 2);
+}
+
+__device__ __forceinline__ const char *scales_of(const MxArgs &A, int e) {
+    const ProductArgs &a = A.p;
+    if (a.m.tab) return (const char *)(a.m.mat ? as_scalar(a.m.tab)[e].s2 : as_scalar(a.m.tab)[e].s13);
+    return (const char *)A.ws + (size_t)e * a.N * (a.K / 32);
+}
+
+// Bytes OA and OB of the scale registers scale this lane's 32 codes of a and b.
+template <int OA, int OB>
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
+    const u32x4 z = {0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(as_i32x8(a, z), as_i32x8(b, z), c, 4, 4, OA, (int)sa,
+                                                           OB, (int)sb);
+}
+
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
+    const u32x4 z = {0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(as_i32x8(a, z), as_i32x8(b, z), c, 4, 4, 0, (int)sa,
+                                                            0, (int)sb);
+}
+
+// ------------------------------------------------------------------ tiles --
+// 128 rows (p) x 256 n (q) a workgroup of four wavefronts, 64 x 128 each; two
+// workgroups a compute unit, so that one multiplies while the other starts or ends a
+// tile. A step is a slab; LDS holds three, two of them copied ahead.
+//
+// Instruction 32x32x64 with x as A and W as B (16x16x128 has the same rate but
+// reads each operand twice as often): a lane (h, b) = (l / 32, l % 32) of result
+// register v has row 8 (v / 4) + 4 h + v % 4 and column b. Column b of tile j is q =
+// 4 b + j of the wavefront's 128, so that a lane holds four consecutive q of a row
+// and 32 lanes store 256 bytes of it. The same order puts the scales of the
+// four tiles into the four bytes of one register, which the instruction picks from.
+constexpr int kXThreads = 256;
+constexpr int kXP = 128, kXQ = 256;
+constexpr int kXS = 3;           // slabs in LDS
+constexpr int kXCopies = 8;      // copy instructions of a wavefront and slab
+
+struct TileLds {
+    char p[kXS][kXP * 64];       // rows of 64 bytes, 16-byte pieces XORed with row / 4
+    char q[kXS][kXQ * 64];       // blocks as in memory, piece 16 g + r at 16 g + (r ^ block % 4)
+    uint32_t xs[kXS][kXP];       // a row's four scales
+    char qs[kXS][kXQ * 4];       // blocks' scales as in memory
+    int src[kXP], dst[kXP];      // rows of x and of out (-1: none) of the rows in LDS
+    int base[kMaxE + 1];         // p tiles before each expert
+    int wsum[kXThreads / kWave];
+};
+
+__global__ __launch_bounds__(kXThreads, 2) void mxfp4_tile_kernel(MxArgs X) {
+    const ProductArgs &A = X.p;
+    __shared__ TileLds L;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int l = lane_id(), t = threadIdx.x, h = l >> 5, b = l & 31;
+    const int wq = w & 1, wp = w >> 1;
+
+    const int tq = (A.N + kXQ - 1) / kXQ, slabs = A.K / 128, blocks = A.N / 16;
+    const size_t ldx = (size_t)A.K / 2, lds = (size_t)A.K / 32;
+    total_tiles<kXThreads>(A, kXP, L.base, L.wsum);
+    const int ns = A.slices, total = L.base[A.E] * tq * ns;
+    const int nx = gridDim.x >= 8 ? 8 : 1;      // workgroup b runs on XCD b % 8
+    const int xcd = blockIdx.x % nx, per = ((int)gridDim.x - xcd + nx - 1) / nx;
+    const int t0 = (int)((long)total * xcd / nx), t1 = (int)((long)total * (xcd + 1) / nx);
+    for (int si = t0 + (int)blockIdx.x / nx; si < t1; si += per) {
+        const int ti = ns > 1 ? si / ns : si, slice = si - ti * ns;     // tile, part of its sum
+        const int e = expert_of(L.base, A.E, tq, ti);
+        const int mp = __builtin_amdgcn_readfirstlane(L.base[e + 1] - L.base[e]);
+        const int li = ti - __builtin_amdgcn_readfirstlane(L.base[e]) * tq;
+        int p0, q0, lo, cnt;
+        group_of(A, e, lo, cnt);
+        // the expert's rows are spread evenly over its tiles, in units of 32 (more
+        // than four of them only where offsets do not ascend)
+        int units = (int)((cnt + 32u * mp - 1) / (32u * mp));
+        units = units < 4 ? units : 4;
+        place_of(li, mp, tq, p0, q0);
+        p0 *= 32 * units, q0 *= kXQ;
+        const int kb = (int)((long)slabs * slice / ns), ke = (int)((long)slabs * (slice + 1) / ns);
+
+        __syncthreads();   // the last tile's readers of L are done
+        if (t < kXP) {
+            // unit u is rows 32 (u / 2) of wavefront row u % 2
+            const int u = 2 * ((t >> 5) & 1) + (t >> 6), p = p0 + 32 * u + (t & 31);
+            const bool in = u < units && p < cnt;
+            const int i = lo + (in ? p : 0);
+            const int s = source_row(A.a, i);
+            int d = -1;
+            if (in && s >= 0) {
+                d = A.out_rows ? A.out_rows[i] : i;
+                d = d < 0 || d >= A.out_n ? -1 : ns > 1 ? i : d;     // (parts keep sorted order)
+            }
+            L.src[t] = s < 0 ? 0 : s;
+            L.dst[t] = d;
+        }
+        __syncthreads();
+
+        // A wavefront copies 32 rows of x, 16 an instruction, and four blocks of W;
+        // blocks past the last one read it and are not stored.
+        const char *pp[2], *qb[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            pp[i] = A.a.base + (size_t)L.src[32 * w + 16 * i + (l >> 2)] * ldx + 16 * ((l & 3) ^ ((l >> 4) & 3));
+        const char *const codes = codes_of(X, e), *const scales = scales_of(X, e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int rb = q0 / 16 + 4 * w + i;
+            qb[i] = codes + (size_t)(rb < blocks ? rb : blocks - 1) * slabs * 1024;
+        }
+        const int sb = q0 / 16 + 4 * w + (l >> 4);
+        const char *const qsp = scales + (size_t)(sb < blocks ? sb : blocks - 1) * slabs * 64 + 4 * (l & 15);
+        const char *const xsp = (const char *)X.xs + (size_t)L.src[64 * (w & 1) + l] * lds;
+        auto fetch = [&](int k, int st) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) lds_dma16(pp[i] + (size_t)k * 64, L.p[st] + (32 * w + 16 * i) * 64);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                lds_dma16(scalar_base(qb[i] + (size_t)k * 1024) + here(16 * (l ^ i)), L.q[st] + (4 * w + i) * 1024);
+            lds_dma4(qsp + (size_t)k * 64, L.qs[st] + 256 * w);
+            lds_dma4(xsp + (size_t)k * 4, &L.xs[st][64 * (w & 1)]);   // (by two wavefronts, so that all count alike)
+        };
+
+        f32x16 acc[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+        if (kb < ke) fetch(kb, 0);
+        if (kb + 1 < ke) fetch(kb + 1, 1);
+        int st = 0;
+        const bool work0 = wp < units, work1 = 2 + wp < units;
+        for (int k = kb; k < ke; ++k) {
+            // slab k is in LDS (the copies of the next one may be in flight), and slab
+            // k - 1, whose place slab k + 2 takes, is read
+            if (k + 1 < ke) wait_copies<kXCopies>();
+            else wait_copies<0>();
+            wait_lds();
+            bare_barrier();
+            if (k + 2 < ke) fetch(k + 2, st == 0 ? 2 : st - 1);
+            if (work0) {
+                const char *const P = L.p[st] + (64 * wp + b) * 64, *const Q = L.q[st] + (8 * wq + (b >> 2)) * 1024;
+                const char *const S = L.qs[st] + (8 * wq + (b >> 2)) * 64 + 16 * h + 4 * (b & 3);
+                const int key = (b >> 2) & 3;
+                u32x4 pf[2][2], qf[2][4];
+                uint32_t ps[2], qs[2];
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    qs[kk] = *(const MOE_LDS uint32_t *)(S + 32 * kk);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        qf[kk][j] = *(const MOE_LDS u32x4 *)(Q + 16 * (32 * kk + 16 * h + 4 * (b & 3) + (j ^ key)));
+                    pf[0][kk] = *(const MOE_LDS u32x4 *)(P + 16 * ((2 * kk + h) ^ key));
+                }
+                ps[0] = L.xs[st][64 * wp + b] >> (8 * h);
+                if (work1) {
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk)
+                        pf[1][kk] = *(const MOE_LDS u32x4 *)(P + 32 * 64 + 16 * ((2 * kk + h) ^ key));
+                    ps[1] = L.xs[st][64 * wp + 32 + b] >> (8 * h);
+                }
+#define MOE_MX(i, kk)                                                                                \
+    acc[i][0] = mfma32<2 * kk, 0>(pf[i][kk], qf[kk][0], acc[i][0], ps[i], qs[kk]);                   \
+    acc[i][1] = mfma32<2 * kk, 1>(pf[i][kk], qf[kk][1], acc[i][1], ps[i], qs[kk]);                   \
+    acc[i][2] = mfma32<2 * kk, 2>(pf[i][kk], qf[kk][2], acc[i][2], ps[i], qs[kk]);                   \
+    acc[i][3] = mfma32<2 * kk, 3>(pf[i][kk], qf[kk][3], acc[i][3], ps[i], qs[kk]);
+                MOE_MX(0, 0)
+                MOE_MX(0, 1)
+                if (work1) {
+                    MOE_MX(1, 0)
+                    MOE_MX(1, 1)
+                }
+#undef MOE_MX
+            }
+            st = st == 2 ? 0 : st + 1;
+        }
+
+        const int q = q0 + 128 * wq + 4 * b;
+        char *const out = ns > 1 ? (char *)(A.part + (size_t)slice * A.R * A.N) : (char *)A.out;
+        const bool f32 = ns > 1 || A.out_f32;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (2 * i + wp >= units) continue;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int to = L.dst[64 * wp + 32 * i + 8 * (v >> 2) + 4 * h + (v & 3)];
+                if (to < 0 || q >= A.N) continue;
+                const f32x4 y = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
+                const size_t at = (size_t)to * A.N + q;
+                typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+                if (f32) *(MOE_GLOBAL f32x4 *)((float *)out + at) = y;
+                else *(MOE_GLOBAL u32x2 *)((uint16_t *)out + at) =
+                         u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+            }
+        }
+    }
+}
+
+// -------------------------------------------------------- a handful of rows --
+// An entry is up to 16 rows of one expert; a tile is one block row of W (16 n) of an
+// entry over all of K, and one wavefront's. Its codes are in the order that the
+// matrix core takes them in: they go from memory straight into registers, a
+// kilobyte a load, and so do x's, whose rows the caches hold. Chunks of four slabs,
+// the next one (of the next tile too) always in flight; 16 wavefronts a compute unit.
+// No LDS and no barrier: each wavefront finds its entries by itself, from the
+// offsets in its registers.
+constexpr int kVThreads = 256, kVWaves = kVThreads / kWave;
+constexpr int kVRows = 16;       // rows of an entry
+constexpr int kVAvg = 16;        // rows per expert on average up to which this kernel runs
+constexpr int kVChunk = 4;       // slabs of a chunk
+constexpr int kVGroups = kMaxE / kWave;
+
+struct Chunk {
+    u32x4 w[kVChunk], x[kVChunk];
+    uint32_t ws[kVChunk], xs[kVChunk];
+};
+
+__global__ __launch_bounds__(kVThreads, 4) void mxfp4_stream_kernel(MxArgs X) {
+    const ProductArgs &A = X.p;
+    const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int g = l >> 4, r = l & 15;
+
+    // entries up to and with each expert, lane by lane, 64 experts a group
+    int incl[kVGroups], first[kVGroups], count[kVGroups], entries = 0;
+#pragma unroll
+    for (int i = 0; i < kVGroups; ++i) {
+        incl[i] = first[i] = count[i] = 0;
+        if (i * kWave + l < A.E) group_of_lane(A, i * kWave + l, first[i], count[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kVGroups; ++i) {
+        if (i * kWave >= A.E) break;
+        int n = (count[i] + kVRows - 1) / kVRows;
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int o = __shfl_up(n, d);
+            if (l >= d) n += o;
+        }
+        incl[i] = entries + n;
+        entries = __builtin_amdgcn_readlane(incl[i], kWave - 1);
+    }
+    // (no more than ascending offsets can give)
+    const int most = A.E + A.R / kVRows;
+    entries = entries < most ? entries : most;
+
+    const int blocks = A.N / 16, slabs = A.K / 128, chunks = (slabs + kVChunk - 1) / kVChunk;
+    const size_t ldx = (size_t)A.K / 2, lds = (size_t)A.K / 32;
+    const unsigned tiles = (unsigned)entries * blocks;          // at most 2^26
+    const unsigned me = blockIdx.x * kVWaves + w, all = kVWaves * gridDim.x;
+    const unsigned each = tiles / all, more = tiles % all;
+    const int t0 = me * each + me * more / all, t1 = (me + 1) * each + (me + 1) * more / all;
+    if (t0 >= t1) return;
+
+    // an entry's expert, rows, and this lane's row of x and of out (row r)
+    struct Entry {
+        int e, lo, src, dst;
+    };
+    auto entry = [&](int ai) {
+        Entry n = {0, 0, 0, -1};
+        int cnt = 0;
+#pragma unroll
+        for (int i = kVGroups - 1; i >= 0; --i) {
+            const unsigned long long m = __ballot(incl[i] > ai);
+            if (i * kWave >= A.E || !m) continue;
+            const int at = __ffsll(m) - 1, c = __builtin_amdgcn_readlane(count[i], at);
+            const int skip = kVRows * (ai - __builtin_amdgcn_readlane(incl[i], at) + (c + kVRows - 1) / kVRows);
+            n.e = i * kWave + at;
+            n.lo = __builtin_amdgcn_readlane(first[i], at) + skip;
+            cnt = c - skip;
+        }
+        // rows past the entry's last one read its first one's and are not stored
+        const int i = n.lo + (r < cnt ? r : 0), s = source_row(A.a, i);
+        n.src = s < 0 ? 0 : s;
+        if (r < cnt && s >= 0) {
+            const int d = A.out_rows ? A.out_rows[i] : i;
+            n.dst = d >= 0 && d < A.out_n ? d : -1;
+        }
+        return n;
+    };
+    // the next chunk to load, and the one to multiply
+    int at = t0, ac = 0, ai = t0 / blocks, arb = t0 - ai * blocks;
+    Entry ahead = entry(ai), cur = ahead;
+    const char *wb = codes_of(X, ahead.e), *sb = scales_of(X, ahead.e);
+    auto load = [&](Chunk &c) {
+        const char *const wp = wb + (size_t)arb * slabs * 1024 + 16 * l, *const sp = sb + (size_t)arb * slabs * 64 + l;
+#pragma unroll
+        for (int i = 0; i < kVChunk; ++i) {
+            const int s = ac * kVChunk + i < slabs ? ac * kVChunk + i : slabs - 1;
+            c.w[i] = load_nt16(wp + (size_t)s * 1024);
+            c.ws[i] = load_u8(sp + (size_t)s * 64);
+        }
+        const char *const xp = A.a.base + (size_t)ahead.src * ldx + 16 * g;
+        const char *const yp = (const char *)X.xs + (size_t)ahead.src * lds;
+#pragma unroll
+        for (int i = 0; i < kVChunk; ++i) {
+            const int s = ac * kVChunk + i < slabs ? ac * kVChunk + i : slabs - 1;
+            c.x[i] = load16(xp + (size_t)s * 64);
+            c.xs[i] = load_u32(yp + (size_t)s * 4);
+        }
+    };
+    auto advance = [&]() {
+        if (++ac < chunks) return;
+        if (at + 1 >= t1) {
+            ac = chunks - 1;     // the last chunk once more, which nothing multiplies
+            return;
+        }
+        ac = 0, ++at;
+        if (++arb == blocks) {
+            arb = 0;
+            ahead = entry(++ai);
+            wb = codes_of(X, ahead.e), sb = scales_of(X, ahead.e);
+        }
+    };
+    int ci = ai, crb = arb, cc = 0;
+    f32x4 sum = {0, 0, 0, 0};
+    auto multiply = [&](const Chunk &c) {
+#pragma unroll
+        for (int i = 0; i < kVChunk; ++i)
+            if (cc * kVChunk + i < slabs) sum = mfma16(c.w[i], c.x[i], sum, c.ws[i], c.xs[i] >> (8 * g));
+        if (++cc < chunks) return;
+        // lane (g, r) has n 4 g .. 4 g + 3 of row r
+        if (cur.dst >= 0) {
+            const size_t o = (size_t)cur.dst * A.N + 16 * crb + 4 * g;
+            typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+            if (A.out_f32) *(MOE_GLOBAL f32x4 *)((float *)A.out + o) = sum;
+            else *(MOE_GLOBAL u32x2 *)((uint16_t *)A.out + o) =
+                     u32x2{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
+        }
+        cc = 0, sum = f32x4{0, 0, 0, 0};
+        if (++crb == blocks) crb = 0, ++ci;
+        if (ci == ai) cur = ahead;      // (an entry ahead of the one that is multiplied is a whole entry's tiles on)
+    };
+    Chunk c0, c1;
+    load(c0);
+    for (int left = (t1 - t0) * chunks;;) {
+        advance(), load(c1);
+        multiply(c0);
+        if (--left == 0) break;
+        advance(), load(c0);
+        multiply(c1);
+        if (--left == 0) break;
+    }
+}
+
+// Whether the streaming kernel runs, from the sizes alone.
+static bool mxfp4_streams(int R, int E) { return R <= (long)kVAvg * E; }
+
+// Parts that the sum of a tile is cut into: where there are fewer tiles than compute
+// units, as many as give each one, of four slabs at least.
+static int mxfp4_slices(int R, int N, int K, int E) {
+    if (R == 0 || mxfp4_streams(R, E)) return 1;
+    const long tiles = ((long)R / kXP + (R < E ? R : E)) * ((N + kXQ - 1) / kXQ);
+    long n = compute_units() / (tiles < 1 ? 1 : tiles);
+    const long steps = K / 128;
+    n = n < steps / 4 ? n : steps / 4;
+    return n < 2 ? 1 : n > 16 ? 16 : (int)n;
+}
+
+size_t mxfp4_part_bytes(int R, int N, int K, int E) {
+    const int n = mxfp4_slices(R, N, K, E);
+    return n < 2 ? 0 : (size_t)n * R * N * sizeof(float);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_grouped_gemm_mxfp4(const uint8_t *x_e2m1, const uint8_t *x_e8m0, const int32_t *x_rows,
+                                      int x_div, int x_n, const int32_t *offsets, const uint8_t *w_e2m1,
+                                      const uint8_t *w_e8m0, const moe_expert_w *experts, int mat, int R,
+                                      int N, int K, int E, void *y, const int32_t *y_rows, int y_n,
+                                      int y_is_fp32, void *ws, size_t ws_bytes, void *stream) {
+    const int rc = check_sizes(R, N, K, E, offsets, 128);
+    if (rc != MOE_OK) return rc;
+    if (N % 16 || (mat != MOE_MAT_W13 && mat != MOE_MAT_W2)) return MOE_EINVAL;
+    if (R == 0) return MOE_OK;
+    if ((!w_e2m1) == (!experts) || (!w_e2m1) != (!w_e8m0) || !aligned16(w_e2m1) || !aligned16(w_e8m0) || !y ||
+        !aligned16(y) || !aligned16(ws))
+        return MOE_EINVAL;
+    if (!x_e8m0 || ((uintptr_t)x_e8m0 & 3) || !rows_ok(x_e2m1, x_rows, x_div, x_n, R) ||
+        y_n < (y_rows ? 1 : R))
+        return MOE_EINVAL;
+    MxArgs m{};
+    ProductArgs &a = m.p;
+    a.offsets = offsets, a.E = E, a.R = R, a.N = N, a.K = K;
+    a.a = rows_in(x_e2m1, x_rows, x_div, x_n);
+    a.m = Mats{(const char *)w_e2m1, nullptr, experts, mat};
+    a.out = y, a.out_rows = y_rows, a.out_n = y_n, a.out_f32 = y_is_fp32 != 0;
+    m.xs = x_e8m0, m.ws = w_e8m0;
+    hipStream_t s = (hipStream_t)stream;
+    const int cu = compute_units();
+    if (mxfp4_streams(R, E)) {
+        const long tiles = (long)(R < E ? R : E + R / kVRows) * (N / 16), groups = (tiles + kVWaves - 1) / kVWaves;
+        MOE_LAUNCH(K_PROD_MXFP4, mxfp4_stream_kernel, dim3((unsigned)(groups < 4L * cu ? groups : 4L * cu)),
+                   dim3(kVThreads), 0, s, m);
+        return check_launch();
+    }
+    a.slices = mxfp4_slices(R, N, K, E);
+    a.part = (float *)ws;
+    if (!ws || ws_bytes < mxfp4_part_bytes(R, N, K, E)) a.slices = 1;
+    const long tiles = ((long)R / kXP + (R < E ? R : E)) * ((N + kXQ - 1) / kXQ) * a.slices;
+    MOE_LAUNCH(K_PROD_MXFP4, mxfp4_tile_kernel, dim3((unsigned)(tiles < 2L * cu ? tiles : 2L * cu)),
+               dim3(kXThreads), 0, s, m);
+    if (a.slices > 1) launch_join(a, N, s);
+    return check_launch();
+}

@@ -311,6 +311,11 @@ int small_slices(const ProductArgs &a, int mode) {
     return n < 2 ? 1 : n > 16 ? 16 : (int)n;
 }
 
+void launch_join(const ProductArgs &a, int Qn, hipStream_t s) {
+    const long n = (long)a.R * (Qn / 4);
+    MOE_LAUNCH(K_PROD_JOIN, join_kernel<false>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, Qn);
+}
+
 void launch_product_small(const ProductArgs &a, int mode, hipStream_t s) {
     const int Qn = mode == kFwd || mode == kFwdFp8 ? a.N : a.K;
     const long tiles = small_tiles(a, mode) * a.slices;
@@ -322,10 +327,9 @@ void launch_product_small(const ProductArgs &a, int mode, hipStream_t s) {
     else if (mode == kDx) MOE_LAUNCH(kid, product_small_kernel<kDx>, grid, block, 0, s, a);
     else MOE_LAUNCH(kid, product_small_kernel<kDw>, grid, block, 0, s, a);
     if (a.slices > 1) {
-        const long n = (mode == kDw ? (long)a.E * a.N : (long)a.R) * (Qn / 4);
-        const dim3 blocks((unsigned)((n + 255) / 256));
-        if (mode == kDw) MOE_LAUNCH(K_PROD_JOIN, join_kernel<true>, blocks, dim3(256), 0, s, a, Qn);
-        else MOE_LAUNCH(K_PROD_JOIN, join_kernel<false>, blocks, dim3(256), 0, s, a, Qn);
+        const long n = (long)a.E * a.N * (Qn / 4);
+        if (mode != kDw) launch_join(a, Qn, s);
+        else MOE_LAUNCH(K_PROD_JOIN, join_kernel<true>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, Qn);
     }
 }
 

@@ -1,0 +1,490 @@
+// What stands around the experts: the norm before the layer, with the residual's
+// addition and its output in 8 or 4 bits, its gradient, and the moves of rows
+// between tokens and sorted order with the router's weights and their gradients.
+//
+//   norm      t = bf16(x + residual), inv = 1 / sqrt(mean(t^2) + eps), y = t inv w
+//   gradient  g = dy w, n = t inv:  dx = inv (g - n mean(g n)) + dtotal,
+//             dw = sum over the rows of dy n
+//   dispatch  out[at] = x[t],  at = pair_row[t][j]
+//   combine   out[t] = sum_j w[t][j] y[at] + add[t];
+//   gradient  dy[at] = w[t][j] dout[t],  dw[t][j] = <dout[t], y[at]>
+//
+// fp32 in registers with one rounding at each output; every value is read once
+// and written once, 16 bytes a lane: HBM bounds the large sizes, the launch and
+// one trip to memory the small ones.
+#include "rows.hpp"
+
+namespace moe {
+
+// ------------------------------------------------------------------- norm --
+
+constexpr int kNormThreads = 256;
+enum NormQuant { kNone = 0, kFp8 = 1, kMxfp4 = 2 };
+
+// Sum over the TPR threads of a row, in a fixed order, in every thread.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *part) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    if (TPR == kWave) return v;
+    __syncthreads();                        // (the last sum's readers are done)
+    if (lane_id() == 0) part[threadIdx.x / kWave] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int i = 1; i < TPR / kWave; ++i) v += part[i];
+    return v;
+}
+
+struct NormArgs {
+    const uint16_t *x, *res, *w;
+    float eps;
+    int R, H;
+    uint16_t *total, *y;
+    uint8_t *q;
+    void *qs;
+};
+
+// 8 columns of a row of t: x, or the rounded sum, which is stored. (total may be x
+// or res: a thread reads its columns before it writes them.)
+__device__ __forceinline__ void norm_row(const NormArgs &a, size_t at, float v[8]) {
+    unpack8(load16(a.x + at), v);
+    if (!a.res) return;
+    float b[8];
+    unpack8(load16(a.res + at), b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += b[i];
+    const u32x4 t = pack8(v);
+    unpack8(t, v);
+    if (a.total) *(MOE_GLOBAL u32x4 *)(a.total + at) = t;
+}
+
+template <int QUANT>
+__device__ __forceinline__ void norm_out(const NormArgs &a, int r, int c, const float v[8]) {
+    const bool in = c < a.H;
+    if (in && a.y) *(MOE_GLOBAL u32x4 *)(a.y + (size_t)r * a.H + c) = pack8(v);
+    if (QUANT == kFp8) {
+        i32x2 code;
+        const float s = block_to_fp8(v, code);
+        if (!in) return;
+        *(MOE_GLOBAL i32x2 *)(a.q + (size_t)r * a.H + c) = code;
+        if ((c & 127) == 0) ((MOE_GLOBAL float *)a.qs)[(size_t)r * ((a.H + 127) / 128) + c / 128] = s;
+    }
+    if (QUANT == kMxfp4) {
+        uint32_t code;
+        const uint32_t s = block_to_mxfp4(v, code);
+        if (!in) return;
+        ((MOE_GLOBAL uint32_t *)a.q)[((size_t)r * a.H + c) / 8] = code;
+        if ((c & 31) == 0) ((MOE_GLOBAL uint8_t *)a.qs)[(size_t)r * (a.H / 32) + c / 32] = (uint8_t)s;
+    }
+}
+
+// TPR threads a row (a wavefront, or the workgroup), NV vectors of 8 columns a
+// thread: the row stays in registers between the sum and the outputs. NV = 0:
+// rows of any length, read again (t from total, where it was rounded).
+template <int TPR, int NV, int QUANT>
+__global__ __launch_bounds__(kNormThreads) void norm_kernel(NormArgs a) {
+    __shared__ float part[kNormThreads / kWave];
+    const long row = block_id() * (kNormThreads / TPR) + threadIdx.x / TPR;
+    if (row >= a.R) return;                 // (whole wavefronts; whole workgroups where they meet)
+    const int r = (int)row, t = threadIdx.x % TPR;
+    const size_t at = (size_t)r * a.H;
+    float v[NV ? NV : 1][8], sum = 0.0f;
+    u32x4 w[NV ? NV : 1];
+    const int per = (a.H + 8 * TPR - 1) / (8 * TPR);
+    for (int i = 0; i < (NV ? NV : per); ++i) {
+        const int c = 8 * (t + TPR * i), k = NV ? i : 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
+        if (c < a.H) {
+            if (NV) w[k] = load16(a.w + c);
+            norm_row(a, at + c, v[k]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fmaf(v[k][j], v[k][j], sum);
+    }
+    const float inv = 1.0f / sqrtf(row_sum<TPR>(sum, part) / (float)a.H + a.eps);
+    const uint16_t *const again = a.res && a.total ? a.total : a.x;
+    for (int i = 0; i < (NV ? NV : per); ++i) {
+        const int c = 8 * (t + TPR * i), k = NV ? i : 0;
+        if (!NV) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
+            if (c < a.H) {
+                w[k] = load16(a.w + c);
+                unpack8(load16(again + at + c), v[k]);
+                if (a.res && !a.total) norm_row(a, at + c, v[k]);
+            }
+        }
+        float y[8];
+        unpack8(w[k], y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = c < a.H ? v[k][j] * inv * y[j] : 0.0f;
+        norm_out<QUANT>(a, r, c, y);
+    }
+}
+
+struct NormGradArgs {
+    const uint16_t *x, *w, *dy, *dt;
+    float eps;
+    int R, H;
+    uint16_t *dx;
+    float *part;              // [slots][H], or NULL
+    int slots;
+};
+
+// Slot s takes the rows s, s + slots, ...: TPR threads, whose part of dw stays in
+// registers over the rows and goes to row s of `part`, which norm_join adds up.
+template <int TPR, int NV>
+__global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(NormGradArgs a) {
+    __shared__ float part[2][kNormThreads / kWave];
+    const int slot = blockIdx.x * (kNormThreads / TPR) + threadIdx.x / TPR, t = threadIdx.x % TPR;
+    if (slot >= a.slots) return;
+    float dw[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+    for (long r = slot; r < a.R; r += a.slots) {
+        const size_t at = (size_t)r * a.H;
+        u32x4 xq[NV], gq[NV], tq[NV];
+        float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = 8 * (t + TPR * i);
+            xq[i] = gq[i] = tq[i] = u32x4{0, 0, 0, 0};
+            if (c < a.H) {
+                xq[i] = load_nt16(a.x + at + c);
+                gq[i] = load_nt16(a.dy + at + c);
+                if (a.dt) tq[i] = load_nt16(a.dt + at + c);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = 8 * (t + TPR * i);
+            float x[8], g[8], w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            unpack8(xq[i], x), unpack8(gq[i], g);
+            if (c < a.H) unpack8(load16(a.w + c), w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                ss = fmaf(x[j], x[j], ss);
+                dot = fmaf(g[j] * w[j], x[j], dot);
+            }
+        }
+        ss = row_sum<TPR>(ss, part[0]);
+        dot = row_sum<TPR>(dot, part[1]);
+        const float inv = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+        const float mean = dot * inv / (float)a.H;              // mean(g n)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = 8 * (t + TPR * i);
+            if (c >= a.H) continue;
+            float x[8], g[8], w[8], d[8];
+            unpack8(xq[i], x), unpack8(gq[i], g), unpack8(load16(a.w + c), w), unpack8(tq[i], d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float n = x[j] * inv;
+                dw[i][j] = fmaf(g[j], n, dw[i][j]);
+                d[j] += inv * (g[j] * w[j] - n * mean);
+            }
+            *(MOE_GLOBAL u32x4 *)(a.dx + at + c) = pack8(d);
+        }
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = 8 * (t + TPR * i);
+        if (c >= a.H) continue;
+        float *const o = a.part + (size_t)slot * a.H + c;
+        *(MOE_GLOBAL f32x4 *)o = f32x4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+        *(MOE_GLOBAL f32x4 *)(o + 4) = f32x4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+    }
+}
+
+// dw: the slots' parts, 64 columns a workgroup: 16 groups of slots, each in order,
+// then the groups in order.
+__global__ __launch_bounds__(256) void norm_join_kernel(const float *__restrict__ part, int slots, int H,
+                                                        int accumulate, float *__restrict__ dw) {
+    __shared__ f32x4 sums[16][16];
+    const int l = threadIdx.x & 15, g = threadIdx.x >> 4, c = 64 * blockIdx.x + 4 * l;
+    const int s0 = (int)((long)slots * g / 16), s1 = (int)((long)slots * (g + 1) / 16);
+    f32x4 v = {0, 0, 0, 0};
+    if (c < H) {
+#pragma unroll 8
+        for (int s = s0; s < s1; ++s) v += *(const MOE_GLOBAL f32x4 *)(part + (size_t)s * H + c);
+    }
+    sums[g][l] = v;
+    __syncthreads();
+    if (g || c >= H) return;
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v += sums[i][l];
+    MOE_GLOBAL f32x4 *const o = (MOE_GLOBAL f32x4 *)(dw + c);
+    *o = accumulate ? *o + v : v;
+}
+
+// ------------------------------------------------------------------ moves --
+
+// Row that pair p stands at, or -1 where it is none of the n there are.
+__device__ __forceinline__ int pair_at(const int32_t *pair_row, size_t p, int n) {
+    const int r = pair_row[p];
+    return r >= 0 && r < n ? r : -1;
+}
+
+// 8 columns of one token a thread: read once, written to its k rows.
+__global__ __launch_bounds__(256) void dispatch_kernel(const uint16_t *__restrict__ x,
+                                                       const int32_t *__restrict__ pair_row, int T, int k,
+                                                       int H, Divisor by, uint16_t *__restrict__ out,
+                                                       int out_n) {
+    const int per = H / 8;
+    const long id = block_id() * blockDim.x + threadIdx.x, t = row_of_unit(id, 8, per, by);
+    if (t >= T) return;
+    const int c = (int)(id - t * per) * 8;
+    const u32x4 v = load_nt16(x + (size_t)t * H + c);
+    for (int j = 0; j < k; ++j) {
+        const int r = pair_at(pair_row, (size_t)t * k + j, out_n);
+        if (r >= 0) *(MOE_GLOBAL u32x4 *)(out + (size_t)r * H + c) = v;
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void load_row8(const void *y, size_t at, float v[8]) {
+    if (F32) {
+        const f32x4 a = *(const MOE_GLOBAL f32x4 *)((const float *)y + at);
+        const f32x4 b = *(const MOE_GLOBAL f32x4 *)((const float *)y + at + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+    } else {
+        unpack8(load_nt16((const uint16_t *)y + at), v);
+    }
+}
+
+// 8 columns of one token a thread; the rows of up to KB pairs are loaded together.
+template <bool F32, int KB>
+__global__ __launch_bounds__(64) void combine_rows_kernel(const void *__restrict__ y, int y_n,
+                                                          const int32_t *__restrict__ pair_row,
+                                                          const float *__restrict__ w,
+                                                          const uint16_t *__restrict__ add, int T, int k,
+                                                          int H, Divisor by, uint16_t *__restrict__ out) {
+    const int per = H / 8;
+    const long id = block_id() * blockDim.x + threadIdx.x, t = row_of_unit(id, 6, per, by);
+    if (t >= T) return;
+    const int c = (int)(id - t * per) * 8;
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int j0 = 0; j0 < k; j0 += KB) {
+        float v[KB][8], f[KB];
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            const int r = j0 + j < k ? pair_at(pair_row, (size_t)t * k + j0 + j, y_n) : -1;
+            f[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+            if (r >= 0) {
+                f[j] = w ? w[(size_t)t * k + j0 + j] : 1.0f;
+                load_row8<F32>(y, (size_t)r * H + c, v[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] = fmaf(f[j], v[j][i], sum[i]);
+    }
+    if (add) {
+        float v[8];
+        unpack8(load_nt16(add + (size_t)t * H + c), v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += v[i];
+    }
+    *(MOE_GLOBAL u32x4 *)(out + (size_t)t * H + c) = pack8(sum);
+}
+
+// One wavefront a pair; the pairs of a token are neighbours, so that dout's row
+// comes from the caches for all but one of them.
+__global__ __launch_bounds__(256) void combine_rows_grad_kernel(
+    const uint16_t *__restrict__ dout, const uint16_t *__restrict__ y, int y_n,
+    const int32_t *__restrict__ pair_row, const float *__restrict__ w, long pairs, int k, Divisor by, int H,
+    uint16_t *__restrict__ dy, float *__restrict__ dw) {
+    constexpr int U = 4;
+    const long p = block_id() * (blockDim.x / kWave) + threadIdx.x / kWave;
+    if (p >= pairs) return;
+    const int l = lane_id(), r = pair_at(pair_row, (size_t)p, y_n);
+    const size_t from = (size_t)((uint32_t)p / by) * H, at = (size_t)(r < 0 ? 0 : r) * H;
+    const float f = w ? w[p] : 1.0f;
+    float sum = 0.0f;
+    if (r >= 0) {
+        for (int c0 = 8 * l; c0 < H; c0 += 8 * kWave * U) {
+            u32x4 dq[U], yq[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int c = c0 + 8 * kWave * i;
+                dq[i] = yq[i] = u32x4{0, 0, 0, 0};
+                if (c < H) {
+                    dq[i] = load16(dout + from + c);
+                    if (dw) yq[i] = load_nt16(y + at + c);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int c = c0 + 8 * kWave * i;
+                float d[8], v[8];
+                unpack8(dq[i], d), unpack8(yq[i], v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    sum = fmaf(d[j], v[j], sum);
+                    d[j] *= f;
+                }
+                if (dy && c < H) *(MOE_GLOBAL u32x4 *)(dy + at + c) = pack8(d);
+            }
+        }
+    }
+    if (!dw) return;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    if (l == 0) dw[p] = sum;
+}
+
+// ------------------------------------------------------------------- host --
+
+template <int QUANT>
+static void launch_norm(const NormArgs &a, hipStream_t s) {
+    const dim3 block(kNormThreads);
+    if (a.H <= 1024) {
+        const dim3 grid = blocks_of(((long)a.R + 3) / 4);
+        if (a.H <= 512) MOE_LAUNCH(K_NORM, (norm_kernel<64, 1, QUANT>), grid, block, 0, s, a);
+        else MOE_LAUNCH(K_NORM, (norm_kernel<64, 2, QUANT>), grid, block, 0, s, a);
+        return;
+    }
+    const dim3 grid = blocks_of(a.R);
+    if (a.H <= 2048) MOE_LAUNCH(K_NORM, (norm_kernel<256, 1, QUANT>), grid, block, 0, s, a);
+    else if (a.H <= 4096) MOE_LAUNCH(K_NORM, (norm_kernel<256, 2, QUANT>), grid, block, 0, s, a);
+    else if (a.H <= 8192) MOE_LAUNCH(K_NORM, (norm_kernel<256, 4, QUANT>), grid, block, 0, s, a);
+    else MOE_LAUNCH(K_NORM, (norm_kernel<256, 0, QUANT>), grid, block, 0, s, a);
+}
+
+constexpr int kMaxGradH = 16384;     // columns whose dw stays in the registers of 256 threads
+
+// Two workgroups a compute unit, eight wavefronts.
+static int grad_slots(int R, int H) {
+    const int most = (H <= 1024 ? 8 : 2) * compute_units();
+    return R < most ? R : most;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+static bool eps_ok(float eps) { return eps >= 0.0f && eps <= 3.0e38f; }
+
+extern "C" int moe_rms_norm(const uint16_t *x_bf16, const uint16_t *residual_bf16,
+                            const uint16_t *weight_bf16, float eps, int R, int H, uint16_t *total_bf16,
+                            uint16_t *y_bf16, int quant, uint8_t *q, void *q_scale, void *stream) {
+    if (!row_sizes_ok(R, H) || !eps_ok(eps) || quant < kNone || quant > kMxfp4) return MOE_EINVAL;
+    if (quant == kMxfp4 && H % 32) return MOE_EINVAL;
+    if (R == 0) return MOE_OK;
+    if (!al16(x_bf16) || !al16(weight_bf16) || ((uintptr_t)residual_bf16 & 15) ||
+        ((uintptr_t)total_bf16 & 15) || ((uintptr_t)y_bf16 & 15))
+        return MOE_EINVAL;
+    if (total_bf16 && !residual_bf16) return MOE_EINVAL;
+    if (quant != kNone ? !al16(q) || !q_scale || ((uintptr_t)q_scale & (quant == kFp8 ? 3 : 0)) : !y_bf16)
+        return MOE_EINVAL;
+    const NormArgs a{x_bf16, residual_bf16, weight_bf16, eps, R, H, total_bf16, y_bf16, q, q_scale};
+    if (quant == kNone) launch_norm<kNone>(a, (hipStream_t)stream);
+    else if (quant == kFp8) launch_norm<kFp8>(a, (hipStream_t)stream);
+    else launch_norm<kMxfp4>(a, (hipStream_t)stream);
+    return check_launch();
+}
+
+extern "C" int moe_rms_norm_grad_workspace(int R, int H, size_t *bytes) {
+    if (!row_sizes_ok(R, H) || H > kMaxGradH || !bytes) return MOE_EINVAL;
+    *bytes = (size_t)grad_slots(R, H) * H * sizeof(float);
+    return MOE_OK;
+}
+
+extern "C" int moe_rms_norm_grad(const uint16_t *x_bf16, const uint16_t *weight_bf16,
+                                 const uint16_t *dy_bf16, const uint16_t *dtotal_bf16, float eps, int R,
+                                 int H, uint16_t *dx_bf16, float *dw, int accumulate, void *ws,
+                                 size_t ws_bytes, void *stream) {
+    if (!row_sizes_ok(R, H) || H > kMaxGradH || !eps_ok(eps)) return MOE_EINVAL;
+    const int slots = grad_slots(R, H);
+    if (((uintptr_t)dw & 15) || ((uintptr_t)ws & 15)) return MOE_EINVAL;
+    if (dw && R > 0 && (!ws || ws_bytes < (size_t)slots * H * sizeof(float))) return MOE_EINVAL;
+    if (R > 0 && (!al16(x_bf16) || !al16(weight_bf16) || !al16(dy_bf16) || !al16(dx_bf16) ||
+                  ((uintptr_t)dtotal_bf16 & 15)))
+        return MOE_EINVAL;
+    hipStream_t s = (hipStream_t)stream;
+    if (R > 0) {
+        const NormGradArgs a{x_bf16, weight_bf16, dy_bf16, dtotal_bf16, eps, R, H, dx_bf16,
+                             dw ? (float *)ws : nullptr, slots};
+        const dim3 block(kNormThreads);
+        if (H <= 1024) {
+            const dim3 grid((unsigned)((slots + 3) / 4));
+            if (H <= 512) MOE_LAUNCH(K_NORM_GRAD, (norm_grad_kernel<64, 1>), grid, block, 0, s, a);
+            else MOE_LAUNCH(K_NORM_GRAD, (norm_grad_kernel<64, 2>), grid, block, 0, s, a);
+        } else {
+            const dim3 grid((unsigned)slots);
+            if (H <= 2048) MOE_LAUNCH(K_NORM_GRAD, (norm_grad_kernel<256, 1>), grid, block, 0, s, a);
+            else if (H <= 4096) MOE_LAUNCH(K_NORM_GRAD, (norm_grad_kernel<256, 2>), grid, block, 0, s, a);
+            else if (H <= 8192) MOE_LAUNCH(K_NORM_GRAD, (norm_grad_kernel<256, 4>), grid, block, 0, s, a);
+            else MOE_LAUNCH(K_NORM_GRAD, (norm_grad_kernel<256, 8>), grid, block, 0, s, a);
+        }
+        const int rc = check_launch();
+        if (rc != MOE_OK) return rc;
+    }
+    if (!dw) return MOE_OK;
+    MOE_LAUNCH(K_NORM_JOIN, norm_join_kernel, dim3((unsigned)((H + 63) / 64)), dim3(256), 0, s,
+               (const float *)ws, R > 0 ? slots : 0, H, accumulate != 0, dw);
+    return check_launch();
+}
+
+// Sizes of the moves: T tokens of k pairs each.
+static bool moves_ok(int T, int k, int H) {
+    return T >= 0 && k >= 1 && row_sizes_ok(T, H) && (long)T * k <= kMaxRows;
+}
+
+extern "C" int moe_dispatch(const uint16_t *x_bf16, const int32_t *pair_row, int T, int k, int H,
+                            uint16_t *out_bf16, int out_n, void *stream) {
+    if (!moves_ok(T, k, H) || out_n < 0) return MOE_EINVAL;
+    if (T == 0) return MOE_OK;
+    if (!al16(x_bf16) || !pair_row || !al16(out_bf16)) return MOE_EINVAL;
+    const long blocks = ((long)T * (H / 8) + 255) / 256;
+    if (!blocks_ok(blocks)) return MOE_EINVAL;
+    MOE_LAUNCH(K_DISPATCH, dispatch_kernel, blocks_of(blocks), dim3(256), 0, (hipStream_t)stream, x_bf16,
+               pair_row, T, k, H, divisor(H / 8), out_bf16, out_n);
+    return check_launch();
+}
+
+extern "C" int moe_combine_rows(const void *y, int y_is_fp32, int y_n, const int32_t *pair_row,
+                                const float *w, const uint16_t *add_bf16, int T, int k, int H,
+                                uint16_t *out_bf16, void *stream) {
+    if (!moves_ok(T, k, H) || y_n < 0) return MOE_EINVAL;
+    if (T == 0) return MOE_OK;
+    if (!al16(y) || !pair_row || ((uintptr_t)add_bf16 & 15) || !al16(out_bf16)) return MOE_EINVAL;
+    const long blocks = ((long)T * (H / 8) + 63) / 64;
+    if (!blocks_ok(blocks)) return MOE_EINVAL;
+    hipStream_t s = (hipStream_t)stream;
+#define MOE_CR(F32, KB)                                                                             \
+    MOE_LAUNCH(K_COMBINE_ROWS, (combine_rows_kernel<F32, KB>), blocks_of(blocks), dim3(64), 0, s, y, \
+               y_n, pair_row, w, add_bf16, T, k, H, divisor(H / 8), out_bf16)
+    if (k <= 2) {
+        if (y_is_fp32) MOE_CR(true, 2);
+        else MOE_CR(false, 2);
+    } else {
+        if (y_is_fp32) MOE_CR(true, 8);
+        else MOE_CR(false, 8);
+    }
+#undef MOE_CR
+    return check_launch();
+}
+
+extern "C" int moe_combine_rows_grad(const uint16_t *dout_bf16, const uint16_t *y_bf16, int y_n,
+                                     const int32_t *pair_row, const float *w, int T, int k, int H,
+                                     uint16_t *dy_bf16, float *dw, void *stream) {
+    if (!moves_ok(T, k, H) || y_n < 0) return MOE_EINVAL;
+    if (T == 0) return MOE_OK;
+    if (!al16(dout_bf16) || !pair_row || ((uintptr_t)dy_bf16 & 15) || (!dy_bf16 && !dw)) return MOE_EINVAL;
+    if (dw && !al16(y_bf16)) return MOE_EINVAL;
+    const long pairs = (long)T * k;
+    MOE_LAUNCH(K_COMBINE_ROWS_GRAD, combine_rows_grad_kernel, blocks_of((pairs + 3) / 4), dim3(256), 0,
+               (hipStream_t)stream, dout_bf16, y_bf16, y_n, pair_row, w, pairs, k, divisor(k), H, dy_bf16,
+               dw);
+    return check_launch();
+}

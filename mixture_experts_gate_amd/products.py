@@ -1,8 +1,9 @@
 """The expert products as calls on tensors, on top of the C ABI.
 
-For experts whose matrices are bf16 (with both gradients, for training) or FP8
-with a scale per 128 x 128 block: the products grouped by expert, the gated
-activation between them with its gradient, and rows to FP8. Every call checks
+For experts whose matrices are bf16 (with both gradients, for training), FP8
+with a scale per 128 x 128 block or MXFP4 (E2M1 codes with an E8M0 scale per 32
+columns): the products grouped by expert, the gated activation between them with
+its gradient, and rows to FP8 and MXFP4. Every call checks
 its tensors (types, shapes, contiguity, one device), allocates what it is not
 given, and enqueues one kernel of ``libmoe.so`` on the current stream of the
 tensors' device, or on ``stream`` (a torch stream or the handle of one). Nothing
@@ -45,6 +46,7 @@ from . import _lib
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
 _OUT = (torch.bfloat16, torch.float32)
+_U8, _E8M0 = (torch.uint8,), (torch.uint8, torch.float8_e8m0fnu)
 
 
 class TableMatrices(NamedTuple):
@@ -273,6 +275,42 @@ def grouped_matmul_fp8(x, x_scale, w, w_scale=None, offsets=None, *, rows=None, 
     return out
 
 
+def grouped_matmul_mxfp4(x, x_scale, w, w_scale=None, offsets=None, *, rows=None, div=1,
+                         out_rows=None, out=None, ws=None, stream=None):
+    """y[i] = W_e x[i] over sorted rows from MXFP4: x E2M1 codes [n, K/2] (uint8) with
+    E8M0 scales [n, K/32] (from ``quant_mxfp4``), w in the kernel layout, codes [E, N,
+    K/2] with scales [E, N, K/32] (from ``quant_mxfp4_matrices``) or the
+    ``TableMatrices`` of packed "mxfp4" blobs -> [R, N] bf16 or fp32. N is a multiple
+    of 16, K of 128."""
+    dev = _matrix(x, "x", _U8).get_device()
+    _no_history(w)
+    if isinstance(w, TableMatrices):
+        pw, ps, tab, mat, E, N, K = _weights(w, w_scale, _U8, dev)
+    else:
+        _need(w, "w", _U8, dev)
+        if w.dim() not in (2, 3):
+            _fail(f"w: [E, N, K/2] or [N, K/2] is needed, got {tuple(w.shape)}")
+        E, N, K = (1, *w.shape) if w.dim() == 2 else w.shape
+        K *= 2
+        _int(max(E, N, K), "w")
+        _need(w_scale, "w_scale", _E8M0, dev)
+        if w_scale.shape[-2:] != (N, K // 32) or w_scale.numel() != E * N * (K // 32):
+            _fail(f"w_scale: {tuple(w_scale.shape)}, [E, {N}, {K // 32}] is needed")
+        pw, ps, tab, mat = w.data_ptr(), w_scale.data_ptr(), None, 0
+    if 2 * x.shape[1] != K:
+        _fail(f"x: {2 * x.shape[1]} columns, w has {K}")
+    if _matrix(x_scale, "x_scale", _E8M0, dev).shape != (x.shape[0], K // 32):
+        _fail(f"x_scale: {tuple(x_scale.shape)}, [{x.shape[0]}, {K // 32}] is needed")
+    R = _count(x, rows, "rows")
+    out = _rows_output(out, "out", R, N, out_rows, _OUT, dev, stream)
+    ws, pws, nws = _workspace(_lib.MOE_GEMM_MXFP4, R, N, K, E, dev, stream, ws)
+    _run("moe_grouped_gemm_mxfp4", dev, stream, x.data_ptr(), x_scale.data_ptr(),
+         _index(rows, "rows", R, dev), _int(div, "div"), x.shape[0], _offsets(offsets, E, dev), pw, ps, tab,
+         mat, R, N, K, E, out.data_ptr(), _index(out_rows, "out_rows", R, dev), out.shape[0],
+         int(out.dtype is torch.float32), pws, nws)
+    return out
+
+
 def grouped_matmul_dx(dy, w, offsets=None, *, rows=None, div=1, out_rows=None, out=None,
                       ws=None, stream=None):
     """dx[i] = W_e^T dy[i] over sorted rows: dy bf16 [n, N], w bf16 -> [R, K]
@@ -408,3 +446,54 @@ def swiglu_quant_fp8(h, n_rows=None, q=None, s=None, stream=None):
     R, I, dev = _halves(h)
     _no_history(h)
     return _to_fp8("moe_swiglu_quant_fp8", h, R, I, n_rows, q, s, dev, stream)
+
+
+def _to_mxfp4(fn, x, R, K, n_rows, q, s, dev, stream):
+    if K % 32:
+        _fail(f"{K} columns, a multiple of 32 is needed")
+    q = _output(q, "q", (R, K // 2), _U8, dev, stream)
+    s = _output(s, "s", (R, K // 32), _E8M0, dev, stream)
+    if q.shape != (R, K // 2) or s.shape != (R, K // 32):
+        _fail(f"q, s: {tuple(q.shape)}, {tuple(s.shape)} for {R} rows of {K}")
+    _run(fn, dev, stream, x.data_ptr(), _limit(n_rows, dev), R, K, q.data_ptr(), s.data_ptr())
+    return q, s
+
+
+def quant_mxfp4(x, n_rows=None, q=None, s=None, stream=None):
+    """Rows x bf16 [R, K] in MXFP4: (E2M1 codes uint8 [R, K/2], the even column in the
+    low half, E8M0 scales uint8 [R, K/32]): scale = 2^(floor(log2 amax) - 2), at least
+    2^-127, over 32 columns of a row, code = x / scale to the nearest of 0, 0.5, 1, 1.5,
+    2, 3, 4, 6 (ties to the even code). An infinity or NaN makes its block's scale NaN.
+    ``n_rows`` as for ``swiglu``. K is a multiple of 32."""
+    dev = _matrix(x, "x", _BF16).get_device()
+    _no_history(x)
+    return _to_mxfp4("moe_quant_mxfp4", x, x.shape[0], x.shape[1], n_rows, q, s, dev, stream)
+
+
+def swiglu_quant_mxfp4(h, n_rows=None, q=None, s=None, stream=None):
+    """``quant_mxfp4`` of the fp32 values silu(g) u of rows h [R, 2I] = [g | u]."""
+    R, I, dev = _halves(h)
+    _no_history(h)
+    return _to_mxfp4("moe_swiglu_quant_mxfp4", h, R, I, n_rows, q, s, dev, stream)
+
+
+def quant_mxfp4_matrices(w, q=None, s=None, stream=None):
+    """Matrices w bf16 [E, N, K] (or [N, K]) in MXFP4, their rows as ``quant_mxfp4``
+    has them, in the kernel layout that ``grouped_matmul_mxfp4`` reads (blocks of 16
+    rows x 128 columns, include/moe.h): (codes [E, N, K/2], scales [E, N, K/32]). N is a
+    multiple of 16, K of 128."""
+    dev = _need(w, "w", _BF16).get_device()
+    _no_history(w)
+    if w.dim() not in (2, 3):
+        _fail(f"w: [E, N, K] or [N, K] is needed, got {tuple(w.shape)}")
+    E, N, K = (1, *w.shape) if w.dim() == 2 else w.shape
+    if N % 16 or K % 128:
+        _fail(f"w: {N} x {K}, multiples of 16 and 128 are needed")
+    _int(max(E, N, K), "w")
+    lead = w.shape[:-1]
+    q = _output(q, "q", (*lead, K // 2), _U8, dev, stream)
+    s = _output(s, "s", (*lead, K // 32), _E8M0, dev, stream)
+    if q.shape != (*lead, K // 2) or s.shape != (*lead, K // 32):
+        _fail(f"q, s: {tuple(q.shape)}, {tuple(s.shape)} for {tuple(w.shape)}")
+    _run("moe_quant_mxfp4_matrices", dev, stream, w.data_ptr(), E, N, K, q.data_ptr(), s.data_ptr())
+    return q, s
