@@ -36,17 +36,6 @@ namespace moe {
 constexpr int kPThreads = 512;   // 8 wavefronts: 2 along p x 4 along q
 constexpr int kBP = 256, kBQ = 256;   // p and q per tile
 
-// Barrier without a memory fence (a fenced one would wait for the copies in
-// flight); the compiler keeps memory accesses and matrix instructions on
-// their side of it.
-__device__ __forceinline__ void phase_barrier() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" ::: "memory");
-}
-
 struct TileLds {
     char p[2][kBP * 128];
     char q[2][kBQ * 128];

@@ -227,6 +227,15 @@ __device__ __forceinline__ void bare_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// The same, and the compiler keeps matrix instructions on their side of it too.
+__device__ __forceinline__ void phase_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
 // Whether q is the row of the matrix instruction's result (Q its A operand) or
 // its column. dx: row, see below; FP8: row, so that a lane's four results share
 // one p and one scale (as column, with four scales a lane: 632 against 530 us

@@ -27,6 +27,11 @@ __device__ __forceinline__ const char *scales_of(const MxArgs &A, int e) {
     return (const char *)A.ws + (size_t)e * a.N * (a.K / 32);
 }
 
+template <int V>
+struct Const {
+    static constexpr int v = V;
+};
+
 // Bytes OA and OB of the scale registers scale this lane's 32 codes of a and b.
 template <int OA, int OB>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
@@ -56,6 +61,25 @@ constexpr int kXThreads = 256;
 constexpr int kXP = 128, kXQ = 256;
 constexpr int kXS = 3;           // slabs in LDS
 constexpr int kXCopies = 8;      // copy instructions of a wavefront and slab
+
+// 32 rows of a wavefront's results, four columns from q, to the rows of out in `dst`.
+// (The results are pinned to their registers first: the compiler would keep them in the
+// order of the stores throughout the sum, and spill 160 registers.)
+__device__ __forceinline__ void store_rows(const ProductArgs &A, char *out, bool f32, const int *dst, int q, int h,
+                                           f32x16 (&acc)[4]) {
+    typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[j]));
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+        const int to = dst[8 * (v >> 2) + 4 * h + (v & 3)];
+        if (to < 0 || q >= A.N) continue;
+        const f32x4 y = {acc[0][v], acc[1][v], acc[2][v], acc[3][v]};
+        const size_t at = (size_t)to * A.N + q;
+        if (f32) *(MOE_GLOBAL f32x4 *)((float *)out + at) = y;
+        else *(MOE_GLOBAL u32x2 *)((uint16_t *)out + at) = u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+    }
+}
 
 struct TileLds {
     char p[kXS][kXP * 64];       // rows of 64 bytes, 16-byte pieces XORed with row / 4
@@ -194,25 +218,302 @@ __global__ __launch_bounds__(kXThreads, 2) void mxfp4_tile_kernel(MxArgs X) {
             st = st == 2 ? 0 : st + 1;
         }
 
-        const int q = q0 + 128 * wq + 4 * b;
         char *const out = ns > 1 ? (char *)(A.part + (size_t)slice * A.R * A.N) : (char *)A.out;
-        const bool f32 = ns > 1 || A.out_f32;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (2 * i + wp < units)
+                store_rows(A, out, ns > 1 || A.out_f32, L.dst + 64 * wp + 32 * i, q0 + 128 * wq + 4 * b, h, acc[i]);
+    }
+}
+
+// ------------------------------------------------------------ large tiles --
+// 256 x 256 a workgroup of eight wavefronts, 64 x 128 each as above, one workgroup a
+// compute unit: two thirds of the bytes that tiles of 128 x 256 copy into LDS. The
+// wavefronts of a SIMD (w and w + 4) run one phase apart: one reads a slab's fragments
+// and issues copies while the other multiplies; a barrier ends each phase.
+//
+// LDS holds four slabs, two pairs. The copies run three slabs ahead, and on into the
+// next tile, whose rows are looked up during this one's first slabs: only a workgroup's
+// first tile waits for its first slab. Scales come a pair at a time (8 bytes a row,
+// 128 a block). What a phase may take, the other wavefront's 512 cycles of matrix
+// instructions, is about a hundred instructions: hence pairs, whose places in LDS are
+// constants, 32-bit offsets from uniform addresses for copies and stores, and no branch
+// a row in the stores (rows of none lie outside the buffer's range).
+constexpr int kBThreads = 512;
+constexpr int kBT = 256;         // rows and n of a tile
+constexpr int kBSlabs = 6;       // slabs of K from which this kernel runs, an even number:
+                                 // a tile's copies begin three before the end of the last
+                                 // tile, which by then has looked up its rows
+constexpr uint32_t kBBytes = 0x7FFFFFF0u;    // bytes of out at most; offsets from here on are not stored
+constexpr int kBPair = 32768;    // bytes of a pair of slabs of p or q
+
+struct LargeLds {
+    char p[2][kBPair], q[2][kBPair];             // slabs as in TileLds, 256 rows each
+    uint32_t xs[2][kBT][2];                      // rows' scales, of a pair
+    char qs[2][8][288];                          // two blocks' scales, of a pair (32 bytes on
+                                                 // for every two: 8 blocks in different banks)
+    int raw[kBT], rawo[kBT];                     // the next tile's indices into x and out
+    uint32_t to[2][kBT];                         // offset of rows in out, by tile
+    int base[kMaxE + 1];                         // p tiles before each expert
+    int wsum[kBThreads / kWave];
+};
+
+template <int N>
+__device__ __forceinline__ void wait_some(int more) {      // until N + more are in flight, more 0, 16 or 32
+    if (more == 0) wait_copies<N>();
+    else if (more == 16) wait_copies<N + 16>();
+    else wait_copies<N + 32>();
+}
+
+__global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
+    const ProductArgs &A = X.p;
+    __shared__ LargeLds L;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int l = lane_id(), h = l >> 5, b = l & 31;
+    const int wq = w & 1, wp = w >> 1;
+    const int tq = (A.N + kBT - 1) / kBT, slabs = A.K / 128, blocks = A.N / 16;
+    total_tiles<kBThreads>(A, kBT, L.base, L.wsum);
+    const int total = L.base[A.E] * tq;
+    const int nx = gridDim.x >= 8 ? 8 : 1;      // workgroup b runs on XCD b % 8
+    const int xcd = blockIdx.x % nx, per = ((int)gridDim.x - xcd + nx - 1) / nx;
+    const int t0 = (int)((long)total * xcd / nx), t1 = (int)((long)total * (xcd + 1) / nx);
+    int si = t0 + (int)blockIdx.x / nx;
+    if (si >= t1) return;
+
+    struct Tile {
+        int e, lo, cnt, p0, q0, units;
+    };
+    auto locate = [&](int ti, int e) {
+        Tile t;
+        t.e = e;
+        const int mp = __builtin_amdgcn_readfirstlane(L.base[e + 1] - L.base[e]);
+        const int li = ti - __builtin_amdgcn_readfirstlane(L.base[e]) * tq;
+        group_of(A, e, t.lo, t.cnt);
+        // rows spread evenly over the expert's tiles, in units of 32 (more than
+        // eight only where offsets do not ascend)
+        const int units = (int)((t.cnt + 32u * mp - 1) / (32u * mp));
+        t.units = units < 8 ? units : 8;
+        place_of(li, mp, tq, t.p0, t.q0);
+        t.p0 *= 32 * t.units, t.q0 *= kBT;
+        return t;
+    };
+    // the expert of a later tile: 64 experts a look
+    auto expert_from = [&](int e, int ti) {
+        for (;; e += kWave) {
+            const int i = e + 1 + l < A.E ? e + 1 + l : A.E;
+            const unsigned long long m = __ballot((long)L.base[i] * tq > ti);
+            if (m) return e + __ffsll(m) - 1;
+        }
+    };
+    // row `row` of LDS: unit u is rows 32 (u / 4) of wavefront row u % 4; -1: past the end
+    auto place = [&](const Tile &t, int row) {
+        const int u = 4 * ((row >> 5) & 1) + (row >> 6), p = t.p0 + 32 * u + (row & 31);
+        return u < t.units && p < t.cnt ? p : -1;
+    };
+    const uint32_t ldo = (uint32_t)A.N * (A.out_f32 ? 4 : 2);
+    auto out_at = [&](const Tile &t, int row, int raw, int rawo) {
+        const int p = place(t, row);
+        if (p < 0 || (A.a.idx && row_of_index(A.a, raw) < 0)) return kBufOff;
+        const int d = A.out_rows ? rawo : t.lo + p;
+        return d >= 0 && d < A.out_n ? (uint32_t)d * ldo : kBufOff;
+    };
+    auto index_at = [&](const Tile &t, int row) {
+        const int p = place(t, row);
+        return t.lo + (p < 0 ? 0 : p);      // (a row past the end reads the expert's first one)
+    };
+
+    Tile cur = locate(si, expert_of(L.base, A.E, tq, si)), next = cur;
+    bool more = si + per < t1;
+    // the first tile's rows, from memory
+    if (threadIdx.x < kBT) {
+        const int t = threadIdx.x, i = index_at(cur, t);
+        const int raw = A.a.idx ? A.a.idx[i] : 0;
+        L.raw[t] = raw;
+        L.to[0][t] = out_at(cur, t, raw, A.out_rows ? A.out_rows[i] : 0);
+    }
+    __syncthreads();
+
+    // Copies: a wavefront takes 32 rows of x, 16 an instruction, and two blocks of W.
+    // The lane's offsets into x, its scales and W's, and the wavefront's blocks, by tile.
+    uint32_t po[2], xo, so;
+    const char *qb[2], *sb;
+    auto enter = [&](const Tile &t) {
+        auto row_at = [&](int row) {
+            const int r = A.a.idx ? row_of_index(A.a, L.raw[row]) : index_at(t, row);
+            return (uint32_t)(r < 0 ? 0 : r);
+        };
+        const int rb = t.q0 / 16 + 2 * w;
+        const char *const codes = codes_of(X, t.e);
+        sb = scales_of(X, t.e);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (2 * i + wp >= units) continue;
+            po[i] = row_at(32 * w + 16 * i + (l >> 2)) * (uint32_t)(A.K / 2) + 16 * ((l & 3) ^ ((l >> 4) & 3));
+            qb[i] = codes + (size_t)(rb + i < blocks ? rb + i : blocks - 1) * slabs * 1024;
+        }
+        xo = row_at(32 * w + (l >> 1)) * (uint32_t)(A.K / 32) + 4 * (l & 1);
+        so = (uint32_t)((rb + h < blocks ? rb + h : blocks - 1) * slabs) * 64 + 4 * b;
+    };
+    const uint32_t qo[2] = {16u * (l ^ ((2 * w) & 3)), 16u * (l ^ ((2 * w + 1) & 3))};
+    int ck = 0;
+    auto copy_slab = [&](int place) {                // 4 copies
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int to = L.dst[64 * wp + 32 * i + 8 * (v >> 2) + 4 * h + (v & 3)];
-                if (to < 0 || q >= A.N) continue;
-                const f32x4 y = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
-                const size_t at = (size_t)to * A.N + q;
+        for (int i = 0; i < 2; ++i) {
+            lds_dma16(scalar_base(A.a.base + (size_t)ck * 64) + here(po[i]), &L.p[0][0] + place + (32 * w + 16 * i) * 64);
+            lds_dma16(scalar_base(qb[i] + (size_t)ck * 1024) + here(qo[i]), &L.q[0][0] + place + (2 * w + i) * 1024);
+        }
+        ++ck;
+    };
+    auto copy_scales = [&](int u) {                  // 2 copies
+        lds_dma4(scalar_base((const char *)X.xs + (size_t)ck * 4) + here(xo), &L.xs[u][32 * w][0]);
+        lds_dma4(scalar_base(sb + (size_t)ck * 64) + here(so), L.qs[u][w]);
+    };
+
+    // this lane's places in LDS: x's two pieces of a slab, W's of tile j, and the scales
+    const int key = (b >> 2) & 3;
+    const char *P[2], *Q[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) P[i] = L.p[0] + (64 * wp + b) * 64 + 16 * ((2 * i + h) ^ key);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        Q[j] = L.q[0] + (8 * wq + (b >> 2)) * 1024 + 16 * (16 * h + 4 * (b & 3) + (j ^ key));
+    const char *const S = L.qs[0][4 * wq + (b >> 3)] + 128 * ((b >> 2) & 1) + 16 * h + 4 * (b & 3);
+    const char *const XS = (const char *)L.xs[0][64 * wp + b];
+
+    f32x16 acc[2][4];
+    u32x4 pf[2][2], qf[2][4];
+    uint32_t ps[2][2], qs[2][2];
+    enter(cur);
+    copy_scales(0), copy_slab(0), copy_slab(kBPair / 2);
+    copy_scales(1), copy_slab(kBPair);
+    wait_copies<10>();
+    bare_barrier();
+    if (wp >= 2) bare_barrier();
+
+    int u = 0, db = 0, stores = 0;       // pair in LDS, tile's place in `to`, stores before this tile
+    bool copying = true;
+    for (;;) {
+        const bool work0 = wp < cur.units, work1 = 4 + wp < cur.units;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+        auto read = [&](int o) {
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) qf[kk][j] = *(const MOE_LDS u32x4 *)(Q[j] + o + 512 * kk);
+                pf[0][kk] = *(const MOE_LDS u32x4 *)(P[kk] + o);
+                if (work1) pf[1][kk] = *(const MOE_LDS u32x4 *)(P[kk] + o + 2048);
+            }
+        };
+        auto multiply = [&](auto slab) {
+            constexpr int s = decltype(slab)::v;
+            wait_lds();
+            phase_barrier();
+            __builtin_amdgcn_s_setprio(1);
+#define MOE_MX(i, kk, j) acc[i][j] = mfma32<2 * kk, j>(pf[i][kk], qf[kk][j], acc[i][j], ps[s][i], qs[s][kk]);
+#define MOE_MX4(i, kk) MOE_MX(i, kk, 0) MOE_MX(i, kk, 1) MOE_MX(i, kk, 2) MOE_MX(i, kk, 3)
+            if (work0) {
+                MOE_MX4(0, 0)
+                MOE_MX4(0, 1)
+                if (work1) {
+                    MOE_MX4(1, 0)
+                    MOE_MX4(1, 1)
+                }
+            }
+#undef MOE_MX4
+#undef MOE_MX
+            __builtin_amdgcn_s_setprio(0);
+            phase_barrier();
+        };
+        for (int k = 0; k < slabs; k += 2) {
+            // the pair's first slab, and its scales
+            if (work0) {
                 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
-                if (f32) *(MOE_GLOBAL f32x4 *)((float *)out + at) = y;
-                else *(MOE_GLOBAL u32x2 *)((uint16_t *)out + at) =
-                         u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+                read(u * kBPair);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk)
+                        qs[s][kk] = *(const MOE_LDS uint32_t *)(S + u * (int)sizeof(L.qs[0]) + 64 * s + 32 * kk);
+                const u32x2 x0 = *(const MOE_LDS u32x2 *)(XS + u * (int)sizeof(L.xs[0]));
+                const u32x2 x1 = *(const MOE_LDS u32x2 *)(XS + u * (int)sizeof(L.xs[0]) + 256);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) ps[s][0] = x0[s] >> (8 * h), ps[s][1] = x1[s] >> (8 * h);
+            }
+            if (k == 0 && more) {
+                // the next tile, and the indices of its rows
+                next = locate(si + per, expert_from(cur.e, si + per));
+                const int i = index_at(next, 64 * (w & 3) + l);
+                if (w < 4 ? A.a.idx != nullptr : A.out_rows != nullptr)
+                    lds_dma4((w < 4 ? A.a.idx : A.out_rows) + i, (w < 4 ? L.raw : L.rawo) + 64 * (w & 3));
+            }
+            // Slab k + 3, into the place that slab k - 1, read by all, had. Then slab k + 1
+            // has to be there: of what is in flight, the copies of slab k + 3 (4), of slab
+            // k + 2 with its scales (6) and the last tile's stores are younger.
+            const int behind = k == 0 ? stores : 0;
+            if (copying) {
+                copy_slab((u ^ 1) * kBPair + kBPair / 2);
+                wait_some<10>(behind);
+            } else {
+                wait_copies<0>();
+            }
+            multiply(Const<0>{});
+
+            // its second slab
+            if (work0) read(u * kBPair + kBPair / 2);
+            if (k == 2 && more) {
+                const int t = 32 * w + b;
+                L.to[db ^ 1][t] = out_at(next, t, L.raw[t], L.rawo[t]);
+            }
+            if (ck == slabs) {
+                copying = more;
+                if (more) ck = 0, enter(next);
+            }
+            if (copying) {
+                copy_scales(u), copy_slab(u * kBPair);
+                wait_some<10>(behind);
+            } else {
+                wait_copies<0>();
+            }
+            multiply(Const<1>{});
+            u ^= 1;
+        }
+        // A lane stores four columns of 16 rows of each unit.
+        const int q = cur.q0 + 128 * wq + 4 * b, bytes = A.out_f32 ? 4 : 2;
+        const uint32_t col = q < A.N ? (uint32_t)(q * bytes) : kBBytes;
+        const buf_rsrc out = make_rsrc(A.out, (uint32_t)A.out_n * ldo);
+        stores = (work0 ? 16 : 0) + (work1 ? 16 : 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (4 * i + wp >= cur.units) continue;
+            typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[i][j]));
+            u32x4 at[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) at[c] = *(const MOE_LDS u32x4 *)&L.to[db][64 * wp + 32 * i + 8 * c + 4 * h];
+            if (A.out_f32) {
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const f32x4 y = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), out, at[v >> 2][v & 3] + col, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    __builtin_amdgcn_raw_buffer_store_b64(
+                        u32x2{pack_bf16x2(acc[i][0][v], acc[i][1][v]), pack_bf16x2(acc[i][2][v], acc[i][3][v])}, out,
+                        at[v >> 2][v & 3] + col, 0, 0);
             }
         }
+        if (!more) break;
+        db ^= 1, si += per, cur = next;
+        more = si + per < t1;
     }
+    if (wp < 2) bare_barrier();
 }
 
 // -------------------------------------------------------- a handful of rows --
@@ -364,6 +665,15 @@ __global__ __launch_bounds__(kVThreads, 4) void mxfp4_stream_kernel(MxArgs X) {
 // Whether the streaming kernel runs, from the sizes alone.
 static bool mxfp4_streams(int R, int E) { return R <= (long)kVAvg * E; }
 
+// Whether tiles of 256 x 256 run rather than 128 x 256.
+static bool mxfp4_large(const ProductArgs &a) {
+    const size_t out = (size_t)a.out_n * a.N * (a.out_f32 ? 4 : 2);
+    if (a.K % 256 || a.K < 128 * kBSlabs || (size_t)a.a.n * (a.K / 2) > 0xFFFFFFFFull || out > kBBytes) return false;
+    if ((long)a.N * (a.K / 32) > 0x7FFFFFFFL) return false;
+    const long tiles = ((long)a.R / kBT + (a.R < a.E ? a.R : a.E)) * ((a.N + kBT - 1) / kBT);
+    return 2 * tiles > compute_units() && a.R >= 128L * a.E;
+}
+
 // Parts that the sum of a tile is cut into: where there are fewer tiles than compute
 // units, as many as give each one, of four slabs at least.
 static int mxfp4_slices(int R, int N, int K, int E) {
@@ -417,6 +727,12 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t *x_e2m1, const uint8_t *x_e8
     a.slices = mxfp4_slices(R, N, K, E);
     a.part = (float *)ws;
     if (!ws || ws_bytes < mxfp4_part_bytes(R, N, K, E)) a.slices = 1;
+    if (mxfp4_large(a)) {
+        const long tiles = ((long)R / kBT + (R < E ? R : E)) * ((N + kBT - 1) / kBT);
+        MOE_LAUNCH(K_PROD_MXFP4, mxfp4_large_kernel, dim3((unsigned)(tiles < cu ? tiles : cu)), dim3(kBThreads), 0, s,
+                   m);
+        return check_launch();
+    }
     const long tiles = ((long)R / kXP + (R < E ? R : E)) * ((N + kXQ - 1) / kXQ) * a.slices;
     MOE_LAUNCH(K_PROD_MXFP4, mxfp4_tile_kernel, dim3((unsigned)(tiles < 2L * cu ? tiles : 2L * cu)),
                dim3(kXThreads), 0, s, m);

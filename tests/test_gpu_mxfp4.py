@@ -200,6 +200,12 @@ SHAPES = [
     ([100, 0, 31], 48, 2176),
     ([150, 61, 0, 97] * 14, 768, 768),
     ([1300, 513, 1, 900, 1255], 2064, 1152),
+    # large tiles, several a workgroup; K of an odd number of slabs
+    ([300, 259, 0, 1, 700, 257] * 8, 2064, 768),
+    ([130] * 50 + [0] * 3 + [700], 3856, 1024),
+    ([2000, 2049, 31], 4112, 1280),
+    ([513] * 16, 2048, 1792),
+    ([300] * 24, 1040, 1664),
 ]
 
 
