@@ -334,9 +334,10 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
     __syncthreads();
 
     // Copies: a wavefront takes 32 rows of x, 16 an instruction, and two blocks of W.
-    // The lane's offsets into x, its scales and W's, and the wavefront's blocks, by tile.
+    // The lane's offsets into x, its scales and W's, and where the next slab's are.
     uint32_t po[2], xo, so;
-    const char *qb[2], *sb;
+    const char *pn, *qn[2], *xn, *sn;
+    int ck = 0;                                      // that slab
     auto enter = [&](const Tile &t) {
         auto row_at = [&](int row) {
             const int r = A.a.idx ? row_of_index(A.a, L.raw[row]) : index_at(t, row);
@@ -344,28 +345,29 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
         };
         const int rb = t.q0 / 16 + 2 * w;
         const char *const codes = codes_of(X, t.e);
-        sb = scales_of(X, t.e);
+        pn = A.a.base, xn = (const char *)X.xs, sn = scales_of(X, t.e);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             po[i] = row_at(32 * w + 16 * i + (l >> 2)) * (uint32_t)(A.K / 2) + 16 * ((l & 3) ^ ((l >> 4) & 3));
-            qb[i] = codes + (size_t)(rb + i < blocks ? rb + i : blocks - 1) * slabs * 1024;
+            qn[i] = codes + (size_t)(rb + i < blocks ? rb + i : blocks - 1) * slabs * 1024;
         }
         xo = row_at(32 * w + (l >> 1)) * (uint32_t)(A.K / 32) + 4 * (l & 1);
         so = (uint32_t)((rb + h < blocks ? rb + h : blocks - 1) * slabs) * 64 + 4 * b;
+        ck = 0;
     };
     const uint32_t qo[2] = {16u * (l ^ ((2 * w) & 3)), 16u * (l ^ ((2 * w + 1) & 3))};
-    int ck = 0;
+    char *const pl = L.p[0] + 32 * w * 64, *const ql = L.q[0] + 2 * w * 1024;
     auto copy_slab = [&](int place) {                // 4 copies
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            lds_dma16(scalar_base(A.a.base + (size_t)ck * 64) + here(po[i]), &L.p[0][0] + place + (32 * w + 16 * i) * 64);
-            lds_dma16(scalar_base(qb[i] + (size_t)ck * 1024) + here(qo[i]), &L.q[0][0] + place + (2 * w + i) * 1024);
-        }
-        ++ck;
+        lds_dma16(scalar_base(pn) + here(po[0]), pl + place);
+        lds_dma16(scalar_base(pn) + here(po[1]), pl + place + 1024);
+        lds_dma16(scalar_base(qn[0]) + here(qo[0]), ql + place);
+        lds_dma16(scalar_base(qn[1]) + here(qo[1]), ql + place + 1024);
+        pn += 64, qn[0] += 1024, qn[1] += 1024, ++ck;
     };
     auto copy_scales = [&](int u) {                  // 2 copies
-        lds_dma4(scalar_base((const char *)X.xs + (size_t)ck * 4) + here(xo), &L.xs[u][32 * w][0]);
-        lds_dma4(scalar_base(sb + (size_t)ck * 64) + here(so), L.qs[u][w]);
+        lds_dma4(scalar_base(xn) + here(xo), &L.xs[u][32 * w][0]);
+        lds_dma4(scalar_base(sn) + here(so), L.qs[u][w]);
+        xn += 8, sn += 128;
     };
 
     // this lane's places in LDS: x's two pieces of a slab, W's of tile j, and the scales
@@ -379,9 +381,13 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
     const char *const S = L.qs[0][4 * wq + (b >> 3)] + 128 * ((b >> 2) & 1) + 16 * h + 4 * (b & 3);
     const char *const XS = (const char *)L.xs[0][64 * wp + b];
 
+    struct Frags {
+        u32x4 p[2][2], q[2][4];
+    };
+    struct Scales {
+        uint32_t p[2][2], q[2][2];       // by slab of the pair
+    };
     f32x16 acc[2][4];
-    u32x4 pf[2][2], qf[2][4];
-    uint32_t ps[2][2], qs[2][2];
     enter(cur);
     copy_scales(0), copy_slab(0), copy_slab(kBPair / 2);
     copy_scales(1), copy_slab(kBPair);
@@ -390,97 +396,90 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
     if (wp >= 2) bare_barrier();
 
     int u = 0, db = 0, stores = 0;       // pair in LDS, tile's place in `to`, stores before this tile
-    bool copying = true;
+    bool work0, work1;
+    auto read = [&](Frags &f, int o) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f.q[kk][j] = *(const MOE_LDS u32x4 *)(Q[j] + o + 512 * kk);
+            f.p[0][kk] = *(const MOE_LDS u32x4 *)(P[kk] + o);
+            f.p[1][kk] = *(const MOE_LDS u32x4 *)(P[kk] + o + 2048);
+        }
+    };
+    auto multiply = [&](const Frags &f, const Scales &c, auto slab) {
+        constexpr int s = decltype(slab)::v;
+        wait_lds();
+        phase_barrier();
+        __builtin_amdgcn_s_setprio(1);
+#define MOE_MX(i, kk, j) acc[i][j] = mfma32<2 * kk, j>(f.p[i][kk], f.q[kk][j], acc[i][j], c.p[s][i], c.q[s][kk]);
+#define MOE_MX4(i, kk) MOE_MX(i, kk, 0) MOE_MX(i, kk, 1) MOE_MX(i, kk, 2) MOE_MX(i, kk, 3)
+        if (work0) {
+            MOE_MX4(0, 0)
+            MOE_MX4(0, 1)
+        }
+        if (work1) {
+            MOE_MX4(1, 0)
+            MOE_MX4(1, 1)
+        }
+#undef MOE_MX4
+#undef MOE_MX
+        __builtin_amdgcn_s_setprio(0);
+        phase_barrier();
+    };
+    auto pair = [&](int k) {
+        typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+        // the pair's first slab, and its scales
+        Frags f0, f1;
+        Scales c;
+        read(f0, u * kBPair);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+                c.q[s][kk] = *(const MOE_LDS uint32_t *)(S + u * (int)sizeof(L.qs[0]) + 64 * s + 32 * kk);
+        const u32x2 x0 = *(const MOE_LDS u32x2 *)(XS + u * (int)sizeof(L.xs[0]));
+        const u32x2 x1 = *(const MOE_LDS u32x2 *)(XS + u * (int)sizeof(L.xs[0]) + 256);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) c.p[s][0] = x0[s] >> (8 * h), c.p[s][1] = x1[s] >> (8 * h);
+        if (k == 0 && more) {
+            // the next tile, and the indices of its rows
+            next = locate(si + per, expert_from(cur.e, si + per));
+            const int i = index_at(next, 64 * (w & 3) + l);
+            if (w < 4 ? A.a.idx != nullptr : A.out_rows != nullptr)
+                lds_dma4((w < 4 ? A.a.idx : A.out_rows) + i, (w < 4 ? L.raw : L.rawo) + 64 * (w & 3));
+        }
+        // Slab k + 3, into the place that slab k - 1, read by all, had. Then slab k + 1 has
+        // to be there: of what is in flight, the copies of slab k + 3 (4), of slab k + 2
+        // with its scales (6) and the last tile's stores are younger.
+        copy_slab((u ^ 1) * kBPair + kBPair / 2);
+        wait_some<10>(k == 0 ? stores : 0);
+        multiply(f0, c, Const<0>{});
+
+        // its second slab
+        read(f1, u * kBPair + kBPair / 2);
+        if (k == 2 && more) {
+            const int t = 32 * w + b;
+            L.to[db ^ 1][t] = out_at(next, t, L.raw[t], L.rawo[t]);
+        }
+        if (ck == slabs) {
+            // on to the next tile; behind the last one, its last pair once more
+            if (more) enter(next);
+            else pn -= 128, qn[0] -= 2048, qn[1] -= 2048, xn -= 8, sn -= 128, ck -= 2;
+        }
+        copy_scales(u), copy_slab(u * kBPair);
+        wait_some<10>(k == 0 ? stores : 0);
+        multiply(f1, c, Const<1>{});
+        u ^= 1;
+    };
     for (;;) {
-        const bool work0 = wp < cur.units, work1 = 4 + wp < cur.units;
+        work0 = wp < cur.units, work1 = 4 + wp < cur.units;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-        auto read = [&](int o) {
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) qf[kk][j] = *(const MOE_LDS u32x4 *)(Q[j] + o + 512 * kk);
-                pf[0][kk] = *(const MOE_LDS u32x4 *)(P[kk] + o);
-                if (work1) pf[1][kk] = *(const MOE_LDS u32x4 *)(P[kk] + o + 2048);
-            }
-        };
-        auto multiply = [&](auto slab) {
-            constexpr int s = decltype(slab)::v;
-            wait_lds();
-            phase_barrier();
-            __builtin_amdgcn_s_setprio(1);
-#define MOE_MX(i, kk, j) acc[i][j] = mfma32<2 * kk, j>(pf[i][kk], qf[kk][j], acc[i][j], ps[s][i], qs[s][kk]);
-#define MOE_MX4(i, kk) MOE_MX(i, kk, 0) MOE_MX(i, kk, 1) MOE_MX(i, kk, 2) MOE_MX(i, kk, 3)
-            if (work0) {
-                MOE_MX4(0, 0)
-                MOE_MX4(0, 1)
-                if (work1) {
-                    MOE_MX4(1, 0)
-                    MOE_MX4(1, 1)
-                }
-            }
-#undef MOE_MX4
-#undef MOE_MX
-            __builtin_amdgcn_s_setprio(0);
-            phase_barrier();
-        };
-        for (int k = 0; k < slabs; k += 2) {
-            // the pair's first slab, and its scales
-            if (work0) {
-                typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
-                read(u * kBPair);
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk)
-                        qs[s][kk] = *(const MOE_LDS uint32_t *)(S + u * (int)sizeof(L.qs[0]) + 64 * s + 32 * kk);
-                const u32x2 x0 = *(const MOE_LDS u32x2 *)(XS + u * (int)sizeof(L.xs[0]));
-                const u32x2 x1 = *(const MOE_LDS u32x2 *)(XS + u * (int)sizeof(L.xs[0]) + 256);
-#pragma unroll
-                for (int s = 0; s < 2; ++s) ps[s][0] = x0[s] >> (8 * h), ps[s][1] = x1[s] >> (8 * h);
-            }
-            if (k == 0 && more) {
-                // the next tile, and the indices of its rows
-                next = locate(si + per, expert_from(cur.e, si + per));
-                const int i = index_at(next, 64 * (w & 3) + l);
-                if (w < 4 ? A.a.idx != nullptr : A.out_rows != nullptr)
-                    lds_dma4((w < 4 ? A.a.idx : A.out_rows) + i, (w < 4 ? L.raw : L.rawo) + 64 * (w & 3));
-            }
-            // Slab k + 3, into the place that slab k - 1, read by all, had. Then slab k + 1
-            // has to be there: of what is in flight, the copies of slab k + 3 (4), of slab
-            // k + 2 with its scales (6) and the last tile's stores are younger.
-            const int behind = k == 0 ? stores : 0;
-            if (copying) {
-                copy_slab((u ^ 1) * kBPair + kBPair / 2);
-                wait_some<10>(behind);
-            } else {
-                wait_copies<0>();
-            }
-            multiply(Const<0>{});
-
-            // its second slab
-            if (work0) read(u * kBPair + kBPair / 2);
-            if (k == 2 && more) {
-                const int t = 32 * w + b;
-                L.to[db ^ 1][t] = out_at(next, t, L.raw[t], L.rawo[t]);
-            }
-            if (ck == slabs) {
-                copying = more;
-                if (more) ck = 0, enter(next);
-            }
-            if (copying) {
-                copy_scales(u), copy_slab(u * kBPair);
-                wait_some<10>(behind);
-            } else {
-                wait_copies<0>();
-            }
-            multiply(Const<1>{});
-            u ^= 1;
-        }
+        for (int k = 0; k < slabs; k += 2) pair(k);
         // A lane stores four columns of 16 rows of each unit.
         const int q = cur.q0 + 128 * wq + 4 * b, bytes = A.out_f32 ? 4 : 2;
         const uint32_t col = q < A.N ? (uint32_t)(q * bytes) : kBBytes;
@@ -513,6 +512,7 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
         db ^= 1, si += per, cur = next;
         more = si + per < t1;
     }
+    wait_copies<0>();       // (copies that nothing reads: LDS is another workgroup's next)
     if (wp < 2) bare_barrier();
 }
 
