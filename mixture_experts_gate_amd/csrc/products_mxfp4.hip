@@ -230,7 +230,8 @@ __global__ __launch_bounds__(kXThreads, 2) void mxfp4_tile_kernel(MxArgs X) {
 // 256 x 256 a workgroup of eight wavefronts, 64 x 128 each as above, one workgroup a
 // compute unit: two thirds of the bytes that tiles of 128 x 256 copy into LDS. The
 // wavefronts of a SIMD (w and w + 4) run one phase apart: one reads a slab's fragments
-// and issues copies while the other multiplies; a barrier ends each phase.
+// while the other multiplies, its copies between the matrix instructions; a barrier
+// ends each phase.
 //
 // LDS holds four slabs, two pairs. The copies run three slabs ahead, and on into the
 // next tile, whose rows are looked up during this one's first slabs: only a workgroup's
@@ -279,6 +280,14 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
     const int t0 = (int)((long)total * xcd / nx), t1 = (int)((long)total * (xcd + 1) / nx);
     int si = t0 + (int)blockIdx.x / nx;
     if (si >= t1) return;
+
+    // The workgroups that have a tile less than others start later, by up to the time
+    // of one (about 1000 cycles a slab): begun together, all tiles end together, and
+    // each end's stores, 32 MB from the device, wait for HBM with nothing to multiply
+    // (gate/up of 8192 tokens: 185 -> 171 us).
+    const int rank = blockIdx.x / nx, late = (t1 - t0) % per;
+    if (late > 0 && rank >= late)
+        for (int i = (int)((long)slabs * 12 * (rank - late) / (per - late)); i > 0; --i) __builtin_amdgcn_s_sleep(1);
 
     struct Tile {
         int e, lo, cnt, p0, q0, units;
@@ -357,12 +366,18 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
     };
     const uint32_t qo[2] = {16u * (l ^ ((2 * w) & 3)), 16u * (l ^ ((2 * w + 1) & 3))};
     char *const pl = L.p[0] + 32 * w * 64, *const ql = L.q[0] + 2 * w * 1024;
-    auto copy_slab = [&](int place) {                // 4 copies
-        lds_dma16(scalar_base(pn) + here(po[0]), pl + place);
-        lds_dma16(scalar_base(pn) + here(po[1]), pl + place + 1024);
-        lds_dma16(scalar_base(qn[0]) + here(qo[0]), ql + place);
-        lds_dma16(scalar_base(qn[1]) + here(qo[1]), ql + place + 1024);
-        pn += 64, qn[0] += 1024, qn[1] += 1024, ++ck;
+    auto copy_some = [&](int place, auto n) {        // copy n of 4 of that slab
+        constexpr int i = decltype(n)::v;
+        if constexpr (i == 0) lds_dma16(scalar_base(pn) + here(po[0]), pl + place);
+        if constexpr (i == 1) lds_dma16(scalar_base(pn) + here(po[1]), pl + place + 1024);
+        if constexpr (i == 2) lds_dma16(scalar_base(qn[0]) + here(qo[0]), ql + place);
+        if constexpr (i == 3) {
+            lds_dma16(scalar_base(qn[1]) + here(qo[1]), ql + place + 1024);
+            pn += 64, qn[0] += 1024, qn[1] += 1024, ++ck;
+        }
+    };
+    auto copy_slab = [&](int place) {
+        copy_some(place, Const<0>{}), copy_some(place, Const<1>{}), copy_some(place, Const<2>{}), copy_some(place, Const<3>{});
     };
     auto copy_scales = [&](int u) {                  // 2 copies
         lds_dma4(scalar_base(xn) + here(xo), &L.xs[u][32 * w][0]);
@@ -406,22 +421,34 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
             f.p[1][kk] = *(const MOE_LDS u32x4 *)(P[kk] + o + 2048);
         }
     };
-    auto multiply = [&](const Frags &f, const Scales &c, auto slab) {
+    auto multiply = [&](const Frags &f, const Scales &c, auto slab, auto copy) {
         constexpr int s = decltype(slab)::v;
+        auto between = [&](auto n) {
+            __builtin_amdgcn_sched_barrier(0);
+            copy(n);
+            __builtin_amdgcn_sched_barrier(0);
+        };
         wait_lds();
         phase_barrier();
         __builtin_amdgcn_s_setprio(1);
 #define MOE_MX(i, kk, j) acc[i][j] = mfma32<2 * kk, j>(f.p[i][kk], f.q[kk][j], acc[i][j], c.p[s][i], c.q[s][kk]);
-#define MOE_MX4(i, kk) MOE_MX(i, kk, 0) MOE_MX(i, kk, 1) MOE_MX(i, kk, 2) MOE_MX(i, kk, 3)
+#define MOE_MX2(i, kk, j) MOE_MX(i, kk, j) MOE_MX(i, kk, j + 1)
         if (work0) {
-            MOE_MX4(0, 0)
-            MOE_MX4(0, 1)
+            MOE_MX2(0, 0, 0)
+            between(Const<0>{});
+            MOE_MX2(0, 0, 2)
+            between(Const<1>{});
+            MOE_MX2(0, 1, 0)
+            between(Const<2>{});
+            MOE_MX2(0, 1, 2)
+            between(Const<3>{});
+        } else {
+            copy(Const<0>{}), copy(Const<1>{}), copy(Const<2>{}), copy(Const<3>{});
         }
         if (work1) {
-            MOE_MX4(1, 0)
-            MOE_MX4(1, 1)
+            MOE_MX2(1, 0, 0) MOE_MX2(1, 0, 2) MOE_MX2(1, 1, 0) MOE_MX2(1, 1, 2)
         }
-#undef MOE_MX4
+#undef MOE_MX2
 #undef MOE_MX
         __builtin_amdgcn_s_setprio(0);
         phase_barrier();
@@ -448,12 +475,12 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
             if (w < 4 ? A.a.idx != nullptr : A.out_rows != nullptr)
                 lds_dma4((w < 4 ? A.a.idx : A.out_rows) + i, (w < 4 ? L.raw : L.rawo) + 64 * (w & 3));
         }
-        // Slab k + 3, into the place that slab k - 1, read by all, had. Then slab k + 1 has
-        // to be there: of what is in flight, the copies of slab k + 3 (4), of slab k + 2
-        // with its scales (6) and the last tile's stores are younger.
-        copy_slab((u ^ 1) * kBPair + kBPair / 2);
-        wait_some<10>(k == 0 ? stores : 0);
-        multiply(f0, c, Const<0>{});
+        // Slab k + 1 has to be there: of what is in flight, the copies of slab k + 2 with
+        // its scales (6) and the last tile's stores are younger. Slab k + 3 goes into the
+        // place that slab k - 1, read by all, had.
+        wait_some<6>(k == 0 ? stores : 0);
+        const int p3 = (u ^ 1) * kBPair + kBPair / 2, p4 = u * kBPair;
+        multiply(f0, c, Const<0>{}, [&](auto n) { copy_some(p3, n); });
 
         // its second slab
         read(f1, u * kBPair + kBPair / 2);
@@ -466,9 +493,11 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
             if (more) enter(next);
             else pn -= 128, qn[0] -= 2048, qn[1] -= 2048, xn -= 8, sn -= 128, ck -= 2;
         }
-        copy_scales(u), copy_slab(u * kBPair);
-        wait_some<10>(k == 0 ? stores : 0);
-        multiply(f1, c, Const<1>{});
+        wait_some<4>(k == 0 ? stores : 0);
+        multiply(f1, c, Const<1>{}, [&](auto n) {
+            if constexpr (decltype(n)::v == 0) copy_scales(u);
+            copy_some(p4, n);
+        });
         u ^= 1;
     };
     for (;;) {
@@ -498,14 +527,14 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
                     const f32x4 y = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), out, at[v >> 2][v & 3] + col, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), out, at[v >> 2][v & 3] + col, 0, kBufNt);
                 }
             } else {
 #pragma unroll
                 for (int v = 0; v < 16; ++v)
                     __builtin_amdgcn_raw_buffer_store_b64(
                         u32x2{pack_bf16x2(acc[i][0][v], acc[i][1][v]), pack_bf16x2(acc[i][2][v], acc[i][3][v])}, out,
-                        at[v >> 2][v & 3] + col, 0, 0);
+                        at[v >> 2][v & 3] + col, 0, kBufNt);
             }
         }
         if (!more) break;
