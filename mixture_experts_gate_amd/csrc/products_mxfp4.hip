@@ -691,23 +691,37 @@ __global__ __launch_bounds__(kVThreads, 4) void mxfp4_stream_kernel(MxArgs X) {
     }
 }
 
-// Whether the streaming kernel runs, from the sizes alone.
-static bool mxfp4_streams(int R, int E) { return R <= (long)kVAvg * E; }
+static long tiles_of(int R, int N, int E, int p, int q) {
+    return ((long)R / p + (R < E ? R : E)) * ((N + q - 1) / q);
+}
 
-// Whether tiles of 256 x 256 run rather than 128 x 256.
+// Which kernel, from the sizes alone. us of a call with uneven routing (popularity
+// e^(N(0,1)/4.5 to 2)), streaming / 128 x 256 / 256 x 256 tiles:
+//   128 experts of 1536 x 2048, 8 a token: 1, 2, 4, 16, 64, 256, 1024, 4096 tokens
+//     7.3/11.1/14.2  10.0/13.5/15.3  14.9/14.4/15.8  33.5/27.8/30.5  52/46.3/47.5
+//     90/48.4/48.5  -/63/57  -/107/106
+//   256 experts of 4096 x 4096, 6 a token: 1, 2, 8, 32, 256 tokens
+//     15.9/17.7/21.9  25/21.9/23.6  80/80/78  235/211/192  592/338/331
+//   one of 4096 x 4096: 1, 16, 64, 512, 4001 rows
+//     8.8/11.6/20.4  10.1/12.8/20.5  -/16.6/21.2  -/28.5/29.9  -/51/43
+// The streaming kernel, which needs no second launch for a sum in parts, wins with few
+// tiles; large ones win where rows fill them or the tiles are many.
+static bool mxfp4_streams(int R, int N, int E) {
+    return R <= (long)kVAvg * E && tiles_of(R, N, E, kBT, kBT) <= 128;
+}
 static bool mxfp4_large(const ProductArgs &a) {
     const size_t out = (size_t)a.out_n * a.N * (a.out_f32 ? 4 : 2);
     if (a.K % 256 || a.K < 128 * kBSlabs || (size_t)a.a.n * (a.K / 2) > 0xFFFFFFFFull || out > kBBytes) return false;
     if ((long)a.N * (a.K / 32) > 0x7FFFFFFFL) return false;
-    const long tiles = ((long)a.R / kBT + (a.R < a.E ? a.R : a.E)) * ((a.N + kBT - 1) / kBT);
-    return 2 * tiles > compute_units() && a.R >= 128L * a.E;
+    const long tiles = tiles_of(a.R, a.N, a.E, kBT, kBT);
+    return tiles >= compute_units() && (a.R >= 32L * a.E || tiles >= 4L * compute_units());
 }
 
 // Parts that the sum of a tile is cut into: where there are fewer tiles than compute
 // units, as many as give each one, of four slabs at least.
 static int mxfp4_slices(int R, int N, int K, int E) {
-    if (R == 0 || mxfp4_streams(R, E)) return 1;
-    const long tiles = ((long)R / kXP + (R < E ? R : E)) * ((N + kXQ - 1) / kXQ);
+    if (R == 0 || mxfp4_streams(R, N, E)) return 1;
+    const long tiles = tiles_of(R, N, E, kXP, kXQ);
     long n = compute_units() / (tiles < 1 ? 1 : tiles);
     const long steps = K / 128;
     n = n < steps / 4 ? n : steps / 4;
@@ -747,7 +761,7 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t *x_e2m1, const uint8_t *x_e8
     m.xs = x_e8m0, m.ws = w_e8m0;
     hipStream_t s = (hipStream_t)stream;
     const int cu = compute_units();
-    if (mxfp4_streams(R, E)) {
+    if (mxfp4_streams(R, N, E)) {
         const long tiles = (long)(R < E ? R : E + R / kVRows) * (N / 16), groups = (tiles + kVWaves - 1) / kVWaves;
         MOE_LAUNCH(K_PROD_MXFP4, mxfp4_stream_kernel, dim3((unsigned)(groups < 4L * cu ? groups : 4L * cu)),
                    dim3(kVThreads), 0, s, m);
@@ -757,12 +771,12 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t *x_e2m1, const uint8_t *x_e8
     a.part = (float *)ws;
     if (!ws || ws_bytes < mxfp4_part_bytes(R, N, K, E)) a.slices = 1;
     if (mxfp4_large(a)) {
-        const long tiles = ((long)R / kBT + (R < E ? R : E)) * ((N + kBT - 1) / kBT);
+        const long tiles = tiles_of(R, N, E, kBT, kBT);
         MOE_LAUNCH(K_PROD_MXFP4, mxfp4_large_kernel, dim3((unsigned)(tiles < cu ? tiles : cu)), dim3(kBThreads), 0, s,
                    m);
         return check_launch();
     }
-    const long tiles = ((long)R / kXP + (R < E ? R : E)) * ((N + kXQ - 1) / kXQ) * a.slices;
+    const long tiles = tiles_of(R, N, E, kXP, kXQ) * a.slices;
     MOE_LAUNCH(K_PROD_MXFP4, mxfp4_tile_kernel, dim3((unsigned)(tiles < 2L * cu ? tiles : 2L * cu)),
                dim3(kXThreads), 0, s, m);
     if (a.slices > 1) launch_join(a, N, s);

@@ -27,51 +27,57 @@ _U8 = (torch.uint8,)
 _OUT = (torch.bfloat16, torch.float32)
 
 
-def _vector(t, name, n, dev):
-    if _need(t, name, _BF16, dev).shape != (n,):
-        _fail(f"{name}: {tuple(t.shape)}, [{n}] is needed")
-    return t.data_ptr()
-
-
-def _like(t, name, shape, dtypes, dev):
-    """Address of t, which may be None."""
-    if t is None:
-        return None
-    if _need(t, name, dtypes, dev).shape != shape:
-        _fail(f"{name}: {tuple(t.shape)}, {list(shape)} is needed")
-    return t.data_ptr()
+def _at(t, name, dtypes, shape, dev):
+    """Address of t: contiguous, one of `dtypes`, of this shape, on GPU `dev`. (A small
+    call's time is its checks: one line where all is well.)"""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, name, dtypes, dev)
+    _fail(f"{name}: {tuple(t.shape)}, {list(shape)} is needed")
 
 
 def _given(t, name, shape, dtypes, dev, stream):
-    t = _output(t, name, shape, dtypes, dev, stream)
-    if t.shape != shape:
-        _fail(f"{name}: {tuple(t.shape)}, {list(shape)} is needed")
-    return t
+    """(t, its address); a new tensor where t is None."""
+    if t is None:
+        t = _output(None, name, shape, dtypes, dev, stream)
+        return t, t.data_ptr()
+    return t, _at(t, name, dtypes, shape, dev)
 
 
 def _norm(x, weight, eps, residual, out, total, quant, q, s, stream):
+    """The norm's call: (y, q, s, total), what is asked for of them."""
     dev = _matrix(x, "x", _BF16).get_device()
     _no_history(x, weight, residual)
-    R, H = x.shape
-    pw, pr = _vector(weight, "weight", H, dev), _like(residual, "residual", x.shape, _BF16, dev)
+    shape = x.shape
+    R, H = shape
+    pw = _at(weight, "weight", _BF16, (H,), dev)
+    pr = pt = py = pq = ps = None
     if residual is not None:
-        total = _given(total, "total", x.shape, _BF16, dev, stream)
+        pr = _at(residual, "residual", _BF16, shape, dev)
+        total, pt = _given(total, "total", shape, _BF16, dev, stream)
     elif total is not None:
         _fail("total: given without a residual")
-    _run("moe_rms_norm", dev, stream, x.data_ptr(), pr, pw, eps, R, H,
-         None if total is None else total.data_ptr(), _like(out, "out", x.shape, _BF16, dev), quant,
-         None if q is None else q.data_ptr(), None if s is None else s.data_ptr())
-    return total
+    if out is not None or quant == _lib.MOE_QUANT_NONE:
+        out, py = _given(out, "out", shape, _BF16, dev, stream)
+    if quant == _lib.MOE_QUANT_FP8:
+        q, pq = _given(q, "q", shape, _FP8, dev, stream)
+        s, ps = _given(s, "s", (R, -(-H // 128)), _F32, dev, stream)
+    elif quant == _lib.MOE_QUANT_MXFP4:
+        if H % 32:
+            _fail(f"x: {H} columns, a multiple of 32 is needed")
+        q, pq = _given(q, "q", (R, H // 2), _U8, dev, stream)
+        s, ps = _given(s, "s", (R, H // 32), P._E8M0, dev, stream)
+    _run("moe_rms_norm", dev, stream, x.data_ptr(), pr, pw, eps, R, H, pt, py, quant, pq, ps)
+    return out, q, s, total
 
 
 def rms_norm(x, weight, eps=1e-6, residual=None, *, out=None, total=None, stream=None):
     """y = t / sqrt(mean(t^2) + eps) * weight of rows t = x [R, H], or with
     ``residual`` [R, H] t = bf16(x + residual): y bf16, or (y, t). ``total``, where t
     goes, may be x or residual."""
-    dev = _matrix(x, "x", _BF16).get_device()
-    out = _given(out, "out", x.shape, _BF16, dev, stream)
-    total = _norm(x, weight, eps, residual, out, total, _lib.MOE_QUANT_NONE, None, None, stream)
-    return out if total is None else (out, total)
+    y, _, _, t = _norm(x, weight, eps, residual, out, total, _lib.MOE_QUANT_NONE, None, None, stream)
+    return y if residual is None else (y, t)
 
 
 def rms_norm_fp8(x, weight, eps=1e-6, residual=None, *, out=None, total=None, q=None, s=None,
@@ -79,12 +85,8 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, *, out=None, total=None, q=
     """``rms_norm`` with y as ``products.quant_fp8`` has it, of the unrounded values:
     (codes [R, H], scales [R, ceil(H/128)]), with ``residual`` followed by t. ``out``
     (bf16 [R, H], optional) receives y itself as well, for the router."""
-    dev = _matrix(x, "x", _BF16).get_device()
-    R, H = x.shape
-    q = _given(q, "q", (R, H), _FP8, dev, stream)
-    s = _given(s, "s", (R, -(-H // 128)), _F32, dev, stream)
-    total = _norm(x, weight, eps, residual, out, total, _lib.MOE_QUANT_FP8, q, s, stream)
-    return (q, s) if total is None else (q, s, total)
+    _, q, s, t = _norm(x, weight, eps, residual, out, total, _lib.MOE_QUANT_FP8, q, s, stream)
+    return (q, s) if residual is None else (q, s, t)
 
 
 def rms_norm_mxfp4(x, weight, eps=1e-6, residual=None, *, out=None, total=None, q=None, s=None,
@@ -92,14 +94,8 @@ def rms_norm_mxfp4(x, weight, eps=1e-6, residual=None, *, out=None, total=None, 
     """``rms_norm`` with y as ``products.quant_mxfp4`` has it, of the unrounded values:
     (codes [R, H/2], scales [R, H/32]), with ``residual`` followed by t. ``out`` as for
     ``rms_norm_fp8``. H is a multiple of 32."""
-    dev = _matrix(x, "x", _BF16).get_device()
-    R, H = x.shape
-    if H % 32:
-        _fail(f"x: {H} columns, a multiple of 32 is needed")
-    q = _given(q, "q", (R, H // 2), _U8, dev, stream)
-    s = _given(s, "s", (R, H // 32), P._E8M0, dev, stream)
-    total = _norm(x, weight, eps, residual, out, total, _lib.MOE_QUANT_MXFP4, q, s, stream)
-    return (q, s) if total is None else (q, s, total)
+    _, q, s, t = _norm(x, weight, eps, residual, out, total, _lib.MOE_QUANT_MXFP4, q, s, stream)
+    return (q, s) if residual is None else (q, s, t)
 
 
 _sizes = {}      # workspace bytes by (R, H, GPU)
@@ -127,28 +123,30 @@ def rms_norm_grad(x, weight, dy, eps=1e-6, dtotal=None, *, dx=None, dw=None, acc
     ``_lib.moe_rms_norm_grad_workspace``'s bytes; needed with a stream handle."""
     dev = _matrix(x, "x", _BF16).get_device()
     _no_history(x, weight, dy, dtotal)
-    R, H = x.shape
-    pw = _vector(weight, "weight", H, dev)
-    if _matrix(dy, "dy", _BF16, dev).shape != x.shape:
-        _fail(f"dy: {tuple(dy.shape)}, {list(x.shape)} is needed")
-    pt = _like(dtotal, "dtotal", x.shape, _BF16, dev)
+    shape = x.shape
+    R, H = shape
+    pw = _at(weight, "weight", _BF16, (H,), dev)
+    pdy = _at(dy, "dy", _BF16, shape, dev)
+    pt = None if dtotal is None else _at(dtotal, "dtotal", _BF16, shape, dev)
     if accumulate and dw is None:
         _fail("dw: needed to accumulate into")
-    dx = _given(dx, "dx", x.shape, _BF16, dev, stream)
-    dw = _given(dw, "dw", (H,), _F32, dev, stream)
+    dx, pdx = _given(dx, "dx", shape, _BF16, dev, stream)
+    dw, pdw = _given(dw, "dw", (H,), _F32, dev, stream)
     ws = _grad_workspace(R, H, dev, stream, ws)
-    _run("moe_rms_norm_grad", dev, stream, x.data_ptr(), pw, dy.data_ptr(), pt, eps, R, H, dx.data_ptr(),
-         dw.data_ptr(), int(bool(accumulate)), ws.data_ptr(), ws.numel())
+    _run("moe_rms_norm_grad", dev, stream, x.data_ptr(), pw, pdy, pt, eps, R, H, pdx, pdw,
+         int(bool(accumulate)), ws.data_ptr(), ws.numel())
     return dx, dw
 
 
-def _pairs(pair_row, T, dev):
-    """(address, k)"""
+def _pairs(pair_row, dev):
+    """(address, T, k)"""
     _need(pair_row, "pair_row", _I32, dev)
-    if pair_row.dim() != 2 or pair_row.shape[0] != T or pair_row.shape[1] < 1:
-        _fail(f"pair_row: {tuple(pair_row.shape)}, [{T}, k] is needed")
-    _int(pair_row.numel(), "pair_row")
-    return pair_row.data_ptr(), pair_row.shape[1]
+    if pair_row.dim() != 2:
+        _fail(f"pair_row: {tuple(pair_row.shape)}, [T, k] is needed")
+    T, k = pair_row.shape
+    if k < 1 or T * k > 0x7FFFFFFF:
+        _fail(f"pair_row: {T} x {k} pairs")
+    return pair_row.data_ptr(), T, k
 
 
 def dispatch(x, pair_row, *, out=None, stream=None):
@@ -157,8 +155,10 @@ def dispatch(x, pair_row, *, out=None, stream=None):
     of the pairs are distinct. The gradient is ``combine`` without weights."""
     dev = _matrix(x, "x", _BF16).get_device()
     _no_history(x)
-    T, H = x.shape
-    pr, k = _pairs(pair_row, T, dev)
+    pr, T, k = _pairs(pair_row, dev)
+    if x.shape[0] != T:
+        _fail(f"x: {x.shape[0]} rows, pair_row has {T}")
+    H = x.shape[1]
     out = _output(out, "out", (T * k, H), _BF16, dev, stream)
     if out.dim() != 2 or out.shape[1] != H:
         _fail(f"out: {tuple(out.shape)}, [n, {H}] is needed")
@@ -172,14 +172,12 @@ def combine(y, pair_row, w=None, add=None, *, out=None, stream=None):
     bf16 [T, H] (the always-on expert's rows, or a residual)."""
     dev = _matrix(y, "y", _OUT).get_device()
     _no_history(y, w, add)
-    if not isinstance(pair_row, torch.Tensor) or pair_row.dim() != 2:
-        _fail("pair_row: an int32 tensor [T, k] is needed")
-    T, H = pair_row.shape[0], y.shape[1]
-    pr, k = _pairs(pair_row, T, dev)
-    pw, pa = _like(w, "w", (T, k), _F32, dev), _like(add, "add", (T, H), _BF16, dev)
-    out = _given(out, "out", (T, H), _BF16, dev, stream)
-    _run("moe_combine_rows", dev, stream, y.data_ptr(), int(y.dtype is torch.float32), y.shape[0], pr, pw, pa,
-         T, k, H, out.data_ptr())
+    pr, T, k = _pairs(pair_row, dev)
+    n, H = y.shape
+    pw = None if w is None else _at(w, "w", _F32, (T, k), dev)
+    pa = None if add is None else _at(add, "add", _BF16, (T, H), dev)
+    out, po = _given(out, "out", (T, H), _BF16, dev, stream)
+    _run("moe_combine_rows", dev, stream, y.data_ptr(), int(y.dtype is torch.float32), n, pr, pw, pa, T, k, H, po)
     return out
 
 
@@ -191,15 +189,15 @@ def combine_grad(dout, y, pair_row, w, *, dy=None, dw=None, stream=None):
     distinct. add's gradient is dout."""
     dev = _matrix(dout, "dout", _BF16).get_device()
     _no_history(dout, y, w)
-    T, H = dout.shape
-    if _matrix(y, "y", _BF16, dev).shape[1] != H:
-        _fail(f"y: {y.shape[1]} columns, dout has {H}")
-    pr, k = _pairs(pair_row, T, dev)
+    shape = _matrix(y, "y", _BF16, dev).shape
+    n, H = shape
+    pr, T, k = _pairs(pair_row, dev)
+    if dout.shape != (T, H):
+        _fail(f"dout: {tuple(dout.shape)}, [{T}, {H}] is needed")
     if w is None:
         _fail("w: needed (without weights, dispatch gives dy)")
-    pw = _like(w, "w", (T, k), _F32, dev)
-    dy = _given(dy, "dy", y.shape, _BF16, dev, stream)
-    dw = _given(dw, "dw", (T, k), _F32, dev, stream)
-    _run("moe_combine_rows_grad", dev, stream, dout.data_ptr(), y.data_ptr(), y.shape[0], pr, pw, T, k, H,
-         dy.data_ptr(), dw.data_ptr())
+    pw = _at(w, "w", _F32, (T, k), dev)
+    dy, pdy = _given(dy, "dy", shape, _BF16, dev, stream)
+    dw, pdw = _given(dw, "dw", (T, k), _F32, dev, stream)
+    _run("moe_combine_rows_grad", dev, stream, dout.data_ptr(), y.data_ptr(), n, pr, pw, T, k, H, pdy, pdw)
     return dy, dw

@@ -318,8 +318,9 @@ def test_product_from_packed_blobs():
         _within(got, ref, _bound(ref, mag, K, torch.bfloat16), "y")
 
 
-# paths by rows per expert: streaming, tiles, tiles with a cut sum
-PATHS = {"stream": ([5, 0, 9, 3], 64, 512), "tiles": ([300, 0, 140, 77] * 8, 1040, 256), "cut": ([60, 0, 31], 64, 2048)}
+# the streaming kernel, tiles, tiles with a cut sum, large tiles
+PATHS = {"stream": ([5, 0, 9, 3], 64, 512), "tiles": ([300, 0, 140, 77] * 8, 1040, 256), "cut": ([60, 0, 31], 64, 2048),
+         "large": ([300, 0, 140, 77] * 8, 2064, 768)}
 
 
 @pytest.mark.parametrize("path", list(PATHS))
