@@ -79,6 +79,16 @@ def _need(t, name, dtypes, dev=None):
     _fail(f"{name}: on GPU {t.get_device()}, the others are on {dev}")
 
 
+def _at(t, name, dtypes, shape, dev):
+    """Address of t: contiguous, one of `dtypes`, of this shape, on GPU `dev`. (A small
+    call's time is its checks: one line where all is well.)"""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, name, dtypes, dev)
+    _fail(f"{name}: {tuple(t.shape)}, {list(shape)} is needed")
+
+
 def _int(n, name):
     """n, as the library's 32-bit int takes it (ctypes would cut it to that)."""
     if not -0x80000000 <= n <= 0x7FFFFFFF:
@@ -283,31 +293,26 @@ def grouped_matmul_mxfp4(x, x_scale, w, w_scale=None, offsets=None, *, rows=None
     ``TableMatrices`` of packed "mxfp4" blobs -> [R, N] bf16 or fp32. N is a multiple
     of 16, K of 128."""
     dev = _matrix(x, "x", _U8).get_device()
-    _no_history(w)
+    n, half = x.shape
     if isinstance(w, TableMatrices):
         pw, ps, tab, mat, E, N, K = _weights(w, w_scale, _U8, dev)
     else:
-        _need(w, "w", _U8, dev)
-        if w.dim() not in (2, 3):
+        if _need(w, "w", _U8, dev).dim() not in (2, 3):
             _fail(f"w: [E, N, K/2] or [N, K/2] is needed, got {tuple(w.shape)}")
-        E, N, K = (1, *w.shape) if w.dim() == 2 else w.shape
-        K *= 2
-        _int(max(E, N, K), "w")
-        _need(w_scale, "w_scale", _E8M0, dev)
-        if w_scale.shape[-2:] != (N, K // 32) or w_scale.numel() != E * N * (K // 32):
-            _fail(f"w_scale: {tuple(w_scale.shape)}, [E, {N}, {K // 32}] is needed")
-        pw, ps, tab, mat = w.data_ptr(), w_scale.data_ptr(), None, 0
-    if 2 * x.shape[1] != K:
-        _fail(f"x: {2 * x.shape[1]} columns, w has {K}")
-    if _matrix(x_scale, "x_scale", _E8M0, dev).shape != (x.shape[0], K // 32):
-        _fail(f"x_scale: {tuple(x_scale.shape)}, [{x.shape[0]}, {K // 32}] is needed")
-    R = _count(x, rows, "rows")
+        shape = w.shape
+        E, N = shape[:2] if len(shape) == 3 else (1, shape[0])
+        K = 2 * shape[-1]
+        pw, ps, tab, mat = w.data_ptr(), _at(w_scale, "w_scale", _E8M0, (*shape[:-1], K // 32), dev), None, 0
+    if 2 * half != K:
+        _fail(f"x: {2 * half} columns, w has {K}")
+    pxs = _at(x_scale, "x_scale", _E8M0, (n, K // 32), dev)
+    _int(max(E, N, K), "w")
+    R = n if rows is None else _count(x, rows, "rows")
     out = _rows_output(out, "out", R, N, out_rows, _OUT, dev, stream)
     ws, pws, nws = _workspace(_lib.MOE_GEMM_MXFP4, R, N, K, E, dev, stream, ws)
-    _run("moe_grouped_gemm_mxfp4", dev, stream, x.data_ptr(), x_scale.data_ptr(),
-         _index(rows, "rows", R, dev), _int(div, "div"), x.shape[0], _offsets(offsets, E, dev), pw, ps, tab,
-         mat, R, N, K, E, out.data_ptr(), _index(out_rows, "out_rows", R, dev), out.shape[0],
-         int(out.dtype is torch.float32), pws, nws)
+    _run("moe_grouped_gemm_mxfp4", dev, stream, x.data_ptr(), pxs, _index(rows, "rows", R, dev),
+         _int(div, "div"), n, _offsets(offsets, E, dev), pw, ps, tab, mat, R, N, K, E, out.data_ptr(),
+         _index(out_rows, "out_rows", R, dev), out.shape[0], int(out.dtype is torch.float32), pws, nws)
     return out
 
 
@@ -451,11 +456,12 @@ def swiglu_quant_fp8(h, n_rows=None, q=None, s=None, stream=None):
 def _to_mxfp4(fn, x, R, K, n_rows, q, s, dev, stream):
     if K % 32:
         _fail(f"{K} columns, a multiple of 32 is needed")
-    q = _output(q, "q", (R, K // 2), _U8, dev, stream)
-    s = _output(s, "s", (R, K // 32), _E8M0, dev, stream)
-    if q.shape != (R, K // 2) or s.shape != (R, K // 32):
-        _fail(f"q, s: {tuple(q.shape)}, {tuple(s.shape)} for {R} rows of {K}")
-    _run(fn, dev, stream, x.data_ptr(), _limit(n_rows, dev), R, K, q.data_ptr(), s.data_ptr())
+    if q is None:
+        q = _output(None, "q", (R, K // 2), _U8, dev, stream)
+    if s is None:
+        s = _output(None, "s", (R, K // 32), _E8M0, dev, stream)
+    _run(fn, dev, stream, x.data_ptr(), _limit(n_rows, dev), R, K, _at(q, "q", _U8, (R, K // 2), dev),
+         _at(s, "s", _E8M0, (R, K // 32), dev))
     return q, s
 
 

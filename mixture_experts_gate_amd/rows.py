@@ -21,20 +21,8 @@ from __future__ import annotations
 import torch
 
 from . import _lib, products as P
-from .products import _BF16, _F32, _FP8, _I32, _fail, _int, _matrix, _need, _no_history, _output, _run
-
-_U8 = (torch.uint8,)
-_OUT = (torch.bfloat16, torch.float32)
-
-
-def _at(t, name, dtypes, shape, dev):
-    """Address of t: contiguous, one of `dtypes`, of this shape, on GPU `dev`. (A small
-    call's time is its checks: one line where all is well.)"""
-    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev
-            and t.is_contiguous()):
-        return t.data_ptr()
-    _need(t, name, dtypes, dev)
-    _fail(f"{name}: {tuple(t.shape)}, {list(shape)} is needed")
+from .products import (_BF16, _F32, _FP8, _I32, _OUT, _U8, _at, _fail, _int, _matrix, _need, _no_history, _output,
+                       _run)
 
 
 def _given(t, name, shape, dtypes, dev, stream):
