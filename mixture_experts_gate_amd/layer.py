@@ -11,7 +11,7 @@ import time
 import numpy as np
 import torch
 
-from . import _lib, products
+from . import _lib, products, rows
 from .synth import blob_layout
 
 # moe_permute_ffn_combine derives the permutation in its gate/up launch from
@@ -362,20 +362,22 @@ class MoeLayer:
                             stream)
 
 
-class Fp8BlockLayer:
-    """One layer whose experts are FP8 matrices with a scale per 128 x 128 block
-    (blobs of ``blob_layout(H, I, "fp8_block")``), with at most T_max tokens:
-    route and permute, the tokens to FP8 with a scale per 128 columns, the
-    gate/up product, silu(g) u to FP8, the down product and the combine. H and I
-    are multiples of 32. For inference: inputs that require grad are refused
-    where gradients are enabled.
+class _CodedLayer:
+    """One layer whose experts and their inputs are held in 8 or 4 bits, with at most
+    T_max tokens: (norm,) route and permute, the tokens' rows to codes, the gate/up
+    product, silu(g) u to codes, the down product and the combine. For inference:
+    inputs that require grad are refused where gradients are enabled.
 
-    ``table`` is a device table of moe_expert_w, as ``expert_table`` makes it
-    for resident experts or ``ExpertCache.prefetch`` returns it."""
+    ``table`` is a device table of moe_expert_w, as ``expert_table`` makes it for
+    resident experts or ``ExpertCache.prefetch`` returns it. With ``norm`` the layer
+    has the buffers that ``forward``'s ``norm_w`` needs."""
 
-    def __init__(self, H, E, k, I, T_max, shared=False, device="cuda"):
-        if H % 32 or I % 32 or E > 512:
-            raise ValueError("H and I must be multiples of 32, E at most 512")
+    unit = None                              # H and I are multiples of it
+    quant = gated = product = norm_rows = None
+
+    def __init__(self, H, E, k, I, T_max, shared=False, device="cuda", norm=False):
+        if H % self.unit or I % self.unit or E > 512:
+            raise ValueError(f"H and I must be multiples of {self.unit}, E at most 512")
         self.H, self.E, self.k, self.I, self.T_max, self.shared = H, E, k, I, T_max, shared
         n = max(T_max * k, 1)
         bf16, i32 = torch.bfloat16, torch.int32
@@ -389,16 +391,18 @@ class Fp8BlockLayer:
         self.sorted_pair, self.pair_row = buf(n, dtype=i32), buf(n, dtype=i32)
         self.ws_perm_bytes = max(_lib.moe_workspace_size(T_max, k, H, I, E)[0], 256)
         self.ws_perm = buf(self.ws_perm_bytes, dtype=torch.uint8)
-        self.xq, self.xs = buf(T_max, H, dtype=torch.uint8), buf(T_max, -(-H // 128), dtype=torch.float32)
+        self.xq, self.xs = self._codes(T_max, H, device)
         self.h = buf(n, 2 * I, dtype=bf16)
-        self.aq, self.a_s = buf(n, I, dtype=torch.uint8), buf(n, -(-I // 128), dtype=torch.float32)
+        self.aq, self.a_s = self._codes(n, I, device)
         self.y, self.out = buf(n, H, dtype=bf16), buf(T_max, H, dtype=bf16)
         # of the products' cut sums, of which the forward product's have R x N values
         self.ws_sum = buf(products.workspace_bound(n, max(2 * I, H), 0, E, device), dtype=torch.uint8)
         if shared:
             self.h_sh, self.y_sh = buf(T_max, 2 * I, dtype=bf16), buf(T_max, H, dtype=bf16)
-            self.aq_sh = buf(T_max, I, dtype=torch.uint8)
-            self.as_sh = buf(T_max, -(-I // 128), dtype=torch.float32)
+            self.aq_sh, self.as_sh = self._codes(T_max, I, device)
+        self.norm = norm
+        if norm:
+            self.xn, self.total = buf(T_max, H, dtype=bf16), buf(T_max, H, dtype=bf16)
 
     def matrices(self, table, E=None):
         """(W13, W2) of the experts of `table`."""
@@ -423,57 +427,120 @@ class Fp8BlockLayer:
         """The experts of the current permutation: y in pair order, and the
         shared expert's rows (or None)."""
         self._check_tables(table, shared_table)
+        self.quant(x[:T], q=self.xq[:T], s=self.xs[:T], stream=stream)
+        return self._experts(T, table, shared_table, stream)
+
+    def _experts(self, T, table, shared_table, stream):
+        """The same for the rows that xq and xs hold."""
         n = T * self.k
         pair = self.sorted_pair[:n]
         w13, w2 = self.matrices(table)
-        xq, xs = products.quant_fp8(x[:T], q=self.xq[:T], s=self.xs[:T], stream=stream)
-        h = products.grouped_matmul_fp8(xq, xs, w13, None, self.offsets, rows=pair, div=self.k,
-                                        out=self.h[:n], ws=self.ws_sum, stream=stream)
-        aq, a_s = products.swiglu_quant_fp8(h, n_rows=self.offsets[self.E:], q=self.aq[:n],
-                                            s=self.a_s[:n], stream=stream)
-        products.grouped_matmul_fp8(aq, a_s, w2, None, self.offsets, out_rows=pair,
-                                    out=self.y[:n], ws=self.ws_sum, stream=stream)
+        xq, xs = self.xq[:T], self.xs[:T]
+        h = self.product(xq, xs, w13, None, self.offsets, rows=pair, div=self.k,
+                         out=self.h[:n], ws=self.ws_sum, stream=stream)
+        aq, a_s = self.gated(h, n_rows=self.offsets[self.E:], q=self.aq[:n], s=self.a_s[:n],
+                             stream=stream)
+        self.product(aq, a_s, w2, None, self.offsets, out_rows=pair, out=self.y[:n],
+                     ws=self.ws_sum, stream=stream)
         if shared_table is None:
             return self.y[:n], None
         s13, s2 = self.matrices(shared_table, 1)
-        h = products.grouped_matmul_fp8(xq, xs, s13, out=self.h_sh[:T], ws=self.ws_sum,
-                                        stream=stream)
-        aq, a_s = products.swiglu_quant_fp8(h, q=self.aq_sh[:T], s=self.as_sh[:T], stream=stream)
-        products.grouped_matmul_fp8(aq, a_s, s2, out=self.y_sh[:T], ws=self.ws_sum, stream=stream)
+        h = self.product(xq, xs, s13, out=self.h_sh[:T], ws=self.ws_sum, stream=stream)
+        aq, a_s = self.gated(h, q=self.aq_sh[:T], s=self.as_sh[:T], stream=stream)
+        self.product(aq, a_s, s2, out=self.y_sh[:T], ws=self.ws_sum, stream=stream)
         return self.y[:n], self.y_sh[:T]
 
     def forward(self, T, x, table, logits=None, wg=None, shared_table=None, renormalize=True,
-                stream=None):
-        """route -> permute -> experts -> combine; returns out[:T] (bf16)."""
+                stream=None, *, norm_w=None, residual=None, eps=1e-6):
+        """route -> permute -> experts -> combine; returns out[:T] (bf16). With
+        ``norm_w`` (bf16 [H]) the layer's input, the router's too, is the norm of x, or
+        with ``residual`` (bf16 [T, H]) of t = x + residual, which ``self.total[:T]``
+        then holds; the experts' rows come as codes straight from the norm."""
         if T > self.T_max:
             raise ValueError("T exceeds the buffers' T_max")
         for t, name, n, cols, dtype in ((x, "x", T, self.H, torch.bfloat16),
                                         (logits, "logits", T, self.E, torch.float32),
-                                        (wg, "wg", self.E, self.H, torch.bfloat16)):
+                                        (wg, "wg", self.E, self.H, torch.bfloat16),
+                                        (residual, "residual", T, self.H, torch.bfloat16)):
             if t is None and name != "x":
                 continue
             if (t.dim() != 2 or t.shape[0] < n or t.shape[1] != cols or t.dtype != dtype
                     or not t.is_contiguous() or not t.is_cuda or t.device != self.out.device):
                 raise ValueError(f"{name}: contiguous {dtype} [{n}, {cols}] on {self.out.device} "
                                  "is needed")
-        products._no_history(x, logits, wg)
+        if norm_w is not None:
+            if not self.norm:
+                raise ValueError("layer was built without the norm's buffers")
+            if (norm_w.shape != (self.H,) or norm_w.dtype != torch.bfloat16 or not norm_w.is_contiguous()
+                    or norm_w.device != self.out.device or norm_w.data_ptr() % 16):
+                raise ValueError(f"norm_w: bf16 [{self.H}] on {self.out.device} is needed")
+            if not 0.0 <= eps <= 3e38:
+                raise ValueError(f"eps: {eps}")
+        elif residual is not None:
+            raise ValueError("residual: given without norm_w")
+        products._no_history(x, logits, wg, norm_w, residual)
         if T == 0:
             return self.out[:0]
         if logits is None and wg is None:
             raise ValueError("logits or wg is needed")
-        if x.data_ptr() % 16:
-            raise ValueError("x: must start at a multiple of 16 bytes")
+        for t, name in ((x, "x"), (residual, "residual")):
+            if t is not None and t.data_ptr() % 16:
+                raise ValueError(f"{name}: must start at a multiple of 16 bytes")
         self._check_tables(table, shared_table)
         if x.get_device() != torch.cuda.current_device():
             with torch.cuda.device(x.device):
-                return self.forward(T, x, table, logits, wg, shared_table, renormalize, stream)
+                return self.forward(T, x, table, logits, wg, shared_table, renormalize, stream,
+                                    norm_w=norm_w, residual=residual, eps=eps)
+        if norm_w is not None:
+            total = None if residual is None else self.total[:T]
+            self.norm_rows(x[:T], norm_w, eps, None if residual is None else residual[:T], out=self.xn[:T],
+                           total=total, q=self.xq[:T], s=self.xs[:T], stream=stream)
+            x = self.xn
         _lib.moe_route_permute(x, wg, logits, None if logits is not None else self.logits, T, self.H,
                                self.E, self.k, renormalize, self.topk_ids, self.topk_w,
                                self.offsets, self.sorted_pair, self.pair_row, self.ws_perm,
                                self.ws_perm_bytes, stream)
-        y, y_sh = self.ffn(T, x, table, shared_table, stream)
+        if norm_w is not None:
+            y, y_sh = self._experts(T, table, shared_table, stream)
+        else:
+            y, y_sh = self.ffn(T, x, table, shared_table, stream)
         _lib.moe_combine(y, False, self.topk_w, y_sh, T, self.k, self.H, self.out, stream)
         return self.out[:T]
+
+
+class Fp8BlockLayer(_CodedLayer):
+    __doc__ = """Experts that are FP8 matrices with a scale per 128 x 128 block (blobs of
+    ``blob_layout(H, I, "fp8_block")``), their inputs FP8 with a scale per 128 columns. H
+    and I are multiples of 32.
+
+    """ + _CodedLayer.__doc__
+
+    unit = 32
+    quant, gated = staticmethod(products.quant_fp8), staticmethod(products.swiglu_quant_fp8)
+    product, norm_rows = staticmethod(products.grouped_matmul_fp8), staticmethod(rows.rms_norm_fp8)
+
+    @staticmethod
+    def _codes(n, cols, device):
+        return (torch.empty(n, cols, dtype=torch.uint8, device=device),
+                torch.empty(n, -(-cols // 128), dtype=torch.float32, device=device))
+
+
+class Mxfp4Layer(_CodedLayer):
+    __doc__ = """Experts that are MXFP4 matrices in the kernel layout (packed blobs of
+    ``blob_layout(H, I, "mxfp4")``, as ``MoeLayer`` reads them), their inputs MXFP4 too:
+    four bits on both sides of the products, where ``MoeLayer`` holds the activations to
+    bf16's precision or near it. H and I are multiples of 128.
+
+    """ + _CodedLayer.__doc__
+
+    unit = 128
+    quant, gated = staticmethod(products.quant_mxfp4), staticmethod(products.swiglu_quant_mxfp4)
+    product, norm_rows = staticmethod(products.grouped_matmul_mxfp4), staticmethod(rows.rms_norm_mxfp4)
+
+    @staticmethod
+    def _codes(n, cols, device):
+        return (torch.empty(n, cols // 2, dtype=torch.uint8, device=device),
+                torch.empty(n, cols // 32, dtype=torch.uint8, device=device))
 
 
 def layout_for(cfg):
