@@ -251,13 +251,22 @@ constexpr int kBSlabs = 6;       // slabs of K from which this kernel runs, an e
 constexpr uint32_t kBBytes = 0x7FFFFFF0u;    // bytes of out at most; offsets from here on are not stored
 constexpr int kBPair = 32768;    // bytes of a pair of slabs of p or q
 
+// Rows p0 on of expert e, whose cnt rows begin at lo, `units` times 32 of them; n from q0.
+struct LargeTile {
+    int e, lo, cnt, p0, q0, units;
+};
+constexpr int kBList = 64;       // tiles looked up at a time, one a lane (one after the other
+                                 // they took a microsecond each, of ten)
+
 struct LargeLds {
     char p[2][kBPair], q[2][kBPair];             // slabs as in TileLds, 256 rows each
     uint32_t xs[2][kBT][2];                      // rows' scales, of a pair
     char qs[2][8][288];                          // two blocks' scales, of a pair (32 bytes on
                                                  // for every two: 8 blocks in different banks)
-    int raw[kBT], rawo[kBT];                     // the next tile's indices into x and out
-    uint32_t to[2][kBT];                         // offset of rows in out, by tile
+    int raw[kBT], rawo[kBT];                     // the next tile's indices into x and out,
+    int src[kBT];                                // its rows of x,
+    uint32_t to[2][kBT];                         // and the offsets of its rows in out, by tile
+    LargeTile list[kBList];                      // the workgroup's next tiles
     int base[kMaxE + 1];                         // p tiles before each expert
     int wsum[kBThreads / kWave];
 };
@@ -294,30 +303,34 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
     if (late > 0 && rank >= late)
         for (int i = (int)((long)slabs * 12 * (rank - late) / (per - late)); i > 0; --i) __builtin_amdgcn_s_sleep(1);
 
-    struct Tile {
-        int e, lo, cnt, p0, q0, units;
-    };
-    auto locate = [&](int ti, int e) {
+    using Tile = LargeTile;
+    // the workgroup's tiles n, n + 1, ..., by one wavefront
+    auto look_up = [&](int n) {
+        const long ti = si + (long)(n + l) * per;
+        if (ti >= t1) return;
         Tile t;
+        int e = 0, end = A.E;
+        while (end - e > 1) {
+            const int mid = (e + end) >> 1;
+            if ((long)L.base[mid] * tq <= ti) e = mid;
+            else end = mid;
+        }
+        const int mp = L.base[e + 1] - L.base[e], li = (int)(ti - (long)L.base[e] * tq);
         t.e = e;
-        const int mp = __builtin_amdgcn_readfirstlane(L.base[e + 1] - L.base[e]);
-        const int li = ti - __builtin_amdgcn_readfirstlane(L.base[e]) * tq;
-        group_of(A, e, t.lo, t.cnt);
+        group_of_lane(A, e, t.lo, t.cnt);
         // rows spread evenly over the expert's tiles, in units of 32 (more than
         // eight only where offsets do not ascend)
         const int units = (int)((t.cnt + 32u * mp - 1) / (32u * mp));
         t.units = units < 8 ? units : 8;
         place_of(li, mp, tq, t.p0, t.q0);
         t.p0 *= 32 * t.units, t.q0 *= kBT;
-        return t;
+        L.list[l] = t;
     };
-    // the expert of a later tile: 64 experts a look
-    auto expert_from = [&](int e, int ti) {
-        for (;; e += kWave) {
-            const int i = e + 1 + l < A.E ? e + 1 + l : A.E;
-            const unsigned long long m = __ballot((long)L.base[i] * tq > ti);
-            if (m) return e + __ffsll(m) - 1;
-        }
+    auto listed = [&](int n) {
+        const Tile t = L.list[n % kBList];
+        return Tile{__builtin_amdgcn_readfirstlane(t.e),  __builtin_amdgcn_readfirstlane(t.lo),
+                    __builtin_amdgcn_readfirstlane(t.cnt), __builtin_amdgcn_readfirstlane(t.p0),
+                    __builtin_amdgcn_readfirstlane(t.q0), __builtin_amdgcn_readfirstlane(t.units)};
     };
     // row `row` of LDS: unit u is rows 32 (u / 2) of wavefront row u % 2; -1: past the end
     auto place = [&](const Tile &t, int row) {
@@ -336,14 +349,20 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
         return t.lo + (p < 0 ? 0 : p);      // (a row past the end reads the expert's first one)
     };
 
-    Tile cur = locate(si, expert_of(L.base, A.E, tq, si)), next = cur;
-    bool more = si + per < t1;
-    // the first tile's rows, from memory
-    if (threadIdx.x < kBT) {
-        const int t = threadIdx.x, i = index_at(cur, t);
-        const int raw = A.a.idx ? A.a.idx[i] : 0;
-        L.raw[t] = raw;
-        L.to[0][t] = out_at(cur, t, raw, A.out_rows ? A.out_rows[i] : 0);
+    if (w == 0) look_up(0);
+    __syncthreads();
+    const int tiles = (t1 - si + per - 1) / per;
+    int n = 0;                           // this tile's number
+    Tile cur = listed(0), next = cur;
+    // a thread's row of a tile, from its indices: row of x, offset in out
+    auto note_row = [&](const Tile &t, int to, int raw, int rawo) {
+        const int row = threadIdx.x, r = A.a.idx ? row_of_index(A.a, raw) : index_at(t, row);
+        L.src[row] = r < 0 ? 0 : r;
+        L.to[to][row] = out_at(t, row, raw, rawo);
+    };
+    {
+        const int i = index_at(cur, threadIdx.x);
+        note_row(cur, 0, A.a.idx ? A.a.idx[i] : 0, A.out_rows ? A.out_rows[i] : 0);
     }
     __syncthreads();
 
@@ -353,21 +372,17 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
     const char *pn, *qn[4], *xn, *sn;
     int ck = 0;                                      // that slab
     auto enter = [&](const Tile &t) {
-        auto row_at = [&](int row) {
-            const int r = A.a.idx ? row_of_index(A.a, L.raw[row]) : index_at(t, row);
-            return (uint32_t)(r < 0 ? 0 : r);
-        };
         const int rb = t.q0 / 16 + 4 * w;
         const char *const codes = codes_of(X, t.e);
         pn = A.a.base, xn = (const char *)X.xs, sn = scales_of(X, t.e);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            po[i] = row_at(64 * w + 16 * i + (l >> 2)) * (uint32_t)(A.K / 2) + 16 * ((l & 3) ^ ((l >> 4) & 3));
+            po[i] = (uint32_t)L.src[64 * w + 16 * i + (l >> 2)] * (uint32_t)(A.K / 2) + 16 * ((l & 3) ^ ((l >> 4) & 3));
             qn[i] = codes + (size_t)(rb + i < blocks ? rb + i : blocks - 1) * slabs * 1024;
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            xo[i] = row_at(64 * w + 32 * i + (l >> 1)) * (uint32_t)(A.K / 32) + 4 * (l & 1);
+            xo[i] = (uint32_t)L.src[64 * w + 32 * i + (l >> 1)] * (uint32_t)(A.K / 32) + 4 * (l & 1);
             so[i] = (uint32_t)((rb + 2 * i + h < blocks ? rb + 2 * i + h : blocks - 1) * slabs) * 64 + 4 * b;
         }
         ck = 0;
@@ -432,8 +447,13 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
     int u = 0, db = 0, stores = 0;       // pair in LDS, tile's place in `to`, stores before this tile
     // the next tile, and the indices of its rows
     auto look_ahead = [&]() {
-        if (!more) return;
-        next = locate(si + per, expert_from(cur.e, si + per));
+        if (n + 1 >= tiles) return;
+        if ((n + 1) % kBList == 0) {
+            if (w == 0) look_up(n + 1);
+            wait_lds();
+            bare_barrier();
+        }
+        next = listed(n + 1);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int row = 64 * w + l, at = index_at(next, row);
@@ -493,13 +513,10 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
 #undef MOE_MX
         };
         for (int k = 0; k < slabs; k += 2) {
-            if (k == 2 && more) {
-                const int t = 64 * w + l;
-                L.to[db ^ 1][t] = out_at(next, t, L.raw[t], L.rawo[t]);
-            }
+            if (k == 2 && n + 1 < tiles) note_row(next, db ^ 1, L.raw[threadIdx.x], L.rawo[threadIdx.x]);
             if (ck == slabs) {
                 // on to the next tile; behind the last one, its last pair once more
-                if (more) {
+                if (n + 1 < tiles) {
                     enter(next);
                 } else {
                     pn -= 128, xn -= 8, sn -= 128, ck -= 2;
@@ -525,10 +542,9 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
         // A lane stores four columns of 16 rows of each unit.
         const int q = cur.q0 + 128 * wq + 4 * b, bytes = A.out_f32 ? 4 : 2, last = db;
         const uint32_t col = q < A.N ? (uint32_t)(q * bytes) : kBBytes;
-        const bool done = !more;
-        if (more) {
-            db ^= 1, si += per, cur = next;
-            more = si + per < t1;
+        const bool done = n + 1 >= tiles;
+        if (!done) {
+            db ^= 1, ++n, cur = next;
             look_ahead();
         }
         const buf_rsrc out = make_rsrc(A.out, (uint32_t)A.out_n * ldo);

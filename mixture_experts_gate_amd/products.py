@@ -105,9 +105,11 @@ def _no_history(*inputs):
 
 
 def _matrix(t, name, dtype, dev=None):
-    if _need(t, name, dtype, dev).dim() != 2:
-        _fail(f"{name}: two dimensions are needed, got {tuple(t.shape)}")
-    _int(max(t.shape), name)
+    shape = _need(t, name, dtype, dev).shape
+    if len(shape) != 2:
+        _fail(f"{name}: two dimensions are needed, got {tuple(shape)}")
+    if shape[0] > 0x7FFFFFFF or shape[1] > 0x7FFFFFFF:
+        _int(max(shape), name)
     return t
 
 
@@ -183,13 +185,17 @@ def _output(out, name, shape, dtypes, dev, stream):
 
 def _rows_output(out, name, R, n, out_rows, dtypes, dev, stream):
     out = _output(out, name, (R, n), dtypes, dev, stream)
-    if out.dim() != 2 or out.shape[1] != n or (out_rows is None and out.shape[0] < R):
-        _fail(f"{name}: {tuple(out.shape)}, [{R}, {n}] is needed")
-    _int(out.shape[0], name)
+    shape = out.shape
+    if len(shape) != 2 or shape[1] != n or (out_rows is None and shape[0] < R):
+        _fail(f"{name}: {tuple(shape)}, [{R}, {n}] is needed")
+    if shape[0] > 0x7FFFFFFF:
+        _int(shape[0], name)
     return out
 
 
 _calls = {}      # the library's functions, once looked up
+_current_device = getattr(torch._C, "_cuda_getDevice", None)             # (none in a build without GPUs)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _sizes = {}      # workspace bytes by (kind, R, N, K, E, GPU)
 
 
@@ -229,11 +235,11 @@ def _run(fn, dev, stream, *args):
     call = _calls.get(fn)
     if call is None:
         call = _calls[fn] = getattr(_lib.load(), fn)
-    if torch._C._cuda_getDevice() != dev:
+    if _current_device() != dev:
         with torch.cuda.device(dev):
             return _run(fn, dev, stream, *args)
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
+        stream = _current_stream(dev)
     elif not isinstance(stream, int):
         if stream.device_index != dev:
             _fail(f"stream: of GPU {stream.device_index}, the tensors are on {dev}")
@@ -307,12 +313,18 @@ def grouped_matmul_mxfp4(x, x_scale, w, w_scale=None, offsets=None, *, rows=None
         _fail(f"x: {2 * half} columns, w has {K}")
     pxs = _at(x_scale, "x_scale", _E8M0, (n, K // 32), dev)
     _int(max(E, N, K), "w")
-    R = n if rows is None else _count(x, rows, "rows")
+    pr = po = None
+    R = n
+    if rows is not None:
+        R = _int(_need(rows, "rows", _I32, dev).numel(), "rows")
+        pr = rows.data_ptr()
+    if out_rows is not None:
+        po = _index(out_rows, "out_rows", R, dev)
     out = _rows_output(out, "out", R, N, out_rows, _OUT, dev, stream)
     ws, pws, nws = _workspace(_lib.MOE_GEMM_MXFP4, R, N, K, E, dev, stream, ws)
-    _run("moe_grouped_gemm_mxfp4", dev, stream, x.data_ptr(), pxs, _index(rows, "rows", R, dev),
-         _int(div, "div"), n, _offsets(offsets, E, dev), pw, ps, tab, mat, R, N, K, E, out.data_ptr(),
-         _index(out_rows, "out_rows", R, dev), out.shape[0], int(out.dtype is torch.float32), pws, nws)
+    _run("moe_grouped_gemm_mxfp4", dev, stream, x.data_ptr(), pxs, pr, _int(div, "div"), n,
+         _offsets(offsets, E, dev), pw, ps, tab, mat, R, N, K, E, out.data_ptr(), po, out.shape[0],
+         int(out.dtype is torch.float32), pws, nws)
     return out
 
 

@@ -433,6 +433,23 @@ def test_product_beyond_4_gib():
         _within(y, ref, _bound(ref, mag, K, torch.bfloat16), "y")
 
 
+def test_more_tiles_a_workgroup_than_are_looked_up_at_a_time():
+    """512 experts of a row or two, 33 columns of tiles each: 66 tiles a compute unit."""
+    E, N, K = 512, 8448, 768
+    counts = [1 + (e % 5 == 0) for e in range(E)]
+    R, g = sum(counts), _gen(12)
+    x = torch.randint(0, 256, (R, K // 2), device=DEV, generator=g, dtype=torch.uint8)
+    xs = (120 + torch.randint(-6, 7, (R, K // 32), device=DEV, generator=g)).to(torch.uint8)
+    wq = torch.randint(0, 256, (E, N, K // 2), device=DEV, generator=g, dtype=torch.uint8)
+    ws = (120 + torch.randint(-6, 7, (E, N, K // 32), device=DEV, generator=g)).to(torch.uint8)
+    y = P.grouped_matmul_mxfp4(x, xs, *kernel_order(wq, ws), _offsets(counts), out=torch.empty(R, N, device=DEV))
+    xd, first = decode(x, xs), np.concatenate([[0], np.cumsum(counts)])
+    for e in list(range(0, E, 23)) + [1, 255, 256, 510, 511]:
+        lo, hi = int(first[e]), int(first[e + 1])
+        ref, mag = _ref(xd[lo:hi], decode(wq[e], ws[e])[None], [hi - lo], torch.arange(hi - lo, device=DEV))
+        _within(y[lo:hi], ref, _bound(ref, mag, K, torch.float32), f"expert {e}")
+
+
 def test_refusals():
     x = torch.zeros(4, 64, dtype=torch.uint8, device=DEV)
     xs = torch.zeros(4, 4, dtype=torch.uint8, device=DEV)
