@@ -227,27 +227,31 @@ __global__ __launch_bounds__(kXThreads, 2) void mxfp4_tile_kernel(MxArgs X) {
 }
 
 // ------------------------------------------------------------ large tiles --
-// 256 x 256 a workgroup of four wavefronts, 128 x 128 each with the layout above, one
-// workgroup a compute unit and one wavefront a SIMD: two thirds of the bytes that tiles
-// of 128 x 256 copy into LDS for a product, and of those they read from it. The sums are
-// in 256 accumulation registers; the fragments of a slab are read, and the copies of a
-// later one issued, between the matrix instructions of the one before. One barrier a slab.
+// 256 x 256 a workgroup of eight wavefronts, 64 x 128 each as above, one workgroup a
+// compute unit: two thirds of the bytes that tiles of 128 x 256 copy into LDS. The
+// wavefronts of a SIMD (w and w + 4) run one phase apart: one reads a slab's fragments
+// while the other multiplies, its copies between the matrix instructions; a barrier
+// ends each phase. (Four wavefronts of 128 x 128 read a third less from LDS, but one
+// that reads, waits or stores leaves its SIMD idle: 8192 rows of 8192 x 8192 take
+// 284 us, 257 here.)
 //
-// LDS holds four slabs, two pairs. The copies run four slabs ahead, and on into the next
-// tile, whose rows are looked up during this one's first slabs: only a workgroup's first
-// tile waits for its first slab. Scales come a pair at a time (8 bytes a row, 128 a
-// block). Places in LDS are constants of a pair; copies and stores take 32-bit offsets
-// from uniform addresses, and stores no branch a row (rows of none lie outside the
-// buffer's range).
+// What bounds it: matrix instructions alone reach 6.5 PFLOP/s on random codes (the
+// power limit lowers the clock; on zeros 9.6). One expert of 8192 x 8192 reaches 4.3;
+// gate/up of 8192 tokens of 128 experts (1536 x 2048, 412 GFLOP, 201 MB of results)
+// 2.6: there the compute units store together, about 40 of its 160 us.
 //
-// 8192 x 8192 x 8192: 270 us, 4.1 PFLOP/s. What bounds it is power: matrix instructions
-// alone, on operands of random codes, reach 6.5 PFLOP/s at 1.6 GHz (on zeros 9.6); with
-// eight wavefronts a phase apart that read half as much again from LDS it is the same.
-constexpr int kBThreads = 256;
+// LDS holds four slabs, two pairs. The copies run three slabs ahead, and on into the
+// next tile, whose rows are looked up during this one's first slabs: only a workgroup's
+// first tile waits for its first slab. Scales come a pair at a time (8 bytes a row,
+// 128 a block). What a phase may take, the other wavefront's 512 cycles of matrix
+// instructions, is about a hundred instructions: hence pairs, whose places in LDS are
+// constants, 32-bit offsets from uniform addresses for copies and stores, and no branch
+// a row in the stores (rows of none lie outside the buffer's range).
+constexpr int kBThreads = 512;
 constexpr int kBT = 256;         // rows and n of a tile
-constexpr int kBSlabs = 6;       // slabs of K from which this kernel runs, an even number: a
-                                 // tile's copies begin four before the end of the last one,
-                                 // whose first two slabs have looked up its rows
+constexpr int kBSlabs = 6;       // slabs of K from which this kernel runs, an even number:
+                                 // a tile's copies begin three before the end of the last
+                                 // tile, which by then has looked up its rows
 constexpr uint32_t kBBytes = 0x7FFFFFF0u;    // bytes of out at most; offsets from here on are not stored
 constexpr int kBPair = 32768;    // bytes of a pair of slabs of p or q
 
@@ -271,13 +275,11 @@ struct LargeLds {
     int wsum[kBThreads / kWave];
 };
 
-// Until N + more are in flight (the counter holds 63), more a multiple of 16.
 template <int N>
-__device__ __forceinline__ void wait_some(int more) {
+__device__ __forceinline__ void wait_some(int more) {      // until N + more are in flight, more 0, 16 or 32
     if (more == 0) wait_copies<N>();
     else if (more == 16) wait_copies<N + 16>();
-    else if (more == 32 && N + 32 < 63) wait_copies<(N + 32 < 63 ? N + 32 : 63)>();
-    else wait_copies<63>();
+    else wait_copies<N + 32>();
 }
 
 __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
@@ -332,9 +334,9 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
                     __builtin_amdgcn_readfirstlane(t.cnt), __builtin_amdgcn_readfirstlane(t.p0),
                     __builtin_amdgcn_readfirstlane(t.q0), __builtin_amdgcn_readfirstlane(t.units)};
     };
-    // row `row` of LDS: unit u is rows 32 (u / 2) of wavefront row u % 2; -1: past the end
+    // row `row` of LDS: unit u is rows 32 (u / 4) of wavefront row u % 4; -1: past the end
     auto place = [&](const Tile &t, int row) {
-        const int u = 2 * ((row >> 5) & 3) + (row >> 7), p = t.p0 + 32 * u + (row & 31);
+        const int u = 4 * ((row >> 5) & 1) + (row >> 6), p = t.p0 + 32 * u + (row & 31);
         return u < t.units && p < t.cnt ? p : -1;
     };
     const uint32_t ldo = (uint32_t)A.N * (A.out_f32 ? 4 : 2);
@@ -354,210 +356,195 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
     const int tiles = (t1 - si + per - 1) / per;
     int n = 0;                           // this tile's number
     Tile cur = listed(0), next = cur;
-    // a thread's row of a tile, from its indices: row of x, offset in out
-    auto note_row = [&](const Tile &t, int to, int raw, int rawo) {
-        const int row = threadIdx.x, r = A.a.idx ? row_of_index(A.a, raw) : index_at(t, row);
+    // row `row` of a tile from its indices: row of x, offset in out
+    auto note_row = [&](const Tile &t, int to, int row, int raw, int rawo) {
+        const int r = A.a.idx ? row_of_index(A.a, raw) : index_at(t, row);
         L.src[row] = r < 0 ? 0 : r;
         L.to[to][row] = out_at(t, row, raw, rawo);
     };
-    {
+    if (threadIdx.x < kBT) {
         const int i = index_at(cur, threadIdx.x);
-        note_row(cur, 0, A.a.idx ? A.a.idx[i] : 0, A.out_rows ? A.out_rows[i] : 0);
+        note_row(cur, 0, threadIdx.x, A.a.idx ? A.a.idx[i] : 0, A.out_rows ? A.out_rows[i] : 0);
     }
     __syncthreads();
 
-    // Copies: a wavefront takes 64 rows of x, 16 an instruction, and four blocks of W.
+    // Copies: a wavefront takes 32 rows of x, 16 an instruction, and two blocks of W.
     // The lane's offsets into x, its scales and W's, and where the next slab's are.
-    uint32_t po[4], xo[2], so[2];
-    const char *pn, *qn[4], *xn, *sn;
+    uint32_t po[2], xo, so;
+    const char *pn, *qn[2], *xn, *sn;
     int ck = 0;                                      // that slab
     auto enter = [&](const Tile &t) {
-        const int rb = t.q0 / 16 + 4 * w;
+        const int rb = t.q0 / 16 + 2 * w;
         const char *const codes = codes_of(X, t.e);
         pn = A.a.base, xn = (const char *)X.xs, sn = scales_of(X, t.e);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            po[i] = (uint32_t)L.src[64 * w + 16 * i + (l >> 2)] * (uint32_t)(A.K / 2) + 16 * ((l & 3) ^ ((l >> 4) & 3));
+        for (int i = 0; i < 2; ++i) {
+            po[i] = (uint32_t)L.src[32 * w + 16 * i + (l >> 2)] * (uint32_t)(A.K / 2) + 16 * ((l & 3) ^ ((l >> 4) & 3));
             qn[i] = codes + (size_t)(rb + i < blocks ? rb + i : blocks - 1) * slabs * 1024;
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            xo[i] = (uint32_t)L.src[64 * w + 32 * i + (l >> 1)] * (uint32_t)(A.K / 32) + 4 * (l & 1);
-            so[i] = (uint32_t)((rb + 2 * i + h < blocks ? rb + 2 * i + h : blocks - 1) * slabs) * 64 + 4 * b;
-        }
+        xo = (uint32_t)L.src[32 * w + (l >> 1)] * (uint32_t)(A.K / 32) + 4 * (l & 1);
+        so = (uint32_t)((rb + h < blocks ? rb + h : blocks - 1) * slabs) * 64 + 4 * b;
         ck = 0;
     };
-    char *const pl = L.p[0] + 64 * w * 64, *const ql = L.q[0] + 4 * w * 1024;
-    auto copy_some = [&](int place, auto n) {        // copy n of 8 of that slab
+    const uint32_t qo[2] = {16u * (l ^ ((2 * w) & 3)), 16u * (l ^ ((2 * w + 1) & 3))};
+    char *const pl = L.p[0] + 32 * w * 64, *const ql = L.q[0] + 2 * w * 1024;
+    auto copy_some = [&](int place, auto n) {        // copy n of 4 of that slab
         constexpr int i = decltype(n)::v;
-        if constexpr (i < 4) {
-            lds_dma16(scalar_base(pn) + here(po[i]), pl + place + 1024 * i);
-            if constexpr (i == 3) pn += 64;
-        } else {
-            lds_dma16(scalar_base(qn[i - 4]) + here(16 * (l ^ (i - 4))), ql + place + 1024 * (i - 4));
-            qn[i - 4] += 1024;
-            if constexpr (i == 7) ++ck;
+        if constexpr (i == 0) lds_dma16(scalar_base(pn) + here(po[0]), pl + place);
+        if constexpr (i == 1) lds_dma16(scalar_base(pn) + here(po[1]), pl + place + 1024);
+        if constexpr (i == 2) lds_dma16(scalar_base(qn[0]) + here(qo[0]), ql + place);
+        if constexpr (i == 3) {
+            lds_dma16(scalar_base(qn[1]) + here(qo[1]), ql + place + 1024);
+            pn += 64, qn[0] += 1024, qn[1] += 1024, ++ck;
         }
     };
     auto copy_slab = [&](int place) {
         copy_some(place, Const<0>{}), copy_some(place, Const<1>{}), copy_some(place, Const<2>{}), copy_some(place, Const<3>{});
-        copy_some(place, Const<4>{}), copy_some(place, Const<5>{}), copy_some(place, Const<6>{}), copy_some(place, Const<7>{});
     };
-    auto copy_scale = [&](int u, auto n) {           // copy n of 4 of the scales of the next pair
-        constexpr int i = decltype(n)::v;
-        if constexpr (i < 2) {
-            lds_dma4(scalar_base(xn) + here(xo[i]), &L.xs[u][64 * w + 32 * i][0]);
-            if constexpr (i == 1) xn += 8;
-        } else {
-            lds_dma4(scalar_base(sn) + here(so[i - 2]), L.qs[u][2 * w + i - 2]);
-            if constexpr (i == 3) sn += 128;
-        }
-    };
-    auto copy_scales = [&](int u) {
-        copy_scale(u, Const<0>{}), copy_scale(u, Const<1>{}), copy_scale(u, Const<2>{}), copy_scale(u, Const<3>{});
+    auto copy_scales = [&](int u) {                  // 2 copies
+        lds_dma4(scalar_base(xn) + here(xo), &L.xs[u][32 * w][0]);
+        lds_dma4(scalar_base(sn) + here(so), L.qs[u][w]);
+        xn += 8, sn += 128;
     };
 
     // this lane's places in LDS: x's two pieces of a slab, W's of tile j, and the scales
     const int key = (b >> 2) & 3;
     const char *P[2], *Q[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) P[i] = L.p[0] + (128 * wp + b) * 64 + 16 * ((2 * i + h) ^ key);
+    for (int i = 0; i < 2; ++i) P[i] = L.p[0] + (64 * wp + b) * 64 + 16 * ((2 * i + h) ^ key);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         Q[j] = L.q[0] + (8 * wq + (b >> 2)) * 1024 + 16 * (16 * h + 4 * (b & 3) + (j ^ key));
     const char *const S = L.qs[0][4 * wq + (b >> 3)] + 128 * ((b >> 2) & 1) + 16 * h + 4 * (b & 3);
-    const char *const XS = (const char *)L.xs[0][128 * wp + b];
+    const char *const XS = (const char *)L.xs[0][64 * wp + b];
 
     struct Frags {
-        u32x4 p[4][2], q[2][4];
-        uint32_t ps[4], qs[2];
+        u32x4 p[2][2], q[2][4];
     };
-    f32x16 acc[4][4];
-    // read n of 24 of the slab at `o` (slab s of pair v)
-    auto read = [&](Frags &f, int o, int v, auto slab, auto n) {
-        constexpr int i = decltype(n)::v, s = decltype(slab)::v;
-        if constexpr (i < 8) f.q[i / 4][i % 4] = *(const MOE_LDS u32x4 *)(Q[i % 4] + o + 512 * (i / 4));
-        else if constexpr (i < 16) f.p[(i - 8) / 2][i % 2] = *(const MOE_LDS u32x4 *)(P[i % 2] + o + 2048 * ((i - 8) / 2));
-        else if constexpr (i < 20) f.ps[i - 16] = *(const MOE_LDS uint32_t *)(XS + v * (int)sizeof(L.xs[0]) + 256 * (i - 16) + 4 * s) >> (8 * h);
-        else if constexpr (i < 22) f.qs[i - 20] = *(const MOE_LDS uint32_t *)(S + v * (int)sizeof(L.qs[0]) + 64 * s + 32 * (i - 20));
+    struct Scales {
+        uint32_t p[2][2], q[2][2];       // by slab of the pair
     };
+    f32x16 acc[2][4];
     enter(cur);
     copy_scales(0), copy_slab(0), copy_slab(kBPair / 2);
-    copy_scales(1), copy_slab(kBPair), copy_slab(kBPair + kBPair / 2);
+    copy_scales(1), copy_slab(kBPair);
+    wait_copies<10>();
+    bare_barrier();
+    if (wp >= 2) bare_barrier();
+
     int u = 0, db = 0, stores = 0;       // pair in LDS, tile's place in `to`, stores before this tile
-    // the next tile, and the indices of its rows
-    auto look_ahead = [&]() {
-        if (n + 1 >= tiles) return;
-        if ((n + 1) % kBList == 0) {
-            if (w == 0) look_up(n + 1);
-            wait_lds();
-            bare_barrier();
+    bool work0, work1;
+    auto read = [&](Frags &f, int o) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f.q[kk][j] = *(const MOE_LDS u32x4 *)(Q[j] + o + 512 * kk);
+            f.p[0][kk] = *(const MOE_LDS u32x4 *)(P[kk] + o);
+            f.p[1][kk] = *(const MOE_LDS u32x4 *)(P[kk] + o + 2048);
         }
-        next = listed(n + 1);
+    };
+    auto multiply = [&](const Frags &f, const Scales &c, auto slab, auto copy) {
+        constexpr int s = decltype(slab)::v;
+        auto between = [&](auto n) {
+            __builtin_amdgcn_sched_barrier(0);
+            copy(n);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        wait_lds();
+        phase_barrier();
+        __builtin_amdgcn_s_setprio(1);
+#define MOE_MX(i, kk, j) acc[i][j] = mfma32<2 * kk, j>(f.p[i][kk], f.q[kk][j], acc[i][j], c.p[s][i], c.q[s][kk]);
+#define MOE_MX2(i, kk, j) MOE_MX(i, kk, j) MOE_MX(i, kk, j + 1)
+        if (work0) {
+            MOE_MX2(0, 0, 0)
+            between(Const<0>{});
+            MOE_MX2(0, 0, 2)
+            between(Const<1>{});
+            MOE_MX2(0, 1, 0)
+            between(Const<2>{});
+            MOE_MX2(0, 1, 2)
+            between(Const<3>{});
+        } else {
+            copy(Const<0>{}), copy(Const<1>{}), copy(Const<2>{}), copy(Const<3>{});
+        }
+        if (work1) {
+            MOE_MX2(1, 0, 0) MOE_MX2(1, 0, 2) MOE_MX2(1, 1, 0) MOE_MX2(1, 1, 2)
+        }
+#undef MOE_MX2
+#undef MOE_MX
+        __builtin_amdgcn_s_setprio(0);
+        phase_barrier();
+    };
+    auto pair = [&](int k) {
+        typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+        // the pair's first slab, and its scales
+        Frags f0, f1;
+        Scales c;
+        read(f0, u * kBPair);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+                c.q[s][kk] = *(const MOE_LDS uint32_t *)(S + u * (int)sizeof(L.qs[0]) + 64 * s + 32 * kk);
+        const u32x2 x0 = *(const MOE_LDS u32x2 *)(XS + u * (int)sizeof(L.xs[0]));
+        const u32x2 x1 = *(const MOE_LDS u32x2 *)(XS + u * (int)sizeof(L.xs[0]) + 256);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) c.p[s][0] = x0[s] >> (8 * h), c.p[s][1] = x1[s] >> (8 * h);
+        // Slab k + 1 has to be there: of what is in flight, the copies of slab k + 2 with
+        // its scales (6) and the last tile's stores are younger. Slab k + 3 goes into the
+        // place that slab k - 1, read by all, had.
+        wait_some<6>(k == 0 ? stores : 0);
+        const int p3 = (u ^ 1) * kBPair + kBPair / 2, p4 = u * kBPair;
+        multiply(f0, c, Const<0>{}, [&](auto n) { copy_some(p3, n); });
+
+        // its second slab
+        read(f1, u * kBPair + kBPair / 2);
+        if (k == 0 && n + 1 < tiles) {
+            // the next tile, and the indices of its rows
+            next = listed(n + 1);
+            const int i = index_at(next, 64 * (w & 3) + l);
+            if (w < 4 ? A.a.idx != nullptr : A.out_rows != nullptr)
+                lds_dma4((w < 4 ? A.a.idx : A.out_rows) + i, (w < 4 ? L.raw : L.rawo) + 64 * (w & 3));
+        }
+        if (k == 2 && n + 1 < tiles) {
+            const int row = 32 * w + b;      // (this wavefront's copies read these alone)
+            note_row(next, db ^ 1, row, L.raw[row], L.rawo[row]);
+        }
+        if (ck == slabs) {
+            // on to the next tile; behind the last one, its last pair once more
+            if (n + 1 < tiles) enter(next);
+            else pn -= 128, qn[0] -= 2048, qn[1] -= 2048, xn -= 8, sn -= 128, ck -= 2;
+        }
+        wait_some<4>(k == 0 ? stores : 0);
+        multiply(f1, c, Const<1>{}, [&](auto n) {
+            if constexpr (decltype(n)::v == 0) copy_scales(u);
+            copy_some(p4, n);
+        });
+        u ^= 1;
+    };
+    for (;;) {
+        work0 = wp < cur.units, work1 = 4 + wp < cur.units;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+        for (int k = 0; k < slabs; k += 2) pair(k);
+        // A lane stores four columns of 16 rows of each unit.
+        const int q = cur.q0 + 128 * wq + 4 * b, bytes = A.out_f32 ? 4 : 2;
+        const uint32_t col = q < A.N ? (uint32_t)(q * bytes) : kBBytes;
+        const buf_rsrc out = make_rsrc(A.out, (uint32_t)A.out_n * ldo);
+        stores = (work0 ? 16 : 0) + (work1 ? 16 : 0);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int row = 64 * w + l, at = index_at(next, row);
-            if (i == 0 ? A.a.idx != nullptr : A.out_rows != nullptr)
-                lds_dma4((i == 0 ? A.a.idx : A.out_rows) + at, (i == 0 ? L.raw : L.rawo) + 64 * w);
-        }
-    };
-    Frags f[2];
-    wait_copies<20>();
-    bare_barrier();
-    look_ahead();
-    auto read_all = [&](Frags &f) {
-        auto three = [&](auto n) {
-            constexpr int i = 3 * decltype(n)::v;
-            read(f, 0, 0, Const<0>{}, Const<i>{}), read(f, 0, 0, Const<0>{}, Const<i + 1>{}), read(f, 0, 0, Const<0>{}, Const<i + 2>{});
-        };
-        three(Const<0>{}), three(Const<1>{}), three(Const<2>{}), three(Const<3>{}), three(Const<4>{}), three(Const<5>{}), three(Const<6>{}), three(Const<7>{});
-    };
-    read_all(f[0]);
-    wait_lds();
-    bare_barrier();
-    for (;;) {
-        const int ni = (cur.units - wp + 1) / 2;     // units of this wavefront
-        // Slab k's products, while slab k + 1's fragments come out of LDS and slab k + 4
-        // goes into the place of slab k (whose fragments all wavefronts have). The first
-        // slab's start from zero.
-        auto step = [&](auto slab, auto fresh, int from, int to) {
-            constexpr int s = decltype(slab)::v;
-            constexpr bool z = decltype(fresh)::v != 0;
-            const f32x16 none = {};
-            Frags &c = f[s], &n = f[s ^ 1];
-            const int v = s ? u ^ 1 : u;
-            auto act = [&](auto slot) {
-                constexpr int i = decltype(slot)::v;
-                __builtin_amdgcn_sched_barrier(0);
-                read(n, from, v, Const<s ^ 1>{}, Const<3 * i>{});
-                read(n, from, v, Const<s ^ 1>{}, Const<3 * i + 1>{});
-                read(n, from, v, Const<s ^ 1>{}, Const<3 * i + 2>{});
-                if constexpr (s == 1 && i < 4) copy_scale(u, Const<i>{});
-                if constexpr (s == 0) copy_some(to, Const<i>{});
-                if constexpr (s == 1 && i >= 4) copy_some(to, Const<2 * (i - 4)>{}), copy_some(to, Const<2 * (i - 4) + 1>{});
-                __builtin_amdgcn_sched_barrier(0);
-            };
-#define MOE_MX(i, kk, j) acc[i][j] = mfma32<2 * kk, j>(c.p[i][kk], c.q[kk][j], z && kk == 0 ? none : acc[i][j], c.ps[i], c.qs[kk]);
-#define MOE_MX4(i, kk) MOE_MX(i, kk, 0) MOE_MX(i, kk, 1) MOE_MX(i, kk, 2) MOE_MX(i, kk, 3)
-#define MOE_UNIT(i)                    \
-    if (z || i < ni) { MOE_MX4(i, 0) }      \
-    act(Const<2 * i>{});               \
-    if (i < ni) { MOE_MX4(i, 1) }      \
-    act(Const<2 * i + 1>{});
-            MOE_UNIT(0)
-            MOE_UNIT(1)
-            MOE_UNIT(2)
-            MOE_UNIT(3)
-#undef MOE_UNIT
-#undef MOE_MX4
-#undef MOE_MX
-        };
-        for (int k = 0; k < slabs; k += 2) {
-            if (k == 2 && n + 1 < tiles) note_row(next, db ^ 1, L.raw[threadIdx.x], L.rawo[threadIdx.x]);
-            if (ck == slabs) {
-                // on to the next tile; behind the last one, its last pair once more
-                if (n + 1 < tiles) {
-                    enter(next);
-                } else {
-                    pn -= 128, xn -= 8, sn -= 128, ck -= 2;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) qn[i] -= 2048;
-                }
-            }
-            if (k == 0) step(Const<0>{}, Const<1>{}, u * kBPair + kBPair / 2, u * kBPair);
-            else step(Const<0>{}, Const<0>{}, u * kBPair + kBPair / 2, u * kBPair);
-            // slab k + 2 and its scales are there: slabs k + 3 and k + 4 are younger, and the
-            // last tile's stores
-            wait_some<16>(k == 0 ? stores : 0);
-            wait_lds();
-            phase_barrier();
-            step(Const<1>{}, Const<0>{}, (u ^ 1) * kBPair, u * kBPair + kBPair / 2);
-            // slab k + 3: slabs k + 4 and k + 5 and the scales of both are younger (the next
-            // tile's indices are older than the stores)
-            wait_some<20>(k == 0 ? stores : 0);
-            wait_lds();
-            phase_barrier();
-            u ^= 1;
-        }
-        // A lane stores four columns of 16 rows of each unit.
-        const int q = cur.q0 + 128 * wq + 4 * b, bytes = A.out_f32 ? 4 : 2, last = db;
-        const uint32_t col = q < A.N ? (uint32_t)(q * bytes) : kBBytes;
-        const bool done = n + 1 >= tiles;
-        if (!done) {
-            db ^= 1, ++n, cur = next;
-            look_ahead();
-        }
-        const buf_rsrc out = make_rsrc(A.out, (uint32_t)A.out_n * ldo);
-        stores = 16 * ni;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i >= ni) continue;
+            if (4 * i + wp >= cur.units) continue;
             typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));     // (as in store_rows)
+            for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[i][j]));
             u32x4 at[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) at[c] = *(const MOE_LDS u32x4 *)&L.to[last][128 * wp + 32 * i + 8 * c + 4 * h];
+            for (int c = 0; c < 4; ++c) at[c] = *(const MOE_LDS u32x4 *)&L.to[db][64 * wp + 32 * i + 8 * c + 4 * h];
             if (A.out_f32) {
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
@@ -572,9 +559,13 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
                         at[v >> 2][v & 3] + col, 0, kBufNt);
             }
         }
-        if (done) break;
+        if (n + 1 >= tiles) break;
+        db ^= 1, ++n, cur = next;
+        // (all have read the list's last tile; two barriers come before the next is read)
+        if ((n + 1) % kBList == 0 && w == 0) look_up(n + 1);
     }
     wait_copies<0>();       // (copies that nothing reads: LDS is another workgroup's next)
+    if (wp < 2) bare_barrier();
 }
 
 // -------------------------------------------------------- a handful of rows --
@@ -729,13 +720,13 @@ static long tiles_of(int R, int N, int E, int p, int q) {
 
 // Which kernel, from the sizes alone. us of a call with uneven routing (popularity
 // e^(N(0,1)/4.5 to 2)), streaming / 128 x 256 / 256 x 256 tiles:
-//   128 experts of 1536 x 2048, 8 a token: 1, 2, 4, 16, 64, 256, 1024, 4096 tokens
-//     7.3/11.1/14.2  10.0/13.5/15.3  14.9/14.4/15.8  33.5/27.8/30.5  52/46.3/47.5
-//     90/48.4/48.5  -/63/57  -/107/106
+//   128 experts of 1536 x 2048, 8 a token: 1, 2, 4, 16, 64, 256, 1024, 4096, 8192 tokens
+//     7.0/11.2/13.8  10.3/13.7/14.9  14.7/14.7/16.4  33.7/29.6/30.0  51.0/46.6/45.8
+//     -/48.6/47.2  -/62/54  -/116/101  -/196/160
 //   256 experts of 4096 x 4096, 6 a token: 1, 2, 8, 32, 256 tokens
-//     15.9/17.7/21.9  25/21.9/23.6  80/80/78  235/211/192  592/338/331
-//   one of 4096 x 4096: 1, 16, 64, 512, 4001 rows
-//     8.8/11.6/20.4  10.1/12.8/20.5  -/16.6/21.2  -/28.5/29.9  -/51/43
+//     16.2/17.6/20.4  25.2/21.6/23.7  75/76/75  -/198/181  -/337/328
+//   one of 4096 x 4096: 1, 16, 64, 512, 4001 rows; one of 8192 x 8192, 8192 rows
+//     8.7/12.8/18.6  10.1/12.8/18.6  20.1/16.5/19.4  -/28.6/30.2  -/50/41  -/337/257
 // The streaming kernel, which needs no second launch for a sum in parts, wins with few
 // tiles; large ones win where rows fill them or the tiles are many.
 static bool mxfp4_streams(int R, int N, int E) {
