@@ -573,7 +573,7 @@ int moe_quant_mxfp4_matrices(const uint16_t *w_bf16, int E, int N, int K, uint8_
  * or a table's MOE_W_MXFP4 blobs. Both indices of x (codes and scales) go through
  * x_rows. N a multiple of 16, K of 128; x's scales 4-byte aligned. A NaN scale
  * makes every result that it enters NaN.
- * The matrix core adds 64 (16 rows per expert and less: 128) columns' products and
+ * The matrix core adds 64 or 128 columns' products and
  * the sum so far with an error below 2^-22 of their magnitudes' sum; everything
  * else as for moe_grouped_gemm (workspace kind MOE_GEMM_MXFP4). */
 int moe_grouped_gemm_mxfp4(const uint8_t *x_e2m1, const uint8_t *x_e8m0, const int32_t *x_rows,
@@ -601,8 +601,8 @@ int moe_rms_norm(const uint16_t *x_bf16, const uint16_t *residual_bf16, const ui
                  uint8_t *q, void *q_scale, void *stream);
 
 /* moe_rms_norm_grad -- gradients of y = x / sqrt(mean(x^2) + eps) * weight for dy
- * [R][H]: dx bf16, to which dtotal (optional, the gradient that comes to x past
- * the norm; dx may be the same rows) is added, and dw [H] fp32 (optional;
+ * [R][H]: dx bf16 (it may be dy's or dtotal's rows), to which dtotal (optional, the
+ * gradient that comes to x past the norm) is added, and dw [H] fp32 (optional;
  * accumulate != 0 adds to it, zeros for R = 0 otherwise). With x = total, dx is
  * the gradient of the residual and of what was added to it alike. H up to 16384.
  * ws (16-byte aligned): with dw, at least moe_rms_norm_grad_workspace's bytes;
@@ -614,7 +614,8 @@ int moe_rms_norm_grad(const uint16_t *x_bf16, const uint16_t *weight_bf16, const
 
 /* moe_dispatch -- tokens to the rows of their pairs: out[pair_row[t*k + j]] =
  * x[t], x [T][H], out [out_n][H] bf16 (pair_row as moe_permute writes it). A pair
- * whose row is outside out (-1, say) is left out; rows of out that no pair has are
+ * whose row is outside out (-1, say) is left out (out may be NULL for out_n = 0, as y
+ * may below for y_n = 0); rows of out that no pair has are
  * left as they are; rows are distinct. Its gradient is moe_combine_rows without w. */
 int moe_dispatch(const uint16_t *x_bf16, const int32_t *pair_row, int T, int k, int H,
                  uint16_t *out_bf16, int out_n, void *stream);

@@ -491,7 +491,8 @@ extern "C" int moe_dispatch(const uint16_t *x_bf16, const int32_t *pair_row, int
                             uint16_t *out_bf16, int out_n, void *stream) {
     if (!moves_ok(T, k, H) || out_n < 0) return MOE_EINVAL;
     if (T == 0) return MOE_OK;
-    if (!al16(x_bf16) || !pair_row || !al16(out_bf16)) return MOE_EINVAL;
+    if (!al16(x_bf16) || !pair_row || (out_n && !al16(out_bf16))) return MOE_EINVAL;
+    if (out_n == 0) return MOE_OK;
     const long blocks = ((long)T * (H / 8) + 255) / 256;
     if (!blocks_ok(blocks)) return MOE_EINVAL;
     MOE_LAUNCH(K_DISPATCH, dispatch_kernel, blocks_of(blocks), dim3(256), 0, (hipStream_t)stream, x_bf16,
@@ -504,7 +505,7 @@ extern "C" int moe_combine_rows(const void *y, int y_is_fp32, int y_n, const int
                                 uint16_t *out_bf16, void *stream) {
     if (!moves_ok(T, k, H) || y_n < 0) return MOE_EINVAL;
     if (T == 0) return MOE_OK;
-    if (!al16(y) || !pair_row || ((uintptr_t)add_bf16 & 15) || !al16(out_bf16)) return MOE_EINVAL;
+    if ((y_n && !al16(y)) || !pair_row || ((uintptr_t)add_bf16 & 15) || !al16(out_bf16)) return MOE_EINVAL;
     const long blocks = ((long)T * (H / 8) + 63) / 64;
     if (!blocks_ok(blocks)) return MOE_EINVAL;
     hipStream_t s = (hipStream_t)stream;
@@ -528,8 +529,8 @@ extern "C" int moe_combine_rows_grad(const uint16_t *dout_bf16, const uint16_t *
                                      uint16_t *dy_bf16, float *dw, void *stream) {
     if (!moves_ok(T, k, H) || y_n < 0) return MOE_EINVAL;
     if (T == 0) return MOE_OK;
-    if (!al16(dout_bf16) || !pair_row || ((uintptr_t)dy_bf16 & 15) || (!dy_bf16 && !dw)) return MOE_EINVAL;
-    if (dw && !al16(y_bf16)) return MOE_EINVAL;
+    if (!al16(dout_bf16) || !pair_row || ((uintptr_t)dy_bf16 & 15) || (!dy_bf16 && !dw && y_n)) return MOE_EINVAL;
+    if (dw && y_n && !al16(y_bf16)) return MOE_EINVAL;
     const long pairs = (long)T * k;
     MOE_LAUNCH(K_COMBINE_ROWS_GRAD, combine_rows_grad_kernel, blocks_of((pairs + 3) / 4), dim3(256), 0,
                (hipStream_t)stream, dout_bf16, y_bf16, y_n, pair_row, w, pairs, k, divisor(k), H, dy_bf16,

@@ -104,8 +104,8 @@ def _grad_workspace(R, H, dev, stream, ws):
 def rms_norm_grad(x, weight, dy, eps=1e-6, dtotal=None, *, dx=None, dw=None, accumulate=False,
                   ws=None, stream=None):
     """Gradients of y = x / sqrt(mean(x^2) + eps) * weight for dy [R, H]: (dx bf16, dw
-    fp32 [H]). ``dtotal`` (bf16 [R, H], optional; dx may be the same tensor) is the
-    gradient that comes to x past the norm and is added to dx; with x the rows t of
+    fp32 [H]). ``dtotal`` (bf16 [R, H], optional) is the gradient that comes
+    to x past the norm and is added to dx, which may be dy or dtotal itself; with x the rows t of
     ``rms_norm``, dx is the gradient of x and of residual alike. ``accumulate`` adds to
     ``dw``. H is at most 16384. ``ws`` (uint8): as ``products.py`` has it, of
     ``_lib.moe_rms_norm_grad_workspace``'s bytes; needed with a stream handle."""
@@ -138,9 +138,10 @@ def _pairs(pair_row, dev):
 
 
 def dispatch(x, pair_row, *, out=None, stream=None):
-    """Tokens to sorted order: out[pair_row[t, j]] = x[t] of x bf16 [T, H]. ``out``
-    [n, H] ([T * k, H] where it is not given) keeps the rows that no pair has; the rows
-    of the pairs are distinct. The gradient is ``combine`` without weights."""
+    """Tokens to sorted order: out[pair_row[t, j]] = x[t] of x bf16 [T, H]. Rows of
+    ``out`` [n, H] that no pair has are left as they are (anything, in an out that is
+    not given, [T * k, H]); the rows of the pairs are distinct. The gradient is
+    ``combine`` without weights."""
     dev = _matrix(x, "x", _BF16).get_device()
     _no_history(x)
     pr, T, k = _pairs(pair_row, dev)

@@ -403,6 +403,23 @@ def test_same_bits_by_handle_stream_and_graph(path):
         assert torch.equal(out, eager)
 
 
+@pytest.mark.parametrize("path", list(PATHS))
+def test_two_products_at_once(path):
+    """On two streams, the sums' workspaces their own: each has its bits."""
+    counts, N, K = PATHS[path]
+    R, off = sum(counts), _offsets(counts)
+    sides, sets = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for i in range(2):
+        _, byte, scale, w = _case(counts, N, K, 96 + i)
+        sets.append((byte(R, K // 2), scale(R, K // 32), *kernel_order(*w), off))
+    want = [P.grouped_matmul_mxfp4(*s) for s in sets]
+    torch.cuda.synchronize()
+    got = [[P.grouped_matmul_mxfp4(*sets[i], stream=sides[i]) for i in range(2)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for pair in got:
+        assert torch.equal(pair[0], want[0]) and torch.equal(pair[1], want[1])
+
+
 def test_cut_sum_without_its_workspace_runs_whole():
     counts, N, K = PATHS["cut"]
     _, byte, scale, (wq, ws) = _case(counts, N, K, 95)

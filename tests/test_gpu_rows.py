@@ -347,6 +347,94 @@ def test_moves_beyond_4_gib():
     assert torch.equal(dy[rows.long()], (w[:, :, None] * x.float()[:, None]).to(torch.bfloat16))
 
 
+def test_moves_without_sorted_rows():
+    """No sorted rows at all: every pair's row is outside them."""
+    g = _gen(14)
+    T, k, H = 5, 3, 72
+    rows = torch.randint(-1, 40, (T, k), device=DEV, generator=g, dtype=torch.int32)
+    x, w = _randn(g, T, H), torch.rand(T, k, device=DEV, generator=g)
+    none = torch.empty(0, H, device=DEV, dtype=torch.bfloat16)
+    assert W.dispatch(x, rows, out=none) is none
+    assert not bool(W.combine(none, rows, w).any())
+    assert torch.equal(W.combine(none.float(), rows, w, x), x)
+    dy, dw = W.combine_grad(x, none, rows, w, dw=torch.ones(T, k, device=DEV))
+    assert dy.shape == (0, H) and not bool(dw.any())
+
+
+@pytest.mark.parametrize("R,H", [((1 << 25) + 9, 8), ((1 << 20) + 3, 4104)])
+def test_norm_and_gradient_over_many_rows(R, H):
+    """More workgroups than a launch has along x, and values past 2^32."""
+    g = _gen(15)
+    x, w = torch.zeros(R, H, device=DEV, dtype=torch.bfloat16), _randn(g, H)
+    last, dlast = _stream_rows(g, 70, H), _randn(g, 70, H)
+    x[-70:] = last
+    y = W.rms_norm(x, w, EPS)
+    assert torch.equal(y[-70:], W.rms_norm(last, w, EPS)) and not bool(y[-200:-70].any())
+    del y
+    q, s = W.rms_norm_fp8(x, w, EPS)
+    q2, s2 = W.rms_norm_fp8(last, w, EPS)
+    assert torch.equal(q[-70:].view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s[-70:], s2)
+    del q, s
+    dy = torch.zeros_like(x)
+    dy[-70:] = dlast
+    dx, dw = W.rms_norm_grad(x, w, dy, EPS, dx=dy)
+    dx2, _ = W.rms_norm_grad(last, w, dlast, EPS)
+    assert torch.equal(dx[-70:], dx2) and not bool(dx[-200:-70].any())
+    n = last.double() / torch.sqrt((last.double() ** 2).mean(1, keepdim=True) + EPS)
+    terms = dlast.double() * n
+    b = (_near(H) + (70 + 64) * 2.0 ** -24) * terms.abs().sum(0)      # (the other rows add zeros)
+    _within(dw, terms.sum(0), b, "dw")
+
+
+def test_moves_of_many_pairs():
+    """Units past 2^31: 34 GB of tokens, whose pairs have the few rows there are."""
+    T, H = (1 << 28) + 3, 64
+    g = _gen(16)
+    rows = torch.full((T, 1), -1, device=DEV, dtype=torch.int32)
+    at = torch.tensor([0, 1, (1 << 28) - 1, 1 << 28, T - 1], device=DEV)
+    rows[at, 0] = torch.arange(5, device=DEV, dtype=torch.int32)
+    y = _randn(g, 5, H)
+    out = W.combine(y, rows)
+    assert torch.equal(out[at], y)
+    assert not bool(out[2:2000].any()) and not bool(out[-2000:-4].any())
+    back = W.dispatch(out, rows, out=torch.zeros_like(y))
+    assert torch.equal(back, y)
+    w = torch.full((T, 1), 2.0, device=DEV)
+    dy, dw = W.combine_grad(out, y, rows, w, dy=torch.zeros_like(y))
+    assert torch.equal(dy, 2 * y)
+    ref = (y.double() ** 2).sum(1)
+    _within(dw[at, 0], ref, (H / 64 + 8) * 2.0 ** -24 * ref, "dw")
+    assert not bool(dw[-2000:-4].any())
+
+
+def test_two_calls_at_once():
+    """On two streams, each call with workspaces of its own: each has its bits."""
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    sets = []
+    for i in range(2):
+        g = _gen(17 + i)
+        rows, _ = _pair_rows(g, 300, 8, 2400)
+        sets.append((_stream_rows(g, 300, 2048), _randn(g, 2048), _randn(g, 300, 2048), rows,
+                     torch.rand(300, 8, device=DEV, generator=g)))
+
+    def run(i, stream):
+        x, w, dy, rows, f = sets[i]
+        y = W.rms_norm(x, w, EPS, stream=stream)
+        out = W.combine(W.dispatch(y, rows, stream=stream), rows, f, x, stream=stream)
+        return (y, out, *W.rms_norm_grad(x, w, dy, EPS, out, stream=stream))
+
+    want = [run(i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            got[i].append(run(i, sides[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for one in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(one, want[i]))
+
+
 def test_moves_in_a_graph_and_on_a_stream():
     T, k, H = 50, 4, 1024
     g = _gen(11)

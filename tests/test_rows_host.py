@@ -100,6 +100,7 @@ def test_moves_reject_bad_arguments(lib):
                dict(H=60), dict(n=-1), dict(T=2 ** 30, k=2), dict(H=0)):
         assert dispatch(**kw) == bad, kw
     assert dispatch(T=0, x=None, out=None) == ok
+    assert dispatch(out=None, n=0) == ok             # (nothing to write)
 
     def combine(y=D, f32=0, n=8, rows=D, w=D, add=None, T=4, k=2, H=64, out=D):
         return L.moe_combine_rows(y, f32, n, rows, w, add, T, k, H, out, None)
@@ -108,6 +109,7 @@ def test_moves_reject_bad_arguments(lib):
                dict(H=60), dict(n=-1), dict(T=2 ** 30, k=2)):
         assert combine(**kw) == bad, kw
     assert combine(T=0, y=None, out=None) == ok
+    assert combine(y=None, n=0, out=None) == bad
 
     def grad(dout=D, y=D, n=8, rows=D, w=D, T=4, k=2, H=64, dy=D, dw=D):
         return L.moe_combine_rows_grad(dout, y, n, rows, w, T, k, H, dy, dw, None)
