@@ -102,10 +102,12 @@ __global__ __launch_bounds__(kXThreads, 2) void mxfp4_tile_kernel(MxArgs X) {
     const size_t ldx = (size_t)A.K / 2, lds = (size_t)A.K / 32;
     total_tiles<kXThreads>(A, kXP, L.base, L.wsum);
     const int ns = A.slices, total = L.base[A.E] * tq * ns;
-    const int nx = gridDim.x >= 8 ? 8 : 1;      // workgroup b runs on XCD b % 8
-    const int xcd = blockIdx.x % nx, per = ((int)gridDim.x - xcd + nx - 1) / nx;
-    const int t0 = (int)((long)total * xcd / nx), t1 = (int)((long)total * (xcd + 1) / nx);
-    for (int si = t0 + (int)blockIdx.x / nx; si < t1; si += per) {
+    // workgroup b runs on XCD b % 8 (shifts: with divisions of 64 bits a
+    // workgroup starts 1% of a small call later)
+    const int lx = gridDim.x >= 8 ? 3 : 0;
+    const int xcd = blockIdx.x & ((1 << lx) - 1), per = ((int)gridDim.x - xcd + (1 << lx) - 1) >> lx;
+    const int t0 = (int)((long)total * xcd >> lx), t1 = (int)((long)total * (xcd + 1) >> lx);
+    for (int si = t0 + ((int)blockIdx.x >> lx); si < t1; si += per) {
         const int ti = ns > 1 ? si / ns : si, slice = si - ti * ns;     // tile, part of its sum
         const int e = expert_of(L.base, A.E, tq, ti);
         const int mp = __builtin_amdgcn_readfirstlane(L.base[e + 1] - L.base[e]);
@@ -118,7 +120,7 @@ __global__ __launch_bounds__(kXThreads, 2) void mxfp4_tile_kernel(MxArgs X) {
         units = units < 4 ? units : 4;
         place_of(li, mp, tq, p0, q0);
         p0 *= 32 * units, q0 *= kXQ;
-        const int kb = (int)((long)slabs * slice / ns), ke = (int)((long)slabs * (slice + 1) / ns);
+        const int kb = slabs * slice / ns, ke = slabs * (slice + 1) / ns;      // (2^13 slabs at most, 16 parts)
 
         __syncthreads();   // the last tile's readers of L are done
         if (t < kXP) {
@@ -235,10 +237,14 @@ __global__ __launch_bounds__(kXThreads, 2) void mxfp4_tile_kernel(MxArgs X) {
 // that reads, waits or stores leaves its SIMD idle: 8192 rows of 8192 x 8192 take
 // 284 us, 257 here.)
 //
-// What bounds it: matrix instructions alone reach 6.5 PFLOP/s on random codes (the
-// power limit lowers the clock; on zeros 9.6). One expert of 8192 x 8192 reaches 4.3;
-// gate/up of 8192 tokens of 128 experts (1536 x 2048, 412 GFLOP, 201 MB of results)
-// 2.6: there the compute units store together, about 40 of its 160 us.
+// What bounds it: power. Matrix instructions alone reach 6.5 PFLOP/s on random codes
+// (the limit lowers the clock; on zeros 9.6). One expert of 8192 x 8192 reaches 4.3 at
+// 1.6 of 2.4 GHz, the matrix cores 64% busy; one of 4096 x 4096 (4001 rows) 3.2 at 1.5
+// GHz, where a fifth of the cycles pass before a workgroup's first slab is there
+// (12 thousand of 62: offsets, indices and rows one after another); gate/up of 8192
+// tokens of 128 experts (1536 x 2048, 412 GFLOP, 201 MB of results) 2.6 at 1.8 GHz,
+// where 40 of 160 us go by while the compute units store together. A slab takes 1500
+// cycles of which 1024 multiply.
 //
 // LDS holds four slabs, two pairs. The copies run three slabs ahead, and on into the
 // next tile, whose rows are looked up during this one's first slabs: only a workgroup's
@@ -291,19 +297,19 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
     const int tq = (A.N + kBT - 1) / kBT, slabs = A.K / 128, blocks = A.N / 16;
     total_tiles<kBThreads>(A, kBT, L.base, L.wsum);
     const int total = L.base[A.E] * tq;
-    const int nx = gridDim.x >= 8 ? 8 : 1;      // workgroup b runs on XCD b % 8
-    const int xcd = blockIdx.x % nx, per = ((int)gridDim.x - xcd + nx - 1) / nx;
-    const int t0 = (int)((long)total * xcd / nx), t1 = (int)((long)total * (xcd + 1) / nx);
-    int si = t0 + (int)blockIdx.x / nx;
+    const int lx = gridDim.x >= 8 ? 3 : 0;      // workgroup b runs on XCD b % 8
+    const int xcd = blockIdx.x & ((1 << lx) - 1), per = ((int)gridDim.x - xcd + (1 << lx) - 1) >> lx;
+    const int t0 = (int)((long)total * xcd >> lx), t1 = (int)((long)total * (xcd + 1) >> lx);
+    int si = t0 + ((int)blockIdx.x >> lx);
     if (si >= t1) return;
 
     // The workgroups that have a tile less than others start later, by up to the time
     // of one (about 1000 cycles a slab): begun together, all tiles end together, and
     // each end's stores, 32 MB from the device, wait for HBM with nothing to multiply
     // (gate/up of 8192 tokens: 185 -> 171 us).
-    const int rank = blockIdx.x / nx, late = (t1 - t0) % per;
+    const int rank = blockIdx.x >> lx, late = (t1 - t0) % per;
     if (late > 0 && rank >= late)
-        for (int i = (int)((long)slabs * 12 * (rank - late) / (per - late)); i > 0; --i) __builtin_amdgcn_s_sleep(1);
+        for (int i = slabs * 12 * (rank - late) / (per - late); i > 0; --i) __builtin_amdgcn_s_sleep(1);
 
     using Tile = LargeTile;
     // the workgroup's tiles n, n + 1, ..., by one wavefront
