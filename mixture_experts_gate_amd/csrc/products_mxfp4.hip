@@ -52,7 +52,9 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, 
 // tile. A step is a slab; LDS holds three, two of them copied ahead. The middle sizes
 // run here: 64 tokens of 128 experts of 1536 x 2048 47 us (about 210 MB of W, 4.5
 // TB/s: HBM and the tiles' starts, of few slabs each), 512 rows of one of 4096 x 4096
-// 28 us (the sum in parts, and their join).
+// 28 us (the sum in parts, and their join). Alone on a compute unit a workgroup takes
+// 0.7 us a slab: its reads of LDS, matrix instructions and copies follow one another
+// (four or five slabs in LDS change nothing).
 //
 // Instruction 32x32x64 with x as A and W as B (16x16x128 has the same rate but
 // reads each operand twice as often): a lane (h, b) = (l / 32, l % 32) of result
@@ -738,7 +740,7 @@ static long tiles_of(int R, int N, int E, int p, int q) {
 //   256 experts of 4096 x 4096, 6 a token: 1, 2, 8, 32, 256 tokens
 //     16.2/17.6/20.4  25.2/21.6/23.7  75/76/75  -/198/181  -/337/328
 //   one of 4096 x 4096: 1, 16, 64, 512, 4001 rows; one of 8192 x 8192, 8192 rows
-//     8.7/12.8/18.6  10.1/12.8/18.6  20.1/16.5/19.4  -/28.6/30.2  -/50/41  -/337/257
+//     8.7/12.8/18.6  10.1/12.8/18.6  20.1/14.9/19.4  -/27.9/30.2  -/50/41  -/337/257
 // The streaming kernel, which needs no second launch for a sum in parts, wins with few
 // tiles; large ones win where rows fill them or the tiles are many.
 static bool mxfp4_streams(int R, int N, int E) {
@@ -753,13 +755,15 @@ static bool mxfp4_large(const ProductArgs &a) {
 }
 
 // Parts that the sum of a tile is cut into: where there are fewer tiles than compute
-// units, as many as give each one, of four slabs at least.
+// units, as many as give each one, of eight slabs at least. (4, 8, 16: 64 rows of one
+// expert of 4096 x 4096 16.4, 14.9, 17.4 us, 128 rows 23.8, 20.7, 22.4, 512 rows 28.1,
+// 27.9, 31.4, 500 of 1536 x 2048 19.5, 18.2, 18.0.)
 static int mxfp4_slices(int R, int N, int K, int E) {
     if (R == 0 || mxfp4_streams(R, N, E)) return 1;
     const long tiles = tiles_of(R, N, E, kXP, kXQ);
     long n = compute_units() / (tiles < 1 ? 1 : tiles);
     const long steps = K / 128;
-    n = n < steps / 4 ? n : steps / 4;
+    n = n < steps / 8 ? n : steps / 8;
     return n < 2 ? 1 : n > 16 ? 16 : (int)n;
 }
 
