@@ -47,14 +47,17 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, 
 }
 
 // ------------------------------------------------------------------ tiles --
-// 128 rows (p) x 256 n (q) a workgroup of four wavefronts, 64 x 128 each; two
+// 128 rows (p) x 256 n (q) a workgroup of eight wavefronts, 32 x 128 each; two
 // workgroups a compute unit, so that one multiplies while the other starts or ends a
-// tile. A step is a slab; LDS holds three, two of them copied ahead. The middle sizes
-// run here: 64 tokens of 128 experts of 1536 x 2048 47 us (about 210 MB of W, 4.5
-// TB/s: HBM and the tiles' starts, of few slabs each), 512 rows of one of 4096 x 4096
-// 28 us (the sum in parts, and their join). Alone on a compute unit a workgroup takes
-// 0.7 us a slab: its reads of LDS, matrix instructions and copies follow one another
-// (four or five slabs in LDS change nothing).
+// tile. A step is a slab; LDS holds three, two of them copied ahead. (With four
+// wavefronts of 64 x 128, whose reads of LDS are three fifths of these, nothing runs beside
+// a wavefront's reads where a workgroup is alone on its compute unit: 1024 rows of one
+// expert of 4096 x 4096 take 30.6 us, 27.0 here, 500 of 1536 x 2048 18.3 and 16.5; more
+// slabs in LDS change nothing.)
+//
+// The middle sizes run here: 64 tokens of 128 experts of 1536 x 2048 45.5 us (about 210
+// MB of W, 4.6 TB/s: HBM and the tiles' starts, of few slabs each), 512 rows of one of
+// 4096 x 4096 27 us (start, the sum in parts, and their join).
 //
 // Instruction 32x32x64 with x as A and W as B (16x16x128 has the same rate but
 // reads each operand twice as often): a lane (h, b) = (l / 32, l % 32) of result
@@ -62,10 +65,10 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, 
 // 4 b + j of the wavefront's 128, so that a lane holds four consecutive q of a row
 // and 32 lanes store 256 bytes of it. The same order puts the scales of the
 // four tiles into the four bytes of one register, which the instruction picks from.
-constexpr int kXThreads = 256;
+constexpr int kXThreads = 512;
 constexpr int kXP = 128, kXQ = 256;
 constexpr int kXS = 3;           // slabs in LDS
-constexpr int kXCopies = 8;      // copy instructions of a wavefront and slab
+constexpr int kXCopies = 4;      // copy instructions of a wavefront and slab
 
 // 32 rows of a wavefront's results, four columns from q, to the rows of out in `dst`.
 // (The results are pinned to their registers first: the compiler would keep them in the
@@ -96,7 +99,7 @@ struct TileLds {
     int wsum[kXThreads / kWave];
 };
 
-__global__ __launch_bounds__(kXThreads, 2) void mxfp4_tile_kernel(MxArgs X) {
+__global__ __launch_bounds__(kXThreads, 4) void mxfp4_tile_kernel(MxArgs X) {
     const ProductArgs &A = X.p;
     __shared__ TileLds L;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -129,8 +132,7 @@ __global__ __launch_bounds__(kXThreads, 2) void mxfp4_tile_kernel(MxArgs X) {
 
         __syncthreads();   // the last tile's readers of L are done
         if (t < kXP) {
-            // unit u is rows 32 (u / 2) of wavefront row u % 2
-            const int u = 2 * ((t >> 5) & 1) + (t >> 6), p = p0 + 32 * u + (t & 31);
+            const int u = t >> 5, p = p0 + t;      // (unit u is wavefront row u's)
             const bool in = u < units && p < cnt;
             const int i = lo + (in ? p : 0);
             const int s = source_row(A.a, i);
@@ -144,42 +146,39 @@ __global__ __launch_bounds__(kXThreads, 2) void mxfp4_tile_kernel(MxArgs X) {
         }
         __syncthreads();
 
-        // A wavefront copies 32 rows of x, 16 an instruction, and four blocks of W;
-        // blocks past the last one read it and are not stored.
-        const char *pp[2], *qb[4];
+        // A wavefront copies 16 rows of x and two blocks of W; blocks past the last one
+        // read it and are not stored.
+        const char *const pp =
+            A.a.base + (size_t)L.src[16 * w + (l >> 2)] * ldx + 16 * ((l & 3) ^ ((l >> 4) & 3));
+        const char *const codes = codes_of(X, e), *const scales = scales_of(X, e), *qb[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            pp[i] = A.a.base + (size_t)L.src[32 * w + 16 * i + (l >> 2)] * ldx + 16 * ((l & 3) ^ ((l >> 4) & 3));
-        const char *const codes = codes_of(X, e), *const scales = scales_of(X, e);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int rb = q0 / 16 + 4 * w + i;
+        for (int i = 0; i < 2; ++i) {
+            const int rb = q0 / 16 + 2 * w + i;
             qb[i] = codes + (size_t)(rb < blocks ? rb : blocks - 1) * slabs * 1024;
         }
-        const int sb = q0 / 16 + 4 * w + (l >> 4);
+        const int sb = q0 / 16 + 4 * (w & 3) + (l >> 4);
         const char *const qsp = scales + (size_t)(sb < blocks ? sb : blocks - 1) * slabs * 64 + 4 * (l & 15);
         const char *const xsp = (const char *)X.xs + (size_t)L.src[64 * (w & 1) + l] * lds;
         auto fetch = [&](int k, int st) {
+            lds_dma16(pp + (size_t)k * 64, L.p[st] + 16 * w * 64);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) lds_dma16(pp[i] + (size_t)k * 64, L.p[st] + (32 * w + 16 * i) * 64);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                lds_dma16(scalar_base(qb[i] + (size_t)k * 1024) + here(16 * (l ^ i)), L.q[st] + (4 * w + i) * 1024);
-            lds_dma4(qsp + (size_t)k * 64, L.qs[st] + 256 * w);
-            lds_dma4(xsp + (size_t)k * 4, &L.xs[st][64 * (w & 1)]);   // (by two wavefronts, so that all count alike)
+            for (int i = 0; i < 2; ++i)
+                lds_dma16(scalar_base(qb[i] + (size_t)k * 1024) + here(16 * (l ^ ((2 * w + i) & 3))),
+                          L.q[st] + (2 * w + i) * 1024);
+            // (a row's scales by two wavefronts, so that all count alike)
+            if (w < 4) lds_dma4(qsp + (size_t)k * 64, L.qs[st] + 256 * w);
+            else lds_dma4(xsp + (size_t)k * 4, &L.xs[st][64 * (w & 1)]);
         };
 
-        f32x16 acc[2][4];
+        f32x16 acc[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+            for (int v = 0; v < 16; ++v) acc[j][v] = 0.0f;
         if (kb < ke) fetch(kb, 0);
         if (kb + 1 < ke) fetch(kb + 1, 1);
         int st = 0;
-        const bool work0 = wp < units, work1 = 2 + wp < units;
+        const bool work = wp < units;
         for (int k = kb; k < ke; ++k) {
             // slab k is in LDS (the copies of the next one may be in flight), and slab
             // k - 1, whose place slab k + 2 takes, is read
@@ -188,48 +187,31 @@ __global__ __launch_bounds__(kXThreads, 2) void mxfp4_tile_kernel(MxArgs X) {
             wait_lds();
             bare_barrier();
             if (k + 2 < ke) fetch(k + 2, st == 0 ? 2 : st - 1);
-            if (work0) {
-                const char *const P = L.p[st] + (64 * wp + b) * 64, *const Q = L.q[st] + (8 * wq + (b >> 2)) * 1024;
+            if (work) {
+                const char *const P = L.p[st] + (32 * wp + b) * 64, *const Q = L.q[st] + (8 * wq + (b >> 2)) * 1024;
                 const char *const S = L.qs[st] + (8 * wq + (b >> 2)) * 64 + 16 * h + 4 * (b & 3);
                 const int key = (b >> 2) & 3;
-                u32x4 pf[2][2], qf[2][4];
-                uint32_t ps[2], qs[2];
+                u32x4 pf[2], qf[2][4];
+                uint32_t qs[2];
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     qs[kk] = *(const MOE_LDS uint32_t *)(S + 32 * kk);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         qf[kk][j] = *(const MOE_LDS u32x4 *)(Q + 16 * (32 * kk + 16 * h + 4 * (b & 3) + (j ^ key)));
-                    pf[0][kk] = *(const MOE_LDS u32x4 *)(P + 16 * ((2 * kk + h) ^ key));
+                    pf[kk] = *(const MOE_LDS u32x4 *)(P + 16 * ((2 * kk + h) ^ key));
                 }
-                ps[0] = L.xs[st][64 * wp + b] >> (8 * h);
-                if (work1) {
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk)
-                        pf[1][kk] = *(const MOE_LDS u32x4 *)(P + 32 * 64 + 16 * ((2 * kk + h) ^ key));
-                    ps[1] = L.xs[st][64 * wp + 32 + b] >> (8 * h);
-                }
-#define MOE_MX(i, kk)                                                                                \
-    acc[i][0] = mfma32<2 * kk, 0>(pf[i][kk], qf[kk][0], acc[i][0], ps[i], qs[kk]);                   \
-    acc[i][1] = mfma32<2 * kk, 1>(pf[i][kk], qf[kk][1], acc[i][1], ps[i], qs[kk]);                   \
-    acc[i][2] = mfma32<2 * kk, 2>(pf[i][kk], qf[kk][2], acc[i][2], ps[i], qs[kk]);                   \
-    acc[i][3] = mfma32<2 * kk, 3>(pf[i][kk], qf[kk][3], acc[i][3], ps[i], qs[kk]);
-                MOE_MX(0, 0)
-                MOE_MX(0, 1)
-                if (work1) {
-                    MOE_MX(1, 0)
-                    MOE_MX(1, 1)
-                }
+                const uint32_t ps = L.xs[st][32 * wp + b] >> (8 * h);
+#define MOE_MX(kk, j) acc[j] = mfma32<2 * kk, j>(pf[kk], qf[kk][j], acc[j], ps, qs[kk]);
+                MOE_MX(0, 0) MOE_MX(0, 1) MOE_MX(0, 2) MOE_MX(0, 3)
+                MOE_MX(1, 0) MOE_MX(1, 1) MOE_MX(1, 2) MOE_MX(1, 3)
 #undef MOE_MX
             }
             st = st == 2 ? 0 : st + 1;
         }
 
         char *const out = ns > 1 ? (char *)(A.part + (size_t)slice * A.R * A.N) : (char *)A.out;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (2 * i + wp < units)
-                store_rows(A, out, ns > 1 || A.out_f32, L.dst + 64 * wp + 32 * i, q0 + 128 * wq + 4 * b, h, acc[i]);
+        if (work) store_rows(A, out, ns > 1 || A.out_f32, L.dst + 32 * wp, q0 + 128 * wq + 4 * b, h, acc);
     }
 }
 
@@ -735,12 +717,13 @@ static long tiles_of(int R, int N, int E, int p, int q) {
 // Which kernel, from the sizes alone. us of a call with uneven routing (popularity
 // e^(N(0,1)/4.5 to 2)), streaming / 128 x 256 / 256 x 256 tiles:
 //   128 experts of 1536 x 2048, 8 a token: 1, 2, 4, 16, 64, 256, 1024, 4096, 8192 tokens
-//     7.0/11.2/13.8  10.3/13.7/14.9  14.7/14.7/16.4  33.7/29.6/30.0  51.0/46.6/45.8
-//     -/48.6/47.2  -/62/54  -/116/101  -/196/160
+//     7.3/12.3/13.3  10.3/13.8/14.3  14.7/15.1/15.6  33.7/28.3/29.2  51.0/45.5/45.0
+//     -/47.8/46.2  -/58/54  -/112/99  -/194/160
 //   256 experts of 4096 x 4096, 6 a token: 1, 2, 8, 32, 256 tokens
-//     16.2/17.6/20.4  25.2/21.6/23.7  75/76/75  -/198/181  -/337/328
-//   one of 4096 x 4096: 1, 16, 64, 512, 4001 rows; one of 8192 x 8192, 8192 rows
-//     8.7/12.8/18.6  10.1/12.8/18.6  20.1/14.9/19.4  -/27.9/30.2  -/50/41  -/337/257
+//     16.0/18.5/20.1  25.2/22.5/23.2  75/75/72  -/188/184  -/334/327
+//   one of 4096 x 4096: 1, 16, 64, 512, 1024, 4001 rows; one of 8192 x 8192, 8192 rows
+//     8.7/12.2/18.2  10.1/13.0/18.3  20.1/15.0/19.0  -/27.3/30.0  -/27.2/30.4  -/50/42
+//     -/346/257
 // The streaming kernel, which needs no second launch for a sum in parts, wins with few
 // tiles; large ones win where rows fill them or the tiles are many.
 static bool mxfp4_streams(int R, int N, int E) {
@@ -755,9 +738,9 @@ static bool mxfp4_large(const ProductArgs &a) {
 }
 
 // Parts that the sum of a tile is cut into: where there are fewer tiles than compute
-// units, as many as give each one, of eight slabs at least. (4, 8, 16: 64 rows of one
-// expert of 4096 x 4096 16.4, 14.9, 17.4 us, 128 rows 23.8, 20.7, 22.4, 512 rows 28.1,
-// 27.9, 31.4, 500 of 1536 x 2048 19.5, 18.2, 18.0.)
+// units, as many as give each one, of eight slabs at least. (4, 8, 16, with wavefronts of
+// 64 x 128: 64 rows of one expert of 4096 x 4096 16.4, 14.9, 17.4 us, 128 rows 23.8,
+// 20.7, 22.4, 512 rows 28.1, 27.9, 31.4, 500 of 1536 x 2048 19.5, 18.2, 18.0.)
 static int mxfp4_slices(int R, int N, int K, int E) {
     if (R == 0 || mxfp4_streams(R, N, E)) return 1;
     const long tiles = tiles_of(R, N, E, kXP, kXQ);
