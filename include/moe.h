@@ -584,8 +584,10 @@ int moe_grouped_gemm_mxfp4(const uint8_t *x_e2m1, const uint8_t *x_e8m0, const i
 
 /* ---------------------------------------------------------------------------
  * Rows before and after the experts. bf16 rows start 16-byte aligned, H is a
- * multiple of 8 up to 2^24, and sums are fp32 (squares past its range make
- * an infinite sum: values up to 2^51 are safe at every H).
+ * multiple of 8 up to 2^24, and sums are fp32; a row of the norm or of its
+ * gradient whose sums leave fp32's range is summed in 64 bits, so that finite rows
+ * of any size have their norm. (In the gradient, dy w stays below 2^127; products
+ * dy w x below 2^-126 are added to within 2^-149.)
  *
  * moe_rms_norm -- t = x (+ residual, rounded to bf16 and written to total where
  * that is given), y = t / sqrt(mean(t^2) + eps) * weight, for rows x [R][H] and

@@ -11,7 +11,8 @@
 //
 // fp32 in registers with one rounding at each output; every value is read once
 // and written once, 16 bytes a lane: HBM bounds the large sizes, the launch and
-// one trip to memory the small ones.
+// one trip to memory the small ones. A row of the norm whose sums leave fp32's range
+// is summed again in 64 bits, where every product of three bf16 has its place.
 #include "rows.hpp"
 
 namespace moe {
@@ -40,6 +41,29 @@ __device__ __forceinline__ float row_sum(float v, float *part) {
 #pragma unroll
     for (int i = 1; i < TPR / kWave; ++i) v += part[i];
     return v;
+}
+
+// The same in 64 bits.
+template <int TPR>
+__device__ __forceinline__ double row_sum64(double v, double *part) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    if (TPR == kWave) return v;
+    __syncthreads();
+    if (lane_id() == 0) part[threadIdx.x / kWave] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int i = 1; i < TPR / kWave; ++i) v += part[i];
+    return v;
+}
+
+// Whether a row's fp32 sum of squares, or the mean of them with eps, is not to be used:
+// past 2^120, or so small that squares below 2^-126 lost bits that count (a NaN too,
+// which stays one). The same in all threads of a row, whose sums have the same bits. No
+// ordinary row takes the branch, and its times are the same with it and without.
+__device__ __forceinline__ bool far_row(float squares, float mean) {
+    return !(squares < 0x1p120f && mean > 0x1p-90f);
 }
 
 struct NormArgs {
@@ -98,6 +122,7 @@ __device__ __forceinline__ void norm_out(const NormArgs &a, int r, int c, const 
 template <int TPR, int NV, int QUANT>
 __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormArgs a) {
     __shared__ float part[kNormThreads / kWave];
+    __shared__ double part64[kNormThreads / kWave];
     const long row = block_id() * (kNormThreads / TPR) + threadIdx.x / TPR;
     if (row >= a.R) return;                 // (whole wavefronts; whole workgroups where they meet)
     const int r = (int)row, t = threadIdx.x % TPR;
@@ -116,23 +141,43 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = fmaf(v[k][j], v[k][j], sum);
     }
-    const float inv = 1.0f / sqrtf(row_sum<TPR>(sum, part) / (float)a.H + a.eps);
+    const float squares = row_sum<TPR>(sum, part), mean = squares / (float)a.H + a.eps;
+    const float inv = 1.0f / sqrtf(mean);
+    const bool far = far_row(squares, mean);
     const uint16_t *const again = a.res && a.total ? a.total : a.x;
+    auto read_again = [&](int c, float u[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = 0.0f;
+        if (c >= a.H) return;
+        if (a.res && !a.total) norm_row<true>(a, at + c, u);
+        else unpack8(load16(again + at + c), u);
+    };
+    double inv64 = 0.0;
+    if (far) {
+        double sum64 = 0.0;
+        for (int i = 0; i < (NV ? NV : per); ++i) {
+            const int k = NV ? i : 0;
+            if (!NV) read_again(8 * (t + TPR * i), v[k]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum64 = fma((double)v[k][j], (double)v[k][j], sum64);
+        }
+        inv64 = 1.0 / sqrt(row_sum64<TPR>(sum64, part64) / a.H + (double)a.eps);
+    }
     for (int i = 0; i < (NV ? NV : per); ++i) {
         const int c = 8 * (t + TPR * i), k = NV ? i : 0;
         if (!NV) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
-            if (c < a.H) {
-                w[k] = load16(a.w + c);
-                unpack8(load16(again + at + c), v[k]);
-                if (a.res && !a.total) norm_row<true>(a, at + c, v[k]);
-            }
+            if (c < a.H) w[k] = load16(a.w + c);
+            read_again(c, v[k]);
         }
         float y[8];
         unpack8(w[k], y);
+        if (far) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = c < a.H ? v[k][j] * inv * y[j] : 0.0f;
+            for (int j = 0; j < 8; ++j) y[j] = c < a.H ? (float)((double)v[k][j] * inv64 * (double)y[j]) : 0.0f;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = c < a.H ? v[k][j] * inv * y[j] : 0.0f;
+        }
         norm_out<QUANT>(a, r, c, y);
     }
 }
@@ -155,6 +200,7 @@ template <int TPR, int NV>
 __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(NormGradArgs a) {
     constexpr int W = TPR / kWave;
     __shared__ float part[2][2][kNormThreads / kWave];
+    __shared__ double part64[kNormThreads / kWave];
     const int slot = blockIdx.x * (kNormThreads / TPR) + threadIdx.x / TPR, t = threadIdx.x % TPR;
     if (slot >= a.slots) return;
     struct Row {
@@ -210,11 +256,58 @@ __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(NormGradArgs a)
 #pragma unroll
             for (int i = 1; i < W; ++i) ss += part[turn][0][i], dot += part[turn][1][i];
         }
-        const float inv = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+        const float squares = ss / (float)a.H + a.eps, inv = 1.0f / sqrtf(squares);
         const float mean = dot * inv / (float)a.H;              // mean(g n)
+        if (far_row(ss, squares) || !(fabsf(mean) < 0x1p120f)) {
+            // the row once more from memory, its values read before dx may replace them (64-bit
+            // values of a whole row would take the registers of the rows under way)
+            const size_t at = (size_t)r * a.H;
+            double ss64 = 0.0, dot64 = 0.0;
+#pragma unroll 1
+            for (int c = 2 * t; c < a.H; c += 2 * TPR) {
+                const uint32_t xq = load_u32(a.x + at + c), gq = load_u32(a.dy + at + c), fq = load_u32(a.w + c);
+#pragma unroll
+                for (int j = 0; j < 32; j += 16) {
+                    const double x = bf16_bits_to_f32(xq >> j & 0xFFFFu), g = bf16_bits_to_f32(gq >> j & 0xFFFFu);
+                    ss64 = fma(x, x, ss64);
+                    dot64 = fma(g * (double)bf16_bits_to_f32(fq >> j & 0xFFFFu), x, dot64);
+                }
+            }
+            const double inv64 = 1.0 / sqrt(row_sum64<TPR>(ss64, part64) / a.H + (double)a.eps);
+            const double mean64 = row_sum64<TPR>(dot64, part64) * inv64 / a.H;
+            // n = x inv in two steps: inv itself may lie outside fp32's range
+            const int e = ilogb(inv64), half = e / 2;
+            const float s0 = ldexpf(1.0f, half), s1 = (float)ldexp(inv64, -half);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                asm volatile("" : "+v"(cur.x[i]), "+v"(cur.g[i]));
+                float x[8], g[8];
+                unpack8(cur.x[i], x), unpack8(cur.g[i], g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dw[i][j] = fmaf(g[j], x[j] * s0 * s1, dw[i][j]);
+            }
+#pragma unroll 1
+            for (int c = 2 * t; c < a.H; c += 2 * TPR) {
+                const uint32_t xq = load_u32(a.x + at + c), gq = load_u32(a.dy + at + c), fq = load_u32(a.w + c);
+                const uint32_t dq = a.dt ? load_u32(a.dt + at + c) : 0u;
+                float d[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const double x = bf16_bits_to_f32(xq >> 16 * j & 0xFFFFu), g = bf16_bits_to_f32(gq >> 16 * j & 0xFFFFu);
+                    const double f = bf16_bits_to_f32(fq >> 16 * j & 0xFFFFu), b = bf16_bits_to_f32(dq >> 16 * j & 0xFFFFu);
+                    d[j] = (float)(b + inv64 * (g * f - x * inv64 * mean64));
+                }
+                *(MOE_GLOBAL uint32_t *)(a.dx + at + c) = pack_bf16x2(d[0], d[1]);
+            }
+            cur = next;
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = 8 * (t + TPR * i);
+            // (unpacked once more: kept from the sums, past the branch, these values take 64
+            // registers more at 8192 columns, and spill at 16384)
+            asm volatile("" : "+v"(cur.x[i]), "+v"(cur.g[i]), "+v"(w[i]));
             float x[8], g[8], f[8], d[8];
             unpack8(cur.x[i], x), unpack8(cur.g[i], g), unpack8(w[i], f), unpack8(cur.t[i], d);
 #pragma unroll

@@ -9,8 +9,9 @@ tensors, allocates what it is not given, and enqueues on the current stream of t
 tensors' device or on ``stream``; nothing is computed by PyTorch, and nothing is
 recorded for autograd (inputs that require grad are refused where gradients are
 enabled; the gradients are calls of their own). Rows are bf16, contiguous, start at
-a multiple of 16 bytes and have a multiple of 8 columns; sums are fp32, and each
-output is rounded once.
+a multiple of 16 bytes and have a multiple of 8 columns; sums are fp32 (64 bits for a
+row of the norm or its gradient whose sums leave fp32's range), and each output is
+rounded once.
 
 A pair is (token t, one of its k experts j). ``pair_row`` (int32 [T, k], as
 ``moe_permute`` writes it) is the row that the pair has in sorted order; a pair
