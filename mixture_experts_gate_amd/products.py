@@ -299,6 +299,7 @@ def grouped_matmul_mxfp4(x, x_scale, w, w_scale=None, offsets=None, *, rows=None
     ``TableMatrices`` of packed "mxfp4" blobs -> [R, N] bf16 or fp32. N is a multiple
     of 16, K of 128."""
     dev = _matrix(x, "x", _U8).get_device()
+    _no_history(x_scale, w_scale)
     n, half = x.shape
     if isinstance(w, TableMatrices):
         pw, ps, tab, mat, E, N, K = _weights(w, w_scale, _U8, dev)
