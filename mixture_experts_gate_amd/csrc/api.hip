@@ -60,7 +60,7 @@ static const char *const g_kernel_names[K_COUNT] = {
     "cache_move", "micro_read", "micro_mfma", "scatter_rows", "layer_fused", "product",
     "product_fp8", "product_dx", "product_dw", "product_join", "gated", "gated_grad", "to_fp8",
     "to_mxfp4", "product_mxfp4", "norm", "norm_grad", "norm_join", "dispatch", "combine_rows",
-    "combine_rows_grad"};
+    "combine_rows_grad", "product_mxfp4_stream", "product_mxfp4_large"};
 
 static hipEvent_t pool_event() {
     if (!g_evpool.empty()) {

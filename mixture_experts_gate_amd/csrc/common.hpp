@@ -58,7 +58,8 @@ enum KernelId {
     K_DEC_GATE_UP, K_DEC_DOWN, K_PRE_GATE_UP, K_PRE_DOWN, K_COMBINE, K_CACHE_TABLE, K_PACK, K_ROUTE_PERMUTE, K_PRE_SPLIT,
     K_CACHE_MOVE, K_MICRO_READ, K_MICRO_MFMA, K_SCATTER, K_DEC_SMALL, K_PROD, K_PROD_FP8,
     K_PROD_DX, K_PROD_DW, K_PROD_JOIN, K_GATED, K_GATED_GRAD, K_TO_FP8,
-    K_TO_MXFP4, K_PROD_MXFP4, K_NORM, K_NORM_GRAD, K_NORM_JOIN, K_DISPATCH, K_COMBINE_ROWS, K_COMBINE_ROWS_GRAD, K_COUNT
+    K_TO_MXFP4, K_PROD_MXFP4, K_NORM, K_NORM_GRAD, K_NORM_JOIN, K_DISPATCH, K_COMBINE_ROWS, K_COMBINE_ROWS_GRAD,
+    K_PROD_MXFP4_STREAM, K_PROD_MXFP4_LARGE, K_COUNT
 };
 
 bool timing_enabled();

@@ -785,7 +785,7 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t *x_e2m1, const uint8_t *x_e8
     const int cu = compute_units();
     if (mxfp4_streams(R, N, E)) {
         const long tiles = (long)(R < E ? R : E + R / kVRows) * (N / 16), groups = (tiles + kVWaves - 1) / kVWaves;
-        MOE_LAUNCH(K_PROD_MXFP4, mxfp4_stream_kernel, dim3((unsigned)(groups < 4L * cu ? groups : 4L * cu)),
+        MOE_LAUNCH(K_PROD_MXFP4_STREAM, mxfp4_stream_kernel, dim3((unsigned)(groups < 4L * cu ? groups : 4L * cu)),
                    dim3(kVThreads), 0, s, m);
         return check_launch();
     }
@@ -794,8 +794,8 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t *x_e2m1, const uint8_t *x_e8
     if (!ws || ws_bytes < mxfp4_part_bytes(R, N, K, E)) a.slices = 1;
     if (mxfp4_large(a)) {
         const long tiles = tiles_of(R, N, E, kBT, kBT);
-        MOE_LAUNCH(K_PROD_MXFP4, mxfp4_large_kernel, dim3((unsigned)(tiles < cu ? tiles : cu)), dim3(kBThreads), 0, s,
-                   m);
+        MOE_LAUNCH(K_PROD_MXFP4_LARGE, mxfp4_large_kernel, dim3((unsigned)(tiles < cu ? tiles : cu)), dim3(kBThreads), 0,
+                   s, m);
         return check_launch();
     }
     const long tiles = tiles_of(R, N, E, kXP, kXQ) * a.slices;
