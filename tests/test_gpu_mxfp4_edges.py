@@ -1,11 +1,12 @@
 """The MXFP4 product at its edges: inputs that it refuses, which kernel a size takes,
-and scales at the ends of their range. Bounds are those of test_gpu_mxfp4.py."""
+scales at the ends of their range, and tensors past the widths of the kernels'
+offsets. Bounds are those of test_gpu_mxfp4.py."""
 import pytest
 import torch
 
 from mixture_experts_gate_amd import _lib, products as P
 
-from test_gpu_mxfp4 import PATHS, _bound, _case, _offsets, _ref, _within, decode, kernel_order
+from test_gpu_mxfp4 import PATHS, _bound, _case, _gen, _offsets, _ref, _within, decode, kernel_order
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -84,3 +85,92 @@ def test_scale_bytes_at_the_ends(path):
     y = _takes(path, lambda: P.grouped_matmul_mxfp4(x, xs, *kernel_order(wq, ws), _offsets(counts),
                                                     out=torch.empty(R, N, device=DEV)))
     _within(y, ref, _bound(ref, mag, K, torch.float32), "y")
+
+
+# ---------------------------------------------------------- far addresses --
+
+def _random(g, *shape):
+    return torch.randint(0, 256, shape, device=DEV, generator=g, dtype=torch.uint8)
+
+
+def _scales(g, *shape):
+    return (120 + torch.randint(-6, 7, shape, device=DEV, generator=g)).to(torch.uint8)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("path,R", [("stream", 9), ("tiles", 300), ("cut", 300)])
+def test_result_beyond_4_gib(path, R, dtype):
+    N, K, g = 64, 2176, _gen(40)
+    n = (1 << 32) // (N * dtype.itemsize) + 1000
+    x, xs, wq, ws = _random(g, R, K // 2), _scales(g, R, K // 32), _random(g, 1, N, K // 2), _scales(g, 1, N, K // 32)
+    to = (n - 1 - torch.randperm(900, generator=g, device=DEV)[:R]).to(torch.int32)
+    out = torch.full((n, N), 7.0, dtype=dtype, device=DEV)
+    space = torch.empty(16, dtype=torch.uint8, device=DEV) if path == "tiles" else None
+    _takes(path, lambda: P.grouped_matmul_mxfp4(x, xs, *kernel_order(wq, ws), out_rows=to, out=out, ws=space))
+    ref, mag = _ref(decode(x, xs), decode(wq, ws), [R], torch.arange(R, device=DEV))
+    _within(out[to.long()], ref, _bound(ref, mag, K, dtype), "y")
+    out[to.long()] = 7.0
+    assert bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("over", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_result_at_the_large_tiles_limit(dtype, over):
+    """2 GiB less 16 bytes of rows, the last of them written, N a part of a tile; a row
+    more goes to the smaller tiles. Some rows have no place."""
+    N, K, R, g = 2064, 768, 7424, _gen(41)
+    n = 0x7FFFFFF0 // (N * dtype.itemsize) + over
+    x, xs, wq, ws = _random(g, R, K // 2), _scales(g, R, K // 32), _random(g, 1, N, K // 2), _scales(g, 1, N, K // 32)
+    to = n - 1 - torch.randperm(8000, generator=g, device=DEV)[:R]
+    to[7], to[300], to[R - 1] = n - 1, -1, n
+    to[8:][to[8:] == n - 1] = 0
+    to = to.to(torch.int32)
+    out = torch.full((n, N), 7.0, dtype=dtype, device=DEV)
+    _takes("tiles" if over else "large",
+           lambda: P.grouped_matmul_mxfp4(x, xs, *kernel_order(wq, ws), out_rows=to, out=out))
+    ref, mag = _ref(decode(x, xs), decode(wq, ws), [R], torch.arange(R, device=DEV))
+    live = (to >= 0) & (to < n)
+    _within(out[to[live].long()], ref[live], _bound(ref, mag, K, dtype)[live], "y")
+    out[to[live].long()] = 7.0
+    assert bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("over", [False, True])
+def test_rows_at_the_large_tiles_limit(over):
+    """Just under 4 GiB of x, its last rows read; two rows more go to the smaller tiles."""
+    N, K, R, g = 2064, 1024, 7424, _gen(42)
+    n = 0xFFFFFFFF // (K // 2) + 2 * over
+    x, xs = torch.zeros(n, K // 2, dtype=torch.uint8, device=DEV), torch.full((n, K // 32), 127, dtype=torch.uint8, device=DEV)
+    for part in (slice(0, 300), slice(n - 300, n)):
+        x[part], xs[part] = _random(g, 300, K // 2), _scales(g, 300, K // 32)
+    wq, ws = _random(g, 1, N, K // 2), _scales(g, 1, N, K // 32)
+    pick = torch.randint(-300, 300, (R,), generator=g, device=DEV)
+    pick[0], pick[R - 1] = -1, -300
+    rows = torch.where(pick < 0, n + pick, pick).to(torch.int32)
+    y = _takes("tiles" if over else "large", lambda: P.grouped_matmul_mxfp4(x, xs, *kernel_order(wq, ws), rows=rows))
+    xd = torch.cat([decode(x[:300], xs[:300]), decode(x[-300:], xs[-300:])])
+    ref, mag = _ref(xd, decode(wq, ws), [R], torch.where(pick < 0, 600 + pick, pick))
+    _within(y, ref, _bound(ref, mag, K, torch.bfloat16), "y")
+
+
+@pytest.mark.parametrize("path,K,counts", [("stream", 16384, (1, 2, 3)), ("tiles", 16512, (60, 1, 150)),
+                                           ("large", 16384, (60, 1, 150))])
+def test_matrices_beyond_4_gib(path, K, counts):
+    """270 experts of 16 MiB, of which the first and the last two have rows."""
+    E, N, g = 270, 2048, _gen(43)
+    live, R = (0, E - 2, E - 1), sum(counts)
+    kq, ks = torch.zeros(E, N, K // 2, dtype=torch.uint8, device=DEV), torch.full((E, N, K // 32), 127, dtype=torch.uint8, device=DEV)
+    wq, ws = _random(g, 3, N, K // 2), _scales(g, 3, N, K // 32)
+    for i, e in enumerate(live):
+        a, b = kernel_order(wq[i:i + 1], ws[i:i + 1])
+        kq[e], ks[e] = a[0], b[0]
+    assert kq[E - 1].data_ptr() - kq.data_ptr() > 1 << 32
+    x, xs = _random(g, R, K // 2), _scales(g, R, K // 32)
+    every = [0] * E
+    for i, e in enumerate(live):
+        every[e] = counts[i]
+    y = _takes(path, lambda: P.grouped_matmul_mxfp4(x, xs, kq, ks, _offsets(every), out=torch.empty(R, N, device=DEV)))
+    xd = decode(x, xs)
+    for cols in (slice(0, 80), slice(N - 80, N)):
+        ref, mag = _ref(xd, decode(wq[:, cols].contiguous(), ws[:, cols].contiguous()), counts, torch.arange(R, device=DEV))
+        _within(y[:, cols], ref, _bound(ref, mag, K, torch.float32), "y")
