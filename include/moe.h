@@ -631,8 +631,9 @@ int moe_combine_rows(const void *y, int y_is_fp32, int y_n, const int32_t *pair_
 
 /* moe_combine_rows_grad -- its gradients for dout [T][H] bf16: dy[pair_row[p]] =
  * w[p] dout[t] (optional, bf16 [y_n][H]; rows of no pair are left as they are, rows
- * are distinct) and dw[p] = <dout[t], y[pair_row[p]]> (optional, fp32 [T*k], of y
- * bf16; 0 for a pair whose row is outside y). add's gradient is dout. */
+ * are distinct; w optional, 1 without) and dw[p] = <dout[t], y[pair_row[p]]>
+ * (optional, fp32 [T*k], of y bf16, which is read for dw alone; 0 for a pair whose
+ * row is outside y). add's gradient is dout. */
 int moe_combine_rows_grad(const uint16_t *dout_bf16, const uint16_t *y_bf16, int y_n,
                           const int32_t *pair_row, const float *w, int T, int k, int H,
                           uint16_t *dy_bf16, float *dw, void *stream);
