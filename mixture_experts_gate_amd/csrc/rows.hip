@@ -60,8 +60,7 @@ __device__ __forceinline__ double row_sum64(double v, double *part) {
 
 // Whether a row's fp32 sum of squares, or the mean of them with eps, is not to be used:
 // past 2^120, or so small that squares below 2^-126 lost bits that count (a NaN too,
-// which stays one). The same in all threads of a row, whose sums have the same bits. No
-// ordinary row takes the branch, and its times are the same with it and without.
+// which stays one). The same in all threads of a row, whose sums have the same bits.
 __device__ __forceinline__ bool far_row(float squares, float mean) {
     return !(squares < 0x1p120f && mean > 0x1p-90f);
 }
@@ -144,24 +143,37 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormArgs a) {
     const float squares = row_sum<TPR>(sum, part), mean = squares / (float)a.H + a.eps;
     const float inv = 1.0f / sqrtf(mean);
     const bool far = far_row(squares, mean);
-    const uint16_t *const again = a.res && a.total ? a.total : a.x;
+    // columns c .. c + 7 of t again: from total, where they were rounded, or the inputs
     auto read_again = [&](int c, float u[8]) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = 0.0f;
         if (c >= a.H) return;
         if (a.res && !a.total) norm_row<true>(a, at + c, u);
-        else unpack8(load16(again + at + c), u);
+        else unpack8(load16((a.res ? a.total : a.x) + at + c), u);
     };
-    double inv64 = 0.0;
     if (far) {
+        // (read again, a vector at a time: from registers this code would take up to 40 more
+        // of them than an ordinary row does, and 4096 x 8192 to MXFP4 42.8 us instead of 38.7)
         double sum64 = 0.0;
-        for (int i = 0; i < (NV ? NV : per); ++i) {
-            const int k = NV ? i : 0;
-            if (!NV) read_again(8 * (t + TPR * i), v[k]);
+#pragma unroll 1
+        for (int c = 8 * t; c < a.H; c += 8 * TPR) {
+            float u[8];
+            read_again(c, u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum64 = fma((double)v[k][j], (double)v[k][j], sum64);
+            for (int j = 0; j < 8; ++j) sum64 = fma((double)u[j], (double)u[j], sum64);
         }
-        inv64 = 1.0 / sqrt(row_sum64<TPR>(sum64, part64) / a.H + (double)a.eps);
+        const double inv64 = 1.0 / sqrt(row_sum64<TPR>(sum64, part64) / a.H + (double)a.eps);
+#pragma unroll 1
+        for (int i = 0; i < per; ++i) {          // (all lanes of a block of codes together)
+            const int c = 8 * (t + TPR * i);
+            float u[8], y[8];
+            read_again(c, u);
+            unpack8(c < a.H ? load16(a.w + c) : u32x4{0, 0, 0, 0}, y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = c < a.H ? (float)((double)u[j] * inv64 * (double)y[j]) : 0.0f;
+            norm_out<QUANT>(a, r, c, y);
+        }
+        return;
     }
     for (int i = 0; i < (NV ? NV : per); ++i) {
         const int c = 8 * (t + TPR * i), k = NV ? i : 0;
@@ -171,13 +183,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormArgs a) {
         }
         float y[8];
         unpack8(w[k], y);
-        if (far) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = c < a.H ? (float)((double)v[k][j] * inv64 * (double)y[j]) : 0.0f;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = c < a.H ? v[k][j] * inv * y[j] : 0.0f;
-        }
+        for (int j = 0; j < 8; ++j) y[j] = c < a.H ? v[k][j] * inv * y[j] : 0.0f;
         norm_out<QUANT>(a, r, c, y);
     }
 }
@@ -190,6 +197,42 @@ struct NormGradArgs {
     float *part;              // [slots][H], or NULL
     int slots;
 };
+
+// Row r of the gradient in 64 bits: dx, and its part of dw. (A thread reads its columns
+// before it writes them: dx may be dy's or dtotal's rows.)
+template <int TPR, int NV>
+__device__ __forceinline__ void far_grad(const NormGradArgs &a, long r, int t, float (&dw)[NV][8], double *part) {
+    const uint16_t *const x = a.x + (size_t)r * a.H, *const g = a.dy + (size_t)r * a.H;
+    double ss = 0.0, dot = 0.0;
+#pragma unroll 1
+    for (int c = 8 * t; c < a.H; c += 8 * TPR) {
+        float u[8], v[8], f[8];
+        unpack8(load16(x + c), u), unpack8(load16(g + c), v), unpack8(load16(a.w + c), f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            ss = fma((double)u[j], (double)u[j], ss);
+            dot = fma((double)v[j] * f[j], (double)u[j], dot);
+        }
+    }
+    const double inv = 1.0 / sqrt(row_sum64<TPR>(ss, part) / a.H + (double)a.eps);
+    const double mean = row_sum64<TPR>(dot, part) * inv / a.H;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        asm volatile("" ::: "memory");          // (one vector after the other: few registers)
+        const int c = 8 * (t + TPR * i);
+        if (c >= a.H) continue;
+        float u[8], v[8], f[8], d[8];
+        unpack8(load16(x + c), u), unpack8(load16(g + c), v), unpack8(load16(a.w + c), f);
+        unpack8(a.dt ? load16(a.dt + (size_t)r * a.H + c) : u32x4{0, 0, 0, 0}, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const double n = u[j] * inv;
+            dw[i][j] = fmaf(v[j], (float)n, dw[i][j]);
+            d[j] = (float)(d[j] + inv * ((double)v[j] * f[j] - n * mean));
+        }
+        store_nt(a.dx + (size_t)r * a.H + c, pack8(d));
+    }
+}
 
 // Slot s takes the rows s, s + slots, ...: TPR threads, whose part of dw stays in
 // registers over the rows and goes to row s of `part`, which norm_join adds up (no
@@ -229,96 +272,68 @@ __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(NormGradArgs a)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
     }
-    Row cur, next;
-    load(slot, cur);
     int turn = 0;
-    for (long r = slot; r < a.R; r += a.slots, turn ^= 1) {
-        load(r + a.slots, next);
-        float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float x[8], g[8], f[8];
-            unpack8(cur.x[i], x), unpack8(cur.g[i], g), unpack8(w[i], f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                ss = fmaf(x[j], x[j], ss);
-                dot = fmaf(g[j] * f[j], x[j], dot);
-            }
-        }
-#pragma unroll
-        for (int d = 32; d; d >>= 1) ss += __shfl_xor(ss, d), dot += __shfl_xor(dot, d);
-        if (W > 1) {
-            // (two places in turn: a barrier a row)
-            if (lane_id() == 0) part[turn][0][threadIdx.x / kWave] = ss, part[turn][1][threadIdx.x / kWave] = dot;
-            wait_lds();
-            bare_barrier();             // (one that leaves the loads in flight)
-            ss = part[turn][0][0], dot = part[turn][1][0];
-#pragma unroll
-            for (int i = 1; i < W; ++i) ss += part[turn][0][i], dot += part[turn][1][i];
-        }
-        const float squares = ss / (float)a.H + a.eps, inv = 1.0f / sqrtf(squares);
-        const float mean = dot * inv / (float)a.H;              // mean(g n)
-        if (far_row(ss, squares) || !(fabsf(mean) < 0x1p120f)) {
-            // the row once more from memory, its values read before dx may replace them (64-bit
-            // values of a whole row would take the registers of the rows under way)
-            const size_t at = (size_t)r * a.H;
-            double ss64 = 0.0, dot64 = 0.0;
-#pragma unroll 1
-            for (int c = 2 * t; c < a.H; c += 2 * TPR) {
-                const uint32_t xq = load_u32(a.x + at + c), gq = load_u32(a.dy + at + c), fq = load_u32(a.w + c);
-#pragma unroll
-                for (int j = 0; j < 32; j += 16) {
-                    const double x = bf16_bits_to_f32(xq >> j & 0xFFFFu), g = bf16_bits_to_f32(gq >> j & 0xFFFFu);
-                    ss64 = fma(x, x, ss64);
-                    dot64 = fma(g * (double)bf16_bits_to_f32(fq >> j & 0xFFFFu), x, dot64);
-                }
-            }
-            const double inv64 = 1.0 / sqrt(row_sum64<TPR>(ss64, part64) / a.H + (double)a.eps);
-            const double mean64 = row_sum64<TPR>(dot64, part64) * inv64 / a.H;
-            // n = x inv in two steps: inv itself may lie outside fp32's range
-            const int e = ilogb(inv64), half = e / 2;
-            const float s0 = ldexpf(1.0f, half), s1 = (float)ldexp(inv64, -half);
+    // Rows in turns of 2048. Row n of a turn that is far (its dx is not stored, nor its
+    // part of dw added) has bit n / 64 of lane n % 64's mask, which every wavefront of the
+    // row holds, and follows at the turn's end: 64-bit code inside the loop would take
+    // registers and time from every row (8192 x 2048 25.3 -> 32 us).
+    for (long first = slot; first < a.R; first += 2048L * a.slots) {
+        Row cur, next;
+        load(first, cur);
+        // (here, lest the compiler wait for it inside the loop, and so for `next` too)
+        __builtin_amdgcn_s_waitcnt(0x0F70);         // vmcnt(0)
+        uint32_t far = 0;
+        int row = 0;
+        for (long r = first; r < a.R && row < 2048; r += a.slots, turn ^= 1, ++row) {
+            load(r + a.slots, next);
+            float ss = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                asm volatile("" : "+v"(cur.x[i]), "+v"(cur.g[i]));
-                float x[8], g[8];
-                unpack8(cur.x[i], x), unpack8(cur.g[i], g);
+                float x[8], g[8], f[8];
+                unpack8(cur.x[i], x), unpack8(cur.g[i], g), unpack8(w[i], f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) dw[i][j] = fmaf(g[j], x[j] * s0 * s1, dw[i][j]);
-            }
-#pragma unroll 1
-            for (int c = 2 * t; c < a.H; c += 2 * TPR) {
-                const uint32_t xq = load_u32(a.x + at + c), gq = load_u32(a.dy + at + c), fq = load_u32(a.w + c);
-                const uint32_t dq = a.dt ? load_u32(a.dt + at + c) : 0u;
-                float d[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const double x = bf16_bits_to_f32(xq >> 16 * j & 0xFFFFu), g = bf16_bits_to_f32(gq >> 16 * j & 0xFFFFu);
-                    const double f = bf16_bits_to_f32(fq >> 16 * j & 0xFFFFu), b = bf16_bits_to_f32(dq >> 16 * j & 0xFFFFu);
-                    d[j] = (float)(b + inv64 * (g * f - x * inv64 * mean64));
+                for (int j = 0; j < 8; ++j) {
+                    ss = fmaf(x[j], x[j], ss);
+                    dot = fmaf(g[j] * f[j], x[j], dot);
                 }
-                *(MOE_GLOBAL uint32_t *)(a.dx + at + c) = pack_bf16x2(d[0], d[1]);
+            }
+#pragma unroll
+            for (int d = 32; d; d >>= 1) ss += __shfl_xor(ss, d), dot += __shfl_xor(dot, d);
+            if (W > 1) {
+                // (two places in turn: a barrier a row)
+                if (lane_id() == 0)
+                    part[turn][0][threadIdx.x / kWave] = ss, part[turn][1][threadIdx.x / kWave] = dot;
+                wait_lds();
+                bare_barrier();             // (one that leaves the loads in flight)
+                ss = part[turn][0][0], dot = part[turn][1][0];
+#pragma unroll
+                for (int i = 1; i < W; ++i) ss += part[turn][0][i], dot += part[turn][1][i];
+            }
+            const float squares = ss / (float)a.H + a.eps, inv = 1.0f / sqrtf(squares);
+            const float mean = dot * inv / (float)a.H;              // mean(g n)
+            const bool is_far = far_row(ss, squares) || !(fabsf(mean) < 0x1p120f);
+            far |= is_far && lane_id() == (row & 63) ? 1u << (row >> 6) : 0u;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = 8 * (t + TPR * i);
+                // (unpacked once more: there are not registers for all values of 16384 columns)
+                if (NV > 4) asm volatile("" : "+v"(w[i]));
+                float x[8], g[8], f[8], d[8];
+                unpack8(cur.x[i], x), unpack8(cur.g[i], g), unpack8(w[i], f), unpack8(cur.t[i], d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float n = x[j] * inv;
+                    dw[i][j] = is_far ? dw[i][j] : fmaf(g[j], n, dw[i][j]);
+                    d[j] += inv * (g[j] * f[j] - n * mean);
+                }
+                if (c < a.H && !is_far) store_nt(a.dx + (size_t)r * a.H + c, pack8(d));
             }
             cur = next;
-            continue;
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = 8 * (t + TPR * i);
-            // (unpacked once more: kept from the sums, past the branch, these values take 64
-            // registers more at 8192 columns, and spill at 16384)
-            asm volatile("" : "+v"(cur.x[i]), "+v"(cur.g[i]), "+v"(w[i]));
-            float x[8], g[8], f[8], d[8];
-            unpack8(cur.x[i], x), unpack8(cur.g[i], g), unpack8(w[i], f), unpack8(cur.t[i], d);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float n = x[j] * inv;
-                dw[i][j] = fmaf(g[j], n, dw[i][j]);
-                d[j] += inv * (g[j] * f[j] - n * mean);
-            }
-            if (c < a.H) store_nt(a.dx + (size_t)r * a.H + c, pack8(d));
-        }
-        cur = next;
+        if (!__ballot(far != 0)) continue;
+        for (int b = 0; b < 32; ++b)
+            for (unsigned long long m = __ballot(far >> b & 1); m; m &= m - 1)
+                far_grad<TPR, NV>(a, first + (64L * b + __ffsll(m) - 1) * a.slots, t, dw, part64);
     }
     if (!a.part) return;
 #pragma unroll

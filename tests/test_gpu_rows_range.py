@@ -154,3 +154,25 @@ def test_far_rows_in_a_graph_give_the_calls_bits():
         torch.cuda.synchronize()
         assert torch.equal(y, want_y) and torch.equal(t, want_t)
         assert torch.equal(dx, want_dx) and torch.equal(dw, want_dw)
+
+
+@pytest.mark.parametrize("R,H", [((1 << 23) + 70, 8), ((1 << 20) + 600, 1032)])
+def test_far_rows_among_many(R, H):
+    """Two thousand and more rows a slot: far rows at the first and last places of the
+    kernel's turns of 2048, and neighbours of ordinary ones. (The other rows add zeros.)"""
+    g = _gen(R)
+    slots = (8 if H <= 1024 else 2) * torch.cuda.get_device_properties(0).multi_processor_count
+    assert R > 2048 * slots
+    at = [0, 1, slots - 1, 63 * slots, 64 * slots + 3, 65 * slots + 3, 2047 * slots + 5, 2048 * slots, 2048 * slots + 7, R - 1]
+    far = [0, 5, 1, 8, 2, 3, 10, 4, 6, 7]
+    x, dy = (torch.zeros(R, H, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    x[:] = 1.0
+    xs, ds = (_rows(g, [GRAD_SIZES[i][j] for i in far], H) for j in (0, 1))
+    x[at], dy[at] = xs, ds
+    w = _randn(g, H)
+    ref, refw, b, bw = _grad_ref(xs, w, ds, None, 0.0)
+    dx, dw = W.rms_norm_grad(x, w, dy, 0.0, dx=dy)
+    _within(dx[at], ref, b + (ref.abs() + b) * BF16, "dx")
+    _within(dw, refw, bw, "dw")
+    dx[at] = 0
+    assert not bool(dx.any())
