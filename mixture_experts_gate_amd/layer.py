@@ -529,7 +529,11 @@ class Mxfp4Layer(_CodedLayer):
     __doc__ = """Experts that are MXFP4 matrices in the kernel layout (packed blobs of
     ``blob_layout(H, I, "mxfp4")``, as ``MoeLayer`` reads them), their inputs MXFP4 too:
     four bits on both sides of the products, where ``MoeLayer`` holds the activations to
-    bf16's precision or near it. H and I are multiples of 128.
+    bf16's precision or near it. H and I are multiples of 128. It is made for prompts: of
+    256 experts (H 4096, I 2048, 6 a token) 4096 tokens take 835 us, 512 tokens 612,
+    ``MoeLayer``'s 1345 and 677. Below about 256 tokens ``MoeLayer`` on the same blobs is
+    the faster layer as well as the more precise one (one token 28 us, 41 here; 64 tokens
+    428 and 487; 256 tokens 581 and 593).
 
     """ + _CodedLayer.__doc__
 
