@@ -231,7 +231,9 @@ __global__ __launch_bounds__(kXThreads, 4) void mxfp4_tile_kernel(MxArgs X) {
 // (12 thousand of 62: offsets, indices and rows one after another); gate/up of 8192
 // tokens of 128 experts (1536 x 2048, 412 GFLOP, 201 MB of results) 2.6 at 1.8 GHz,
 // where 40 of 160 us go by while the compute units store together. A slab takes 1500
-// cycles of which 1024 multiply.
+// cycles of which 1024 multiply: a phase's 512 take about 700 with the copies between
+// them, its barriers 120. (LDS is busy for 490 of them: 96 KB of fragments, which it
+// gives out at 240 bytes a cycle, and their conflicts.)
 //
 // LDS holds four slabs, two pairs. The copies run three slabs ahead, and on into the
 // next tile, whose rows are looked up during this one's first slabs: only a workgroup's
@@ -290,10 +292,10 @@ __global__ __launch_bounds__(kBThreads) void mxfp4_large_kernel(MxArgs X) {
     int si = t0 + ((int)blockIdx.x >> lx);
     if (si >= t1) return;
 
-    // The workgroups that have a tile less than others start later, by up to the time
-    // of one (about 1000 cycles a slab): begun together, all tiles end together, and
-    // each end's stores, 32 MB from the device, wait for HBM with nothing to multiply
-    // (gate/up of 8192 tokens: 185 -> 171 us).
+    // The workgroups that have a tile less than others start later, by up to half of
+    // one's time (12 sleeps of 64 cycles a slab, which takes 1500): begun together, all
+    // tiles end together, and each end's stores, 32 MB from the device, wait for HBM with
+    // nothing to multiply (gate/up of 8192 tokens: 185 -> 171 us).
     const int rank = blockIdx.x >> lx, late = (t1 - t0) % per;
     if (late > 0 && rank >= late)
         for (int i = slabs * 12 * (rank - late) / (per - late); i > 0; --i) __builtin_amdgcn_s_sleep(1);
@@ -721,11 +723,14 @@ static long tiles_of(int R, int N, int E, int p, int q) {
 //     -/47.8/46.2  -/58/54  -/112/99  -/194/160
 //   256 experts of 4096 x 4096, 6 a token: 1, 2, 8, 32, 256 tokens
 //     16.0/18.5/20.1  25.2/22.5/23.2  75/75/72  -/188/184  -/334/327
-//   one of 4096 x 4096: 1, 16, 64, 512, 1024, 4001 rows; one of 8192 x 8192, 8192 rows
-//     8.7/12.2/18.2  10.1/13.0/18.3  20.1/15.0/19.0  -/27.3/30.0  -/27.2/30.4  -/50/42
-//     -/346/257
+//   one of 4096 x 4096: 1, 16, 64, 512, 1024, 1536, 2048, 3000, 3800, 4001 rows
+//     8.7/12.2/18.2  10.1/13.0/18.3  20.1/15.0/19.0  -/27.8/30.7  -/27.0/30.6  -/27.8/30.7
+//     -/29.3/30.8  -/41.5/33.3  -/46.2/37.9  -/47.6/39.6
+//   one of 8192 x 8192, 8192 rows -/346/257
 // The streaming kernel, which needs no second launch for a sum in parts, wins with few
-// tiles; large ones win where rows fill them or the tiles are many.
+// tiles; large ones win where rows fill them or the tiles are many. (With one expert
+// they win from where the smaller tiles are more than the compute units, 2100 rows of
+// the one above, which takes them from 3840 on: 8 us late in between.)
 static bool mxfp4_streams(int R, int N, int E) {
     return R <= (long)kVAvg * E && tiles_of(R, N, E, kBT, kBT) <= 128;
 }
@@ -738,9 +743,9 @@ static bool mxfp4_large(const ProductArgs &a) {
 }
 
 // Parts that the sum of a tile is cut into: where there are fewer tiles than compute
-// units, as many as give each one, of eight slabs at least. (4, 8, 16, with wavefronts of
-// 64 x 128: 64 rows of one expert of 4096 x 4096 16.4, 14.9, 17.4 us, 128 rows 23.8,
-// 20.7, 22.4, 512 rows 28.1, 27.9, 31.4, 500 of 1536 x 2048 19.5, 18.2, 18.0.)
+// units, as many as give each one, of eight slabs at least. (4, 8, 16: 64 rows of one
+// expert of 4096 x 4096 16.8, 15.0, 17.4 us, 128 rows 22.9, 19.1, 20.1, 256 rows 25.7,
+// 24.9, 23.4, 512 rows 28.3, 28.3, 29.4, 500 of 1536 x 2048 17.7, 16.3, 15.8.)
 static int mxfp4_slices(int R, int N, int K, int E) {
     if (R == 0 || mxfp4_streams(R, N, E)) return 1;
     const long tiles = tiles_of(R, N, E, kXP, kXQ);

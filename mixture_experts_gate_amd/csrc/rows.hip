@@ -237,8 +237,9 @@ __device__ __forceinline__ void far_grad(const NormGradArgs &a, long r, int t, f
 // Slot s takes the rows s, s + slots, ...: TPR threads, whose part of dw stays in
 // registers over the rows and goes to row s of `part`, which norm_join adds up (no
 // atomics: the order is fixed). The next row is on its way while this one's two sums
-// meet. HBM bounds it: 8192 x 4096 with dtotal 46 us (268 MB, 5.8 TB/s), and 4 for the
-// join; 301 x 2048 5 us, a row a workgroup, and 4.
+// meet. HBM bounds it: 8192 x 4096 with dtotal 46 us (268 MB, 5.8 TB/s), and 5 for the
+// join; 4096 x 8192 53 and 5, 2048 x 16384 59 and 7, where the parts of dw are 17 and 34
+// MB more; 301 x 2048 5 us, a row a workgroup, and 4.
 template <int TPR, int NV>
 __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(NormGradArgs a) {
     constexpr int W = TPR / kWave;
@@ -526,8 +527,11 @@ static void launch_norm(const NormArgs &a, hipStream_t s) {
 constexpr int kMaxGradH = 16384;     // columns whose dw stays in the registers of 256 threads
 
 // Two workgroups a compute unit, eight wavefronts. (The parts of dw are written and
-// read again: with 1, 2, 4 of them the gradient of 8192 x 4096 takes 53, 50.6, 58 us,
-// of 32768 x 512 37, 31.5, 38 us.)
+// read again: with 1, 2, 4 workgroups the gradient of 8192 x 4096 takes 52, 50, 54 us
+// with the join, of 32768 x 512 36, 30, 35.) Past 4096 columns a wavefront holds more
+// than half of a SIMD's registers, so that the second workgroup of a compute unit
+// follows the first: with 1, 2, 4 of them 4096 x 8192 takes 51, 55, 64 us, 16384 x 8192
+// 173, 177, 184, 2048 x 16384 57, 65, 83, 600 x 16384 28, 34, 41.
 static int grad_slots(int R, int H) {
     const int most = (H <= 1024 ? 8 : 2) * compute_units();
     return R < most ? R : most;
